@@ -18,10 +18,16 @@ Forms (see the header for the exact contracts):
   dsa_masked_mha_prefill_strided  the same on strided views, RoPE key columns shared
   dsa_choose_form         predicted time of each form and the fastest (host only)
   dsa_kv_fp8_quantize / dsa_kv_fp8_dequantize  FP8 latent rows of the KV cache
+
+The decode step over the same paged cache:
+  dsa_rope                rotary positions and their gradient (frequencies from dsa_rope_freqs)
+  dsa_kv_append           new tokens' latent rows into the cache, bf16 or FP8, RoPE columns rotated
+  dsa_paged_decode        attention of one new token per request, whole context or its top-k positions
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -44,6 +50,7 @@ _lib_handle = None
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _L = ctypes.c_int64
 
@@ -67,6 +74,15 @@ class FormQuery(ctypes.Structure):
 class FormEstimate(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * 3), ("form", ctypes.c_int), ("union_rows", ctypes.c_double)]
 
+
+class RopeFreqs(ctypes.Structure):
+    """Rotary frequencies (dsa_rope_freqs); read-only once made."""
+    _fields_ = [("d_rope", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
+
+
+ROPE_LAYOUTS = ("interleaved", "half")
+ROPE_SCALINGS = ("none", "linear", "yarn")
 
 _SIGNATURES = {
     "dsa_status_string": (ctypes.c_char_p, [_I]),
@@ -93,6 +109,13 @@ _SIGNATURES = {
     "dsa_kv_fp8_quantize": (_I, [_VP, _I, _I, _I, _VP, _VP]),
     "dsa_kv_fp8_dequantize": (_I, [_VP, _I, _I, _VP, _I, _VP]),
     "dsa_sparse_prefill_fp8": (_I, [_VP, _VP, _I, _I, _VP, _I, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP]),
+    "dsa_rope_freqs_init": (_I, [ctypes.POINTER(RopeFreqs), _I, _D, _I, _I, _D, _I, _D, _D, _F]),
+    "dsa_rope": (_I, [_VP, _L, _L, _VP, _L, _L, _I, _VP, _I, _I, ctypes.POINTER(RopeFreqs), _I, _VP]),
+    "dsa_kv_append": (_I, [_VP, _L, _VP, _L, _I, _I, _VP, _VP, _VP, _I, _I, _I, ctypes.POINTER(RopeFreqs), _VP, _I, _I,
+                           _I, _VP]),
+    "dsa_paged_decode_workspace": (_L, [_I, _I]),
+    "dsa_paged_decode": (_I, [_VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP,
+                              _L, _VP]),
     "dsa_form_calibration_default": (_I, [ctypes.POINTER(FormCalibration)]),
     "dsa_choose_form": (_I, [ctypes.POINTER(FormQuery), ctypes.POINTER(FormCalibration),
                              ctypes.POINTER(FormEstimate)]),
@@ -549,4 +572,206 @@ def dsa_sparse_prefill_fp8(q, kv_fp8, idx, k: int, scale: float, d_rope: int = 6
     _check(lib().dsa_sparse_prefill_fp8(q.data_ptr(), kv_fp8.data_ptr(), N, int(d_rope), idx.data_ptr(), T, H, d_qk,
                                         d_v, k, idx.shape[1], float(scale), out.data_ptr(), lse.data_ptr(),
                                         _stream(stream, q.device)), "dsa_sparse_prefill_fp8")
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# the decode step
+# ---------------------------------------------------------------------------
+def _on_device(t, fn, stream):
+    """Calls fn(stream handle) with t's device current.  A library call works on
+    the current device, so a tensor of another one needs it switched."""
+    import torch
+    index = t.device.index
+    if index == torch.cuda.current_device():
+        return fn(_raw_stream(stream, index))
+    with torch.cuda.device(index):
+        return fn(_raw_stream(stream, index))
+
+
+def _raw_stream(stream, index):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _made_for(stream, *tensors):
+    """Tensors made here on the current stream and used on another one: their
+    memory must not be handed out again before that stream is done."""
+    if stream is not None:
+        import torch
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        cur = torch.cuda.current_stream(tensors[0].device)
+        if s.cuda_stream != cur.cuda_stream:
+            for t in tensors:
+                t.record_stream(s)
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+@functools.lru_cache(maxsize=64)
+def dsa_rope_freqs(d_rope: int, base: float = 10000.0, layout: str = "interleaved", scaling: str = "none",
+                   factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                   mscale: float = 1.0) -> RopeFreqs:
+    """Rotary frequencies for dsa_rope and dsa_kv_append (host only): pairs of ``layout``
+    "interleaved" (2i, 2i+1) or "half" (i, i + d_rope/2), frequencies base^(-2i/d_rope),
+    ``scaling`` "none", "linear" (divided by factor) or "yarn" (fast pairs kept, slow ones
+    divided, mixed between beta_fast and beta_slow turns over original_len positions); mscale
+    multiplies cos and sin.  The table depends on these numbers alone (and is kept by them)."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {ROPE_LAYOUTS}")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
+    f = RopeFreqs()
+    _check(lib().dsa_rope_freqs_init(ctypes.byref(f), int(d_rope), float(base), ROPE_LAYOUTS.index(layout),
+                                     ROPE_SCALINGS.index(scaling), float(factor), int(original_len), float(beta_fast),
+                                     float(beta_slow), float(mscale)), "dsa_rope_freqs_init")
+    return f
+
+
+def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, stream=None):
+    """Rotary positions on x [T, H, d_rope] (bf16 or fp32, any strides with unit last stride: the
+    RoPE columns of a wider head are passed as that view), positions [T] int32.  ``out``: a tensor
+    or view of the same shape and dtype, x itself for in place; a new contiguous one if None.
+    gradient=True turns back: the gradient of the forward with respect to x, given the gradient
+    of its result.  Returns out."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a bf16 or fp32 tensor")
+    if not x.is_cuda or x.dim() != 3 or x.stride(2) != 1:
+        raise ValueError("x must be a 3-D CUDA tensor with unit stride in its last dimension")
+    if not isinstance(freqs, RopeFreqs):
+        raise TypeError("freqs must come from dsa_rope_freqs")
+    _need(positions, torch.int32, "positions", 1)
+    T, H, d = x.shape
+    if d != freqs.d_rope:
+        raise ValueError(f"x has {d} columns, the frequencies {freqs.d_rope}")
+    if positions.shape[0] != T:
+        raise ValueError("positions must have one entry per token")
+    if out is None:
+        out = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
+        _made_for(stream, out)
+    elif out.dtype != x.dtype or out.shape != x.shape or (d > 1 and out.stride(2) != 1):
+        raise ValueError("out must have x's shape and dtype and unit stride in its last dimension")
+    _same_device(x, positions=positions, out=out)
+    xs, ys = x.stride(), out.stride()
+    _check(_on_device(x, lambda s: lib().dsa_rope(
+        x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], 1 if x.dtype == torch.float32 else 0,
+        positions.data_ptr(), T, H, ctypes.byref(freqs), 1 if gradient else 0, s), stream), "dsa_rope")
+    return out
+
+
+def _cache_of(cache, d_rope):
+    """(format, rows, ld) of a bf16 or FP8 cache tensor."""
+    import torch
+    if isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8:
+        _need(cache, torch.uint8, "cache", 2)
+        if cache.shape[1] != dsa_kv_fp8_row_bytes(d_rope):
+            raise ValueError("FP8 cache rows must be dsa_kv_fp8_row_bytes(d_rope) bytes")
+        return 1, cache.shape[0], 0
+    _need(cache, torch.bfloat16, "cache", 2)
+    return 0, cache.shape[0], cache.shape[1]
+
+
+def dsa_kv_append(c_kv, k_pe, positions, block_table, block_size: int, cache, rope: RopeFreqs = None, token_req=None,
+                  stream=None):
+    """New tokens' latent rows into a paged cache: token t of request r (token_req [T] int32, or
+    r = t) at positions[t] (int32, -1 = padding token) goes to row block_table[r][p // block_size] *
+    block_size + p % block_size.  c_kv [T, 512] and k_pe [T, d_rope] bf16 (row-strided views, k_pe
+    None without RoPE columns) are stored with k_pe rotated by ``rope`` (None: as it is).  cache:
+    bf16 [N, ld_kv] or FP8 rows [N, dsa_kv_fp8_row_bytes(d_rope)] uint8.  Returns cache."""
+    import torch
+    for name, x in (("c_kv", c_kv), ("k_pe", k_pe)):
+        if x is None and name == "k_pe":
+            continue
+        if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be a bf16 tensor")
+        if not x.is_cuda or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+            raise ValueError(f"{name} must be a 2-D CUDA tensor with unit stride in its last dimension")
+    T = c_kv.shape[0]
+    d_rope = 0 if k_pe is None else k_pe.shape[1]
+    if c_kv.shape[1] != 512 or (k_pe is not None and k_pe.shape[0] != T):
+        raise ValueError("c_kv must be [T, 512] and k_pe [T, d_rope]")
+    if rope is not None and not isinstance(rope, RopeFreqs):
+        raise TypeError("rope must come from dsa_rope_freqs")
+    _need(positions, torch.int32, "positions", 1)
+    _need(block_table, torch.int32, "block_table", 2)
+    if token_req is not None:
+        _need(token_req, torch.int32, "token_req", 1)
+    if positions.shape[0] != T or (token_req is not None and token_req.shape[0] != T):
+        raise ValueError("positions and token_req must have one entry per token")
+    fmt, N, ld = _cache_of(cache, d_rope)
+    _same_device(cache, c_kv=c_kv, k_pe=k_pe, positions=positions, block_table=block_table, token_req=token_req)
+    pe = k_pe if d_rope else None
+    _check(_on_device(cache, lambda s: lib().dsa_kv_append(
+        c_kv.data_ptr(), c_kv.stride(0), None if pe is None else pe.data_ptr(), 0 if pe is None else pe.stride(0), T,
+        d_rope, positions.data_ptr(), None if token_req is None else token_req.data_ptr(), block_table.data_ptr(),
+        block_table.shape[0], block_table.shape[1], int(block_size), None if rope is None else ctypes.byref(rope),
+        cache.data_ptr(), fmt, N, ld, s), stream), "dsa_kv_append")
+    return cache
+
+
+def dsa_paged_decode_workspace(B: int, H: int) -> int:
+    """Device workspace bytes dsa_paged_decode needs."""
+    n = int(lib().dsa_paged_decode_workspace(int(B), int(H)))
+    if n < 0:
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_paged_decode_workspace")
+    return n
+
+
+def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: float, idx=None, k: int | None = None,
+                     d_v: int = 512, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per request over a paged latent cache.  q [B, H, d_qk] bf16 (d_qk =
+    576 or 512, H <= 128), cache bf16 [N, ld_kv] or FP8 rows uint8, block_table [B, max_blocks] and
+    kv_lens [B] int32 on the device.  idx [B, ld] int32 (first k columns): the token's own top-k
+    positions instead of the whole context.  workspace: a CUDA uint8 tensor of
+    dsa_paged_decode_workspace(B, H) bytes (calls sharing one must not overlap on the GPU); one per
+    call if None.  Returns (out [B, H, 512] bf16, lse [B, H] fp32)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(kv_lens, torch.int32, "kv_lens", 1)
+    B, H, d_qk = q.shape
+    if d_qk not in (512, 576):
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_paged_decode")
+    fmt, N, ld_kv = _cache_of(cache, d_qk - 512)
+    if block_table.shape[0] != B or kv_lens.shape[0] != B:
+        raise ValueError("block_table and kv_lens must have one row per request")
+    ld = 0
+    if idx is not None:
+        _need(idx, torch.int32, "idx", 2)
+        if idx.shape[0] != B:
+            raise ValueError("idx must have one row per request")
+        ld = idx.shape[1]
+        k = ld if k is None else int(k)
+    elif k is not None:
+        raise ValueError("k without idx")
+    made = []
+    if out is None:
+        out = torch.empty((B, H, d_v), dtype=torch.bfloat16, device=q.device)
+        made.append(out)
+    elif _need(out, torch.bfloat16, "out", 3).shape != (B, H, d_v):
+        raise ValueError("out must be [B, H, d_v]")
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    elif _need(lse, torch.float32, "lse", 2).shape != (B, H):
+        raise ValueError("lse must be [B, H]")
+    if workspace is None:
+        workspace = torch.empty(dsa_paged_decode_workspace(B, H), dtype=torch.uint8, device=q.device)
+        made.append(workspace)
+    _need(workspace, torch.uint8, "workspace", 1)
+    _same_device(q, cache=cache, block_table=block_table, kv_lens=kv_lens, idx=idx, out=out, lse=lse,
+                 workspace=workspace)
+    if made:
+        _made_for(stream, *made)
+    _check(_on_device(q, lambda s: lib().dsa_paged_decode(
+        q.data_ptr(), cache.data_ptr(), fmt, N, ld_kv, block_table.data_ptr(), block_table.shape[1], int(block_size),
+        kv_lens.data_ptr(), None if idx is None else idx.data_ptr(), k or 0, ld, B, H, d_qk, d_v, float(scale),
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), s), stream), "dsa_paged_decode")
     return out, lse

@@ -1,5 +1,6 @@
 // C-ABI shim: argument validation, host-side request tables and kernel
 // launches for the entry points declared in include/dsa.h.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <vector>
@@ -483,6 +484,219 @@ int dsa_sparse_prefill_fp8(const uint16_t* q, const uint8_t* kv_fp8, int N, int 
     return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)T * H, d_qk, d_qk, H)) return DSA_ERR_CUDA;
   const int r = dsa::launch_sparse_prefill_fp8(a, d->num_sms, (cudaStream_t)stream);
+  return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
+}
+
+int dsa_rope_freqs_init(dsa_rope_freqs* freqs, int d_rope, double base, int layout, int scaling, double factor,
+                        int original_len, double beta_fast, double beta_slow, float mscale) {
+  if (!freqs || d_rope < 2 || (d_rope & 1) || !(base >= 1.0) || !std::isfinite(base) || !(factor > 0.0) ||
+      !std::isfinite(factor) || !std::isfinite(mscale))
+    return DSA_ERR_INVALID_ARG;
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+  if (scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
+  if (scaling == DSA_ROPE_YARN &&
+      (!(base > 1.0) || original_len < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+    return DSA_ERR_INVALID_ARG;
+  if (d_rope > 2 * DSA_ROPE_MAX_PAIRS) return DSA_ERR_UNSUPPORTED;
+  const double two_pi = 6.283185307179586476925;
+  memset(freqs, 0, sizeof(*freqs));
+  freqs->d_rope = d_rope;
+  freqs->layout = layout;
+  freqs->mscale = mscale;
+  double low = 0.0, high = 1.0;
+  if (scaling == DSA_ROPE_YARN) {
+    auto dim = [&](double turns) { return d_rope * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base)); };
+    low = std::fmax(std::floor(dim(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(dim(beta_slow)), (double)(d_rope - 1));
+    if (!(high > low)) high = low + 0.001;
+  }
+  for (int i = 0; i < d_rope / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / d_rope);
+    if (scaling == DSA_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == DSA_ROPE_YARN) {
+      const double r = std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0);
+      f = f * (1.0 - r) + f / factor * r;
+    }
+    // whole turns per position do not matter: positions are whole numbers
+    double turns = f / two_pi;
+    turns -= std::floor(turns);
+    freqs->turns[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
+  }
+  return DSA_OK;
+}
+
+int dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* y, int64_t y_stride_t, int64_t y_stride_h,
+             int dtype, const int32_t* positions, int T, int H, const dsa_rope_freqs* freqs, int gradient,
+             dsa_stream_t stream) {
+  if (T < 0 || H < 0 || !freqs || x_stride_t < 0 || x_stride_h < 0) return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F32) return DSA_ERR_UNSUPPORTED;
+  const int d = freqs->d_rope;
+  if (d < 2 || (d & 1) || d > 2 * DSA_ROPE_MAX_PAIRS) return DSA_ERR_INVALID_ARG;
+  if (freqs->layout != DSA_ROPE_INTERLEAVED && freqs->layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+  if (T == 0 || H == 0) return DSA_OK;
+  if (!x || !y || !positions || !aligned4(positions)) return DSA_ERR_INVALID_ARG;
+  const int es = dtype == DSA_DTYPE_F32 ? 4 : 2;
+  const uintptr_t px = reinterpret_cast<uintptr_t>(x), py = reinterpret_cast<uintptr_t>(y);
+  if (px % es || py % es) return DSA_ERR_INVALID_ARG;
+  // the result's heads and tokens must not overlap: the closer-packed of the
+  // two dimensions holds a row, the other all of its rows
+  {
+    const bool heads_inside = H == 1 || (T > 1 && y_stride_h <= y_stride_t) || T == 1;
+    const int64_t in_s = heads_inside ? y_stride_h : y_stride_t, in_n = heads_inside ? H : T;
+    const int64_t out_s = heads_inside ? y_stride_t : y_stride_h, out_n = heads_inside ? T : H;
+    if (in_n > 1 && in_s < d) return DSA_ERR_INVALID_ARG;
+    if (out_n > 1 && out_s < (in_n > 1 ? in_s * (in_n - 1) : 0) + d) return DSA_ERR_INVALID_ARG;
+  }
+  if (px == py && ((T > 1 && x_stride_t != y_stride_t) || (H > 1 && x_stride_h != y_stride_h)))
+    return DSA_ERR_INVALID_ARG;
+  DevInfo* dv;
+  if (!dev_info(&dv)) return DSA_ERR_CUDA;
+  dsa::RopeArgs a;
+  a.x = x;
+  a.y = y;
+  a.positions = positions;
+  a.x_stride_t = x_stride_t;
+  a.x_stride_h = x_stride_h;
+  a.y_stride_t = y_stride_t;
+  a.y_stride_h = y_stride_h;
+  a.T = T;
+  a.H = H;
+  a.d = d;
+  a.gradient = gradient ? 1 : 0;
+  a.head_groups = 1;
+  a.table = *freqs;
+  // 16-byte pieces: every row and head starts on one, and they hold whole
+  // pairs (interleaved) or lie in one half
+  const int64_t piece = 16 / es;
+  const int64_t span = freqs->layout == DSA_ROPE_HALF ? d / 2 : d;
+  const bool vec = span % piece == 0 && px % 16 == 0 && py % 16 == 0 && (T == 1 || (x_stride_t % piece == 0 && y_stride_t % piece == 0)) &&
+                   (H == 1 || (x_stride_h % piece == 0 && y_stride_h % piece == 0));
+  const int r = dsa::launch_rope(a, dtype == DSA_DTYPE_F32, vec, dv->num_sms, (cudaStream_t)stream);
+  return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
+}
+
+int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, int64_t pe_stride, int T, int d_rope,
+                  const int32_t* positions, const int32_t* token_req, const int32_t* block_table, int num_req,
+                  int max_blocks, int block_size, const dsa_rope_freqs* freqs, void* cache, int cache_format, int N,
+                  int ld_kv, dsa_stream_t stream) {
+  if (T < 0 || num_req < 0 || max_blocks < 1 || block_size < 1 || N < 0) return DSA_ERR_INVALID_ARG;
+  if (d_rope != 0 && d_rope != 64) return DSA_ERR_UNSUPPORTED;
+  if (cache_format != DSA_CACHE_BF16 && cache_format != DSA_CACHE_FP8) return DSA_ERR_UNSUPPORTED;
+  if (freqs && freqs->d_rope != d_rope) return DSA_ERR_UNSUPPORTED;
+  if (freqs && freqs->layout != DSA_ROPE_INTERLEAVED && freqs->layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+  if (cache_format == DSA_CACHE_BF16 && (ld_kv < 512 + d_rope || (ld_kv & 7) != 0)) return DSA_ERR_INVALID_ARG;
+  if (c_stride < 0 || (c_stride & 7) != 0 || (T > 1 && c_stride != 0 && c_stride < 512)) return DSA_ERR_INVALID_ARG;
+  if (d_rope && (pe_stride < 0 || (pe_stride & 7) != 0 || (T > 1 && pe_stride != 0 && pe_stride < d_rope)))
+    return DSA_ERR_INVALID_ARG;
+  if (token_req == nullptr && T > num_req) return DSA_ERR_INVALID_ARG;
+  if (T == 0) return DSA_OK;
+  if (!c_kv || (d_rope && !k_pe) || !positions || (!block_table && num_req > 0) || (!cache && N > 0))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(c_kv) || (d_rope && !aligned16(k_pe)) || !aligned4(positions) || !aligned4(token_req) ||
+      !aligned4(block_table) || !aligned16(cache))
+    return DSA_ERR_INVALID_ARG;
+  DevInfo* d;
+  if (!dev_info(&d)) return DSA_ERR_CUDA;
+  dsa::AppendArgs a;
+  memset(&a, 0, sizeof(a));
+  a.c_kv = c_kv;
+  a.k_pe = k_pe;
+  a.positions = positions;
+  a.token_req = token_req;
+  a.block_table = block_table;
+  a.cache = cache;
+  a.err = d->err;
+  a.c_stride = c_stride;
+  a.pe_stride = pe_stride;
+  a.T = T;
+  a.d_rope = d_rope;
+  a.num_req = num_req;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.N = N;
+  a.ld_kv = ld_kv;
+  a.rotate = freqs != nullptr;
+  if (freqs) a.table = *freqs;
+  return dsa::launch_kv_append(a, cache_format == DSA_CACHE_FP8, d->num_sms, (cudaStream_t)stream) == 0 ? DSA_OK
+                                                                                                        : DSA_ERR_CUDA;
+}
+
+// bytes of the partial results (log-sum-exp, then outputs): two per CTA group
+static int64_t decode_part_bytes(int H, int64_t* lse_bytes) {
+  const int64_t hp = (int64_t)dsa::decode_head_blocks(H) * dsa::decode_heads_per_cta(H);
+  const int64_t slots = 2 * (dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H));
+  *lse_bytes = (slots * hp * 4 + 255) / 256 * 256;
+  return *lse_bytes + slots * hp * 512 * 4;
+}
+
+int64_t dsa_paged_decode_workspace(int B, int H) {
+  if (B < 0 || H < 1 || H > 128) return -1;
+  int64_t l;
+  return decode_part_bytes(H, &l);
+}
+
+int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                     const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                     const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
+                     float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream) {
+  if (B < 0 || N < 0 || max_blocks < 1 || block_size < 1) return DSA_ERR_INVALID_ARG;
+  if (!(scale > -INFINITY) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+  if (H < 1 || H > 128 || !(d_qk == 576 || d_qk == 512) || d_v != 512) return DSA_ERR_UNSUPPORTED;
+  if (cache_format != DSA_CACHE_BF16 && cache_format != DSA_CACHE_FP8) return DSA_ERR_UNSUPPORTED;
+  if (cache_format == DSA_CACHE_BF16 && (ld_kv < d_qk || (ld_kv & 7) != 0)) return DSA_ERR_INVALID_ARG;
+  if (idx && (k < 0 || ld < k)) return DSA_ERR_INVALID_ARG;
+  if ((int64_t)B * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (B == 0) return DSA_OK;
+  if (!q || (!cache && N > 0) || !block_table || !kv_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||
+      !aligned16(out) || !aligned4(lse))
+    return DSA_ERR_INVALID_ARG;
+  int64_t lse_bytes;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < decode_part_bytes(H, &lse_bytes))
+    return DSA_ERR_INVALID_ARG;
+  DevInfo* d;
+  if (!dev_info(&d)) return DSA_ERR_CUDA;
+  dsa::DecodeArgs a;
+  memset(&a, 0, sizeof(a));
+  const bool fp8 = cache_format == DSA_CACHE_FP8;
+  const int d_rope = d_qk - 512;
+  a.kv8 = fp8 ? static_cast<const uint8_t*>(cache) : nullptr;
+  a.row_bytes = fp8 ? 528 + 2 * d_rope : 0;
+  a.block_table = block_table;
+  a.kv_lens = kv_lens;
+  a.idx = idx;
+  a.out = out;
+  a.lse = lse;
+  a.part_lse = static_cast<float*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lse_bytes);
+  a.err = d->err;
+  a.B = B;
+  a.H = H;
+  a.N = N;
+  a.k = k;
+  a.ld = ld;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.scale = scale;
+  a.head_blocks = dsa::decode_head_blocks(H);
+  const int64_t most = idx ? k : ((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
+  const int64_t max_tiles = (most + 127) / 128;
+  const int ctas = d->num_sms < dsa::kDecodeMaxCtas ? d->num_sms : dsa::kDecodeMaxCtas;
+  const int64_t tiles = (int64_t)B * max_tiles;
+  a.groups = ctas / a.head_blocks;
+  if (tiles < a.groups) a.groups = tiles > 0 ? (int)tiles : 1;
+  // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
+  const bool none = N == 0;
+  const bool mapped = fp8 ? dsa::make_row_gather_map_u8(&a.tmap_kv, none ? (const void*)q : cache,
+                                                        none ? (int64_t)B * H : N, none ? 2 * d_qk : a.row_bytes)
+                          : dsa::make_row_gather_map(&a.tmap_kv, none ? (const void*)q : cache,
+                                                     none ? (int64_t)B * H : N, none ? d_qk : ld_kv,
+                                                     none ? d_qk : ld_kv);
+  if (!mapped) return DSA_ERR_CUDA;
+  if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H))) return DSA_ERR_CUDA;
+  const int r = dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
 }
 

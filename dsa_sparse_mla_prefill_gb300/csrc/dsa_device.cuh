@@ -272,6 +272,44 @@ __device__ __forceinline__ void e4m3x4_dequant_bf16x4(uint32_t w, float s, uint3
   hi = f16x2_scaled_bf16x2(h1, s);
 }
 
+// IEEE float32 operations that keep subnormals (the library is otherwise
+// built to flush them), and the saturating e4m3 conversion (low byte: lo).
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float div_ieee(float a, float b) {
+  float r;
+  asm("div.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_ieee(float a, float b) {
+  float r;
+  asm("max.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float abs_ieee(float a) {
+  float r;
+  asm("abs.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+// One warp quantizes one 128-column block: lane l holds columns 4l .. 4l+3
+// as bf16 bits and gets their four codes (byte i = column 4l + i) and the
+// block's scale.  Every lane of the warp calls it.
+__device__ __forceinline__ uint32_t e4m3_quantize_block(uint2 raw, float& scale) {
+  const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                      __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+  float amax = max_ieee(max_ieee(abs_ieee(v[0]), abs_ieee(v[1])), max_ieee(abs_ieee(v[2]), abs_ieee(v[3])));
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // (amax is +0 or positive: a zero bit pattern is an all-zero block)
+  scale = __float_as_uint(amax) != 0u ? div_ieee(amax, 448.f) : 1.f;
+  const uint32_t lo = f32x2_to_e4m3x2(div_ieee(v[0], scale), div_ieee(v[1], scale));
+  const uint32_t hi = f32x2_to_e4m3x2(div_ieee(v[2], scale), div_ieee(v[3], scale));
+  return lo | (hi << 16);
+}
+
 // cp.async of 4 bytes (src_bytes = 0: zero fill), and an arrival on an
 // mbarrier once this thread's earlier cp.async copies have landed (the
 // barrier's pending count is raised now and lowered then).

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/dsa.h"
+
 namespace dsa {
 
 // Requests whose host-side sequence offsets travel inside the launch
@@ -67,6 +69,50 @@ struct Fp8KvArgs {
   uint16_t* kv_out;     // dequantize: bf16 rows [N, ld_kv]
   uint8_t* fp8;         // FP8 rows [N, 528 + 2 d_rope] (quantize writes, dequantize reads)
   int N, ld_kv, d_rope;
+};
+
+struct RopeArgs {
+  const void* x;              // [T, H, d] by strides (elements), unit last stride
+  void* y;                    // may be x
+  const int32_t* positions;   // [T]
+  int64_t x_stride_t, x_stride_h, y_stride_t, y_stride_h;
+  int T, H, d;
+  int gradient;               // turn back
+  int head_groups;            // threads that share a token's heads (set by the launch)
+  dsa_rope_freqs table;
+};
+
+struct AppendArgs {
+  const uint16_t* c_kv;       // [T, 512] bf16, row stride c_stride
+  const uint16_t* k_pe;       // [T, d_rope] bf16, row stride pe_stride
+  const int32_t* positions;   // [T], -1 = padding token
+  const int32_t* token_req;   // [T] or null: token t is request t's
+  const int32_t* block_table; // [num_req, max_blocks]
+  void* cache;                // bf16 rows [N, ld_kv] or FP8 rows [N, 528 + 2 d_rope]
+  unsigned int* err;
+  int64_t c_stride, pe_stride;
+  int T, d_rope, num_req, max_blocks, block_size, N, ld_kv;
+  int rotate;                 // 0: the RoPE columns are stored as they are
+  dsa_rope_freqs table;
+};
+
+struct DecodeArgs {
+  CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box
+  CUtensorMap tmap_q;         // q viewed [B*H, d_qk], 64-column x HB-row box
+  const uint8_t* kv8;         // FP8 rows (the FP8 kernel)
+  int row_bytes;
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* kv_lens;     // [B]
+  const int32_t* idx;         // [B, ld] positions, or null: every position < kv_len
+  uint16_t* out;              // [B, H, 512] bf16
+  float* lse;                 // [B, H]
+  float* part_o;              // [2 groups][heads padded][512] normalised partial outputs
+  float* part_lse;            // [2 groups][heads padded] their log-sum-exp, base 2
+  unsigned int* err;
+  int B, H, N, k, ld, max_blocks, block_size;
+  int groups;                 // CTA groups (each of head_blocks CTAs)
+  int head_blocks;            // CTAs of a group, each with its own heads
+  float scale;
 };
 
 struct KeyMaskArgs {
@@ -152,6 +198,15 @@ int launch_grouped_prefill(const GroupedArgs& a, int num_sms, cudaStream_t strea
 int launch_masked_mha(const MaskedArgs& a, int num_sms, cudaStream_t stream);
 int launch_wait_timeout(unsigned int* err, cudaStream_t stream);
 int launch_kv_fp8(const Fp8KvArgs& a, bool quantize, int num_sms, cudaStream_t stream);
+int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t stream);
+int launch_kv_append(const AppendArgs& a, bool fp8, int num_sms, cudaStream_t stream);
+
+// Heads per CTA of the decode kernel and the CTAs its heads take.
+inline int decode_heads_per_cta(int H) { return H <= 16 ? 16 : 32; }
+inline int decode_head_blocks(int H) { return (H + decode_heads_per_cta(H) - 1) / decode_heads_per_cta(H); }
+constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
+// max_tiles: an upper bound of a request's key tiles (1: nothing is split).
+int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
 
 // dsa_sparse_prefill with the streamed-call fields of SparseArgs (ready, done,
 // done_blk; all null / 0 for an ordinary call).  Same checks and DSA_* status

@@ -30,31 +30,6 @@ namespace fp8kv {
 constexpr int NT = 128;
 constexpr int RPI = 8;   // rows per CTA per iteration
 
-__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;   // low byte: lo's code
-}
-
-__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
-
-// IEEE float32 operations that keep subnormals
-__device__ __forceinline__ float div_ieee(float a, float b) {
-  float r;
-  asm("div.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_ieee(float a, float b) {
-  float r;
-  asm("max.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float abs_ieee(float a) {
-  float r;
-  asm("abs.f32 %0, %1;" : "=f"(r) : "f"(a));
-  return r;
-}
-
 __global__ void __launch_bounds__(NT) quantize_kernel(Fp8KvArgs a) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rb = 528 + 2 * a.d_rope;
@@ -74,18 +49,11 @@ __global__ void __launch_bounds__(NT) quantize_kernel(Fp8KvArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < RPI; ++r) {
-      const float v[4] = {bf16_bits_to_f32(raw[r].x & 0xffffu), bf16_bits_to_f32(raw[r].x >> 16),
-                          bf16_bits_to_f32(raw[r].y & 0xffffu), bf16_bits_to_f32(raw[r].y >> 16)};
-      float amax = max_ieee(max_ieee(abs_ieee(v[0]), abs_ieee(v[1])), max_ieee(abs_ieee(v[2]), abs_ieee(v[3])));
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float scale;
+      const uint32_t codes = e4m3_quantize_block(raw[r], scale);
       if (n0 + r >= a.N) continue;
       uint8_t* dst = a.fp8 + (size_t)(n0 + r) * rb;
-      // (amax is +0 or positive: a zero bit pattern is an all-zero block)
-      const float scale = __float_as_uint(amax) != 0u ? div_ieee(amax, 448.f) : 1.f;
-      const uint32_t lo = f32x2_to_e4m3x2(div_ieee(v[0], scale), div_ieee(v[1], scale));
-      const uint32_t hi = f32x2_to_e4m3x2(div_ieee(v[2], scale), div_ieee(v[3], scale));
-      *reinterpret_cast<uint32_t*>(dst + 128 * w + 4 * lane) = lo | (hi << 16);
+      *reinterpret_cast<uint32_t*>(dst + 128 * w + 4 * lane) = codes;
       if (lane == 0) *reinterpret_cast<float*>(dst + 512 + 4 * w) = scale;
       if (w == 0 && 2 * lane < a.d_rope)   // RoPE columns: 2 per lane
         *reinterpret_cast<uint32_t*>(dst + 528 + 4 * lane) = rope[r];

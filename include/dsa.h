@@ -384,6 +384,121 @@ int dsa_sparse_prefill_fp8(const uint16_t* q, const uint8_t* kv_fp8, int N, int 
                            dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The decode step over a paged latent cache (no counterpart on the pages,
+ * which end with the prefill): rotary positions, the new tokens' latent rows
+ * into the cache, attention of one new token per request.  All three read
+ * positions, lengths and block tables on the device, plan nothing on the host
+ * and allocate nothing, so a captured graph follows the tensors' contents.
+ * ---------------------------------------------------------------------- */
+
+/* Rotary frequencies (host only).  Pair i of d_rope / 2 turns by
+ *     f_i = base^(-2 i / d_rope)
+ * per position; DSA_ROPE_LINEAR: f_i / factor (positions interpolated);
+ * DSA_ROPE_YARN: f_i (1 - r_i) + f_i / factor * r_i, where r_i rises from 0 to
+ * 1 between the pairs that turn beta_fast and beta_slow times over
+ * original_len positions:
+ *     dim(n) = d_rope ln(original_len / (2 pi n)) / (2 ln base),
+ *     low = max(floor(dim(beta_fast)), 0), high = min(ceil(dim(beta_slow)), d_rope - 1),
+ *     r_i = (i - low) / (high - low) held to [0, 1]  (high = low + 0.001 when equal).
+ * mscale multiplies cos and sin (the attention factor of long-context
+ * scalings; 1 otherwise).  layout: the elements that make a pair, (2i, 2i+1)
+ * or (i, i + d_rope/2).  turns[i] = f_i / (2 pi) modulo 1 as a fraction of
+ * 2^64. */
+#define DSA_ROPE_MAX_PAIRS 128
+enum dsa_rope_layout { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+enum dsa_rope_scaling { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_YARN = 2 };
+
+typedef struct dsa_rope_freqs {
+  int32_t d_rope;
+  int32_t layout;
+  float mscale;
+  int32_t reserved;
+  uint64_t turns[DSA_ROPE_MAX_PAIRS];
+} dsa_rope_freqs;
+
+/* Fills *freqs.  DSA_ERR_INVALID_ARG: null, d_rope odd or < 2, base < 1 or
+ * not finite (YaRN: base <= 1), factor <= 0 or not finite, mscale not finite,
+ * an unknown layout or scaling, YaRN with original_len < 1, or not beta_fast
+ * >= beta_slow > 0; DSA_ERR_UNSUPPORTED: d_rope > 256. */
+int dsa_rope_freqs_init(dsa_rope_freqs* freqs, int d_rope, double base, int layout, int scaling, double factor,
+                        int original_len, double beta_fast, double beta_slow, float mscale);
+
+/* Rotary positions: y[t,h,:] = mscale * R(positions[t]) x[t,h,:], or with
+ * gradient = 1 mscale * R(-positions[t]) x[t,h,:], the gradient of the former.
+ *
+ * x, y       [T, H, d] by strides in elements (x_stride_t, x_stride_h; unit
+ *            last stride), d = freqs->d_rope: a view of part of the head is
+ *            rotated by passing that view.  y may be x (same strides: in
+ *            place); otherwise it must not overlap x.  Heads and tokens of y
+ *            must not overlap each other; x may be broadcast (stride 0).
+ * dtype      DSA_DTYPE_BF16 (the result rounded once) or DSA_DTYPE_F32.
+ * positions  DEVICE int32 [T], any value (negative ones turn backwards).
+ * freqs      HOST, copied into the launch.
+ * Pointers aligned to their element; any strides (16-byte aligned rows, heads
+ * and pointers with d a multiple of 16 bytes' worth of elements run fastest).
+ * DSA_ERR_UNSUPPORTED: more than 2^32 - 256 pairs of all tokens' heads. */
+enum dsa_dtype { DSA_DTYPE_BF16 = 0, DSA_DTYPE_F32 = 1 };
+int dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* y, int64_t y_stride_t, int64_t y_stride_h,
+             int dtype, const int32_t* positions, int T, int H, const dsa_rope_freqs* freqs, int gradient,
+             dsa_stream_t stream);
+
+/* New tokens' latent rows into a paged cache.  Token t of request r at
+ * position p is written to row block_table[r][p / block_size] * block_size +
+ * p % block_size: columns 0..511 from c_kv, then d_rope columns from k_pe
+ * rotated to p (freqs; NULL stores them as they are).
+ *
+ * c_kv, k_pe   bf16 [T, 512] and [T, d_rope], row strides in elements
+ *              (multiples of 8; k_pe ignored at d_rope = 0), 16-byte aligned.
+ * positions    DEVICE int32 [T]; -1 = padding token, writes nothing.
+ * token_req    DEVICE int32 [T], or NULL: token t belongs to request t.
+ * block_table  DEVICE int32 [num_req, max_blocks], physical block ids.
+ * cache        DSA_CACHE_BF16: bf16 [N, ld_kv], ld_kv >= 512 + d_rope and a
+ *              multiple of 8; DSA_CACHE_FP8: rows of dsa_kv_fp8_row_bytes
+ *              bytes as dsa_kv_fp8_quantize writes them (ld_kv ignored): the
+ *              same bits as quantizing the bf16 row.  16-byte aligned.
+ * A token whose position, request, block id or row is out of range writes
+ * nothing and is counted in counts[0] of dsa_last_device_error.  Rows no token
+ * names keep their contents, and so do columns past 512 + d_rope.  Two tokens
+ * that name one row race on it: the row is then unspecified.
+ * d_rope in {0, 64}, and freqs->d_rope = d_rope, else DSA_ERR_UNSUPPORTED. */
+enum dsa_cache_format { DSA_CACHE_BF16 = 0, DSA_CACHE_FP8 = 1 };
+int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, int64_t pe_stride, int T, int d_rope,
+                  const int32_t* positions, const int32_t* token_req, const int32_t* block_table, int num_req,
+                  int max_blocks, int block_size, const dsa_rope_freqs* freqs, void* cache, int cache_format, int N,
+                  int ld_kv, dsa_stream_t stream);
+
+/* Attention of one new token per request over the paged cache:
+ *     out[b,h,:] = softmax_j(scale * q[b,h,:] . c_j) . c_j[0:512]
+ *     lse[b,h]   = ln sum_j exp(scale * q[b,h,:] . c_j)
+ * over the positions j of request b: all j < kv_lens[b] (idx NULL), or the
+ * entries of idx[b, 0:k] (the token's top-k positions, -1 = no selection; an
+ * entry listed twice counts twice).
+ *
+ * q            bf16 [B, H, d_qk], 16-byte aligned; 1 <= H <= 128.
+ * cache        as for dsa_kv_append; d_qk = 576 or 512 (d_rope 64 or 0),
+ *              d_v = 512.  May be NULL when N = 0.
+ * block_table  DEVICE int32 [B, max_blocks].
+ * kv_lens      DEVICE int32 [B].  Zero or less: no keys.  A length past
+ *              max_blocks * block_size is cut to it and counted once.
+ * idx          DEVICE int32 [B, ld] or NULL; k <= ld.
+ * out, lse     bf16 [B, H, 512] (16-byte aligned), fp32 [B, H].
+ * workspace    DEVICE scratch, 256-byte aligned, of at least
+ *              dsa_paged_decode_workspace(B, H) bytes.  Nothing in it has to
+ *              survive between calls or start at zero; calls that share it
+ *              (captured graphs among them) must not overlap on the GPU.
+ * A request without any valid key gets out = 0 and lse = -inf.  Positions
+ * whose block id or row is out of range, and entries of idx that are neither
+ * -1 nor in [0, kv_lens[b]), are treated as absent and counted.  Cache rows
+ * that no position names are never read into a result, whatever they hold.
+ * Two kernels are queued on `stream` (one when no request can hold more than
+ * 128 keys).  scale must be finite.  The same inputs give the same bits. */
+int64_t dsa_paged_decode_workspace(int B, int H);
+int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                     const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                     const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
+                     float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Form choice (host only, no GPU call).  "[Perf][GLM-5.3-Flash] ...", commit
  * messages: prompts within the top-k budget run dense MHA, longer ones masked
  * MHA up to a length threshold (36k tokens at TP4, 64k at TP8) and the

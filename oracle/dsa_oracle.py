@@ -405,6 +405,110 @@ def kv_fp8_dequantize(rows, d_rope: int) -> np.ndarray:
 
 
 # ----------------------------------------------------------------------------
+# the decode step: rotary positions, cache append, paged attention of one token
+# ----------------------------------------------------------------------------
+def rope_frequencies(d: int, base: float, scaling: str = "none", factor: float = 1.0, original_len: int = 4096,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0) -> np.ndarray:
+    """Angle per position of each pair [d/2]: base^(-2i/d); "linear" divides
+    them by factor; "yarn" divides those that turn fewer than beta_slow times
+    over original_len positions, keeps those that turn more than beta_fast
+    times, and mixes the pairs between (a ramp over the pair index whose ends
+    are the pairs with exactly those turn counts, rounded outwards)."""
+    f = np.array([base ** (-2.0 * i / d) for i in range(d // 2)])
+    if scaling == "none":
+        return f
+    if scaling == "linear":
+        return f / factor
+    assert scaling == "yarn"
+
+    def pair_that_turns(n):
+        return d * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base))
+
+    low = max(math.floor(pair_that_turns(beta_fast)), 0)
+    high = min(math.ceil(pair_that_turns(beta_slow)), d - 1)
+    out = np.zeros_like(f)
+    for i in range(d // 2):
+        slow = min(max((i - low) / ((high - low) if high > low else 0.001), 0.0), 1.0)
+        out[i] = f[i] * (1 - slow) + f[i] / factor * slow
+    return out
+
+
+def rope(x, positions, freqs, layout: str, mscale: float = 1.0, gradient: bool = False) -> np.ndarray:
+    """x [T, ..., d] (float64): pair i of token t turned by positions[t] *
+    freqs[i] (back with gradient) and multiplied by mscale; pairs (2i, 2i+1)
+    or (i, i + d/2)."""
+    x = np.asarray(x, dtype=np.float64)
+    d = x.shape[-1]
+    a = np.asarray(positions, dtype=np.float64)[:, None] * np.asarray(freqs)[None]
+    a = a.reshape((x.shape[0],) + (1,) * (x.ndim - 2) + (d // 2,))
+    c, s = mscale * np.cos(a), mscale * np.sin(a) * (-1.0 if gradient else 1.0)
+    out = np.empty_like(x)
+    first = slice(0, None, 2) if layout == "interleaved" else slice(0, d // 2)
+    second = slice(1, None, 2) if layout == "interleaved" else slice(d // 2, None)
+    out[..., first] = x[..., first] * c - x[..., second] * s
+    out[..., second] = x[..., first] * s + x[..., second] * c
+    return out
+
+
+def append_rows(positions, token_req, block_table, block_size: int, N: int):
+    """The cache row each token is written to, -1 for padding tokens (position
+    -1) and for tokens out of range in any way; and the number of the latter."""
+    bt = np.asarray(block_table, dtype=np.int64)
+    rows, bad = [], 0
+    for t, p in enumerate(int(x) for x in positions):
+        r = t if token_req is None else int(token_req[t])
+        row = -1
+        if p != -1:
+            if p >= 0 and 0 <= r < bt.shape[0] and p // block_size < bt.shape[1] and bt[r, p // block_size] >= 0:
+                row = int(bt[r, p // block_size]) * block_size + p % block_size
+                row = row if row < N else -1
+            bad += row < 0
+        rows.append(row)
+    return np.array(rows, dtype=np.int64), bad
+
+
+def paged_decode(q_bits, cache, block_table, kv_lens, block_size: int, scale: float, idx=None, k=None):
+    """Attention of one token per request over the latent rows (cache, float64
+    [N, d_qk]) that its positions name: all positions below kv_lens[b], or
+    those of idx[b, :k].  Absent: -1; absent and counted: positions outside
+    [0, kv_len), unmapped blocks, rows outside the cache.  Returns a dict:
+    out, lse; spread = sum_j w_j |c_j| per output and mass = the largest
+    scale * sum_i |q_i c_ji| per head (what rounding errors are measured by);
+    bad = entries counted."""
+    q = bf16_to_f64(q_bits)
+    B, H, d_qk = q.shape
+    bt = np.asarray(block_table, dtype=np.int64)
+    res = dict(out=np.zeros((B, H, 512)), lse=np.full((B, H), -np.inf), spread=np.zeros((B, H, 512)),
+               mass=np.zeros((B, H)), bad=0)
+    for b in range(B):
+        n = int(kv_lens[b])
+        if n > bt.shape[1] * block_size:
+            n = bt.shape[1] * block_size
+            res["bad"] += 1
+        rows = []
+        listed = range(max(n, 0)) if idx is None else ([int(x) for x in idx[b][:k]] if n > 0 else [])
+        for p in listed:
+            if p == -1:
+                continue
+            blk = bt[b, p // block_size] if 0 <= p < n else -1
+            row = blk * block_size + p % block_size
+            if blk < 0 or row >= len(cache):
+                res["bad"] += 1
+                continue
+            rows.append(row)
+        if not rows:
+            continue
+        c = cache[np.array(rows)]
+        o, l = attend(q[b], c, c[:, :512], scale)
+        res["out"][b], res["lse"][b] = o, l
+        s = scale * (q[b] @ c.T)
+        w = np.exp(s - l[:, None])
+        res["spread"][b] = w @ np.abs(c[:, :512])
+        res["mass"][b] = (abs(scale) * (np.abs(q[b]) @ np.abs(c).T)).max(axis=1)
+    return res
+
+
+# ----------------------------------------------------------------------------
 # comparison used by the parity tests
 # ----------------------------------------------------------------------------
 
