@@ -622,18 +622,20 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
                                                                                                         : DSA_ERR_CUDA;
 }
 
-// bytes of the partial results (log-sum-exp, then outputs): two per CTA group
-static int64_t decode_part_bytes(int H, int64_t* lse_bytes) {
+// workspace: where the ranges end, then two partial results per CTA group
+// (log-sum-exp, then outputs)
+static int64_t decode_part_bytes(int H, int64_t* lse_at, int64_t* out_at) {
   const int64_t hp = (int64_t)dsa::decode_head_blocks(H) * dsa::decode_heads_per_cta(H);
   const int64_t slots = 2 * (dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H));
-  *lse_bytes = (slots * hp * 4 + 255) / 256 * 256;
-  return *lse_bytes + slots * hp * 512 * 4;
+  *lse_at = (16 * (1 + dsa::kDecodeMaxCtas) + 255) / 256 * 256;
+  *out_at = *lse_at + (slots * hp * 4 + 255) / 256 * 256;
+  return *out_at + slots * hp * 512 * 4;
 }
 
 int64_t dsa_paged_decode_workspace(int B, int H) {
   if (B < 0 || H < 1 || H > 128) return -1;
-  int64_t l;
-  return decode_part_bytes(H, &l);
+  int64_t l, o;
+  return decode_part_bytes(H, &l, &o);
 }
 
 int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
@@ -647,14 +649,19 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   if (cache_format == DSA_CACHE_BF16 && (ld_kv < d_qk || (ld_kv & 7) != 0)) return DSA_ERR_INVALID_ARG;
   if (idx && (k < 0 || ld < k)) return DSA_ERR_INVALID_ARG;
   if ((int64_t)B * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  // key tiles of a request at most, and of all (counted in 32 bits)
+  const int64_t most = idx ? k : ((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
+  const int64_t max_tiles = (most + 127) / 128;
+  const int64_t tiles = (int64_t)B * max_tiles;
+  if (tiles > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (B == 0) return DSA_OK;
   if (!q || (!cache && N > 0) || !block_table || !kv_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||
       !aligned16(out) || !aligned4(lse))
     return DSA_ERR_INVALID_ARG;
-  int64_t lse_bytes;
+  int64_t lse_at, out_at;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < decode_part_bytes(H, &lse_bytes))
+      workspace_bytes < decode_part_bytes(H, &lse_at, &out_at))
     return DSA_ERR_INVALID_ARG;
   DevInfo* d;
   if (!dev_info(&d)) return DSA_ERR_CUDA;
@@ -662,15 +669,17 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   memset(&a, 0, sizeof(a));
   const bool fp8 = cache_format == DSA_CACHE_FP8;
   const int d_rope = d_qk - 512;
-  a.kv8 = fp8 ? static_cast<const uint8_t*>(cache) : nullptr;
-  a.row_bytes = fp8 ? 528 + 2 * d_rope : 0;
+  a.rows_base = static_cast<const uint8_t*>(cache);
+  a.row_bytes = fp8 ? 528 + 2 * d_rope : 2 * ld_kv;
+  a.row_used = fp8 ? a.row_bytes : 2 * d_qk;
   a.block_table = block_table;
   a.kv_lens = kv_lens;
   a.idx = idx;
   a.out = out;
   a.lse = lse;
-  a.part_lse = static_cast<float*>(workspace);
-  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lse_bytes);
+  a.borders = static_cast<int4*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lse_at);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + out_at);
   a.err = d->err;
   a.B = B;
   a.H = H;
@@ -680,11 +689,9 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   a.max_blocks = max_blocks;
   a.block_size = block_size;
   a.scale = scale;
+  a.tr = g_trace;
   a.head_blocks = dsa::decode_head_blocks(H);
-  const int64_t most = idx ? k : ((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
-  const int64_t max_tiles = (most + 127) / 128;
   const int ctas = d->num_sms < dsa::kDecodeMaxCtas ? d->num_sms : dsa::kDecodeMaxCtas;
-  const int64_t tiles = (int64_t)B * max_tiles;
   a.groups = ctas / a.head_blocks;
   if (tiles < a.groups) a.groups = tiles > 0 ? (int)tiles : 1;
   // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
@@ -695,6 +702,13 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
                                                      none ? (int64_t)B * H : N, none ? d_qk : ld_kv,
                                                      none ? d_qk : ld_kv);
   if (!mapped) return DSA_ERR_CUDA;
+  // whole-context calls load runs of rows: the largest power of two in the page size, at most a tile
+  const int run = block_size & -block_size;
+  a.box_rows = idx || none || run < 8 ? 0 : (run < 128 ? run : 128);
+  if (a.box_rows &&
+      !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
+            : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
+    return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H))) return DSA_ERR_CUDA;
   const int r = dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);

@@ -98,14 +98,17 @@ struct AppendArgs {
 
 struct DecodeArgs {
   CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box
+  CUtensorMap tmap_box;       // cache rows, 64-column x box_rows box (unset when box_rows = 0)
   CUtensorMap tmap_q;         // q viewed [B*H, d_qk], 64-column x HB-row box
-  const uint8_t* kv8;         // FP8 rows (the FP8 kernel)
-  int row_bytes;
+  const uint8_t* rows_base;   // the cache rows as bytes, their pitch, and the bytes of each that are read
+  int row_bytes, row_used;
+  int box_rows;               // rows that a page holds in one run: 8 .. 128, a power of two; 0 = gather rows
   const int32_t* block_table; // [B, max_blocks]
   const int32_t* kv_lens;     // [B]
   const int32_t* idx;         // [B, ld] positions, or null: every position < kv_len
   uint16_t* out;              // [B, H, 512] bf16
   float* lse;                 // [B, H]
+  int4* borders;              // [1 + groups]: tiles and ranges, then where each range ends
   float* part_o;              // [2 groups][heads padded][512] normalised partial outputs
   float* part_lse;            // [2 groups][heads padded] their log-sum-exp, base 2
   unsigned int* err;
@@ -113,6 +116,7 @@ struct DecodeArgs {
   int groups;                 // CTA groups (each of head_blocks CTAs)
   int head_blocks;            // CTAs of a group, each with its own heads
   float scale;
+  TraceArgs tr;
 };
 
 struct KeyMaskArgs {

@@ -27,11 +27,15 @@
 //               running max grows by more than 2^8); P to shared memory in
 //               bf16; the epilogue (O^T lane = output column).
 //   warp 8      QK issuer: S^T = K q^T, keys on the M side (M = 128, N = heads)
-//   warps 9,10  PV issuers: O^T += V^T P^T, alternate 128-column units
+//   warps 9, 10, 20, 21  PV issuers: O^T += V^T P^T, one 128-column unit each
 //   warp 11     scheduler: walks the range, turns 128 positions per tile into
-//               rows (a ring of four tiles ahead), loads q per request
-//   warps 12-21 TMA row gathers, two warps per unit slot
-//   warp 22     the same for the RoPE columns; warp 23: requests without keys
+//               rows (a ring of four tiles ahead)
+//   warps 12-19 TMA loads of the units: row gathers (4 rows x 128 bytes per
+//               instruction), or boxes of up to 128 rows where every key of the
+//               tile is there and the pages hold them in runs (page sizes that
+//               are multiples of 8 rows)
+//   warp 22     the same for the RoPE columns
+//   warp 23     q per request; the outputs of requests without keys
 // Every key row is gathered once: a tile of 128 keys is four 128-column units
 // (32 KB, in a ring of five) and one RoPE chunk; QK reads a unit K-major, P.V
 // reads the same bytes MN-major, and the unit goes back to the producers when
@@ -42,6 +46,8 @@
 // Rounding: P is rounded to bf16 for the tensor core.  The outputs are divided
 // by the sum of the rounded weights (so that the weights used add up to one);
 // the log-sum-exp comes from the unrounded sum, both in fp32.
+#include <cfloat>
+
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
 
@@ -51,7 +57,7 @@ namespace decode {
 constexpr int BK = 128;          // keys per tile (the MMA's M)
 constexpr int NTHREADS = 768;
 constexpr int NI = 4;            // tiles of rows ahead
-constexpr int NU = 5;            // 128-column unit slots
+constexpr int NPROD = 12;        // warps that load the rows
 constexpr float kTau = 8.0f;     // lazy-rescale threshold (log2 units)
 // 768 threads launched at 80 registers: 256 * 144 + 512 * 48 = 768 * 80
 constexpr int REGS_SOFTMAX = 144;
@@ -60,23 +66,27 @@ constexpr int REGS_REST = 48;
 template <int HB, int NC>
 struct Cfg {
   static constexpr int HT = HB / 2;                      // heads per softmax thread
-  static constexpr int NQ = HB == 16 ? 2 : 1;            // q buffers (what shared memory leaves)
+  // K ring: 64-column chunks; V ring: 128-column units (what shared memory leaves beside q and P)
+  static constexpr int NK = HB == 16 ? 6 : 5;
+  static constexpr int NV = 3;
+  static constexpr int VW = NPROD - NK;                  // warps that load V
+  static constexpr int VL = (64 + VW - 1) / VW;          // row gathers of a unit per V warp
   static constexpr uint32_t CHUNK_BYTES = BK * 128u;     // 128 keys x 64 columns
   static constexpr uint32_t UNIT_BYTES = 2u * CHUNK_BYTES;
   static constexpr uint32_t Q_BYTES = NC * HB * 128u;
   static constexpr uint32_t P_BYTES = 2u * HB * 128u;
   static constexpr uint32_t RED_FLOATS = 2u * 2u * 4u * HT;   // [parity][warpgroup][warp][head]
-  static constexpr uint32_t OFF_U = 0;
-  static constexpr uint32_t OFF_R = NU * UNIT_BYTES;
-  static constexpr uint32_t OFF_Q = OFF_R + (NC == 9 ? CHUNK_BYTES : 0u);
-  static constexpr uint32_t OFF_P = OFF_Q + NQ * Q_BYTES;
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_V = OFF_K + NK * CHUNK_BYTES;
+  static constexpr uint32_t OFF_Q = OFF_V + NV * UNIT_BYTES;
+  static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
   static constexpr uint32_t OFF_ROWS = OFF_P + P_BYTES;
   static constexpr uint32_t OFF_META = OFF_ROWS + NI * BK * 4u;
   static constexpr uint32_t OFF_RED = OFF_META + NI * 16u;
   static constexpr uint32_t OFF_BAR = OFF_RED + 2u * RED_FLOATS * 4u;   // two sums in the epilogue
-  static constexpr int NBAR = 48;
+  static constexpr int NBAR = 58;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
-  static constexpr uint32_t MISC_BYTES = 64u + 2u * 2u * 4u * 4u + 24u * 8u;
+  static constexpr uint32_t MISC_BYTES = 192u;
   static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024u;
   static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
   // TMEM columns: O^T double buffer (2 x 4 HB), S^T double buffer (2 x HB)
@@ -87,8 +97,8 @@ struct Cfg {
 enum {
   B_IDX_FULL = 0,    // [NI]
   B_IDX_EMPTY = 4,   // [NI]
-  B_Q_FULL = 8,      // [2]
-  B_Q_EMPTY = 10,    // [2]
+  B_Q_FULL = 8,
+  B_Q_EMPTY = 10,
   B_S_FULL = 12,     // [2]
   B_S_EMPTY = 14,    // [2]
   B_P_FULL = 16,
@@ -96,11 +106,10 @@ enum {
   B_O_FULL = 18,     // [2]
   B_O_EMPTY = 20,    // [2]
   B_SMX = 22,        // [2] one per softmax warpgroup
-  B_DRAIN = 24,      // [3]
-  B_U_FULL = 28,     // [NU]
-  B_U_EMPTY = 34,    // [NU]
-  B_R_FULL = 40,
-  B_R_EMPTY = 41,
+  B_PLAN = 9,
+  B_DRAIN = 24,      // [2] one per MMA issuer
+  B_FULL = 26,       // [16] K slots from 0, V slots from 8
+  B_EMPTY = 42,      // [16]
 };
 
 // flags of a tile
@@ -108,6 +117,7 @@ constexpr int F_FIRST = 1;    // first tile of its request in this range
 constexpr int F_LAST = 2;     // last one
 constexpr int F_PART = 4;     // the request is cut: store a partial result
 constexpr int F_SLOT1 = 8;    // ... into the range's second slot (it did not begin the range)
+constexpr int F_BOX = 16;     // every key there, in runs of box_rows rows: loaded by boxes
 
 // key tiles of a request
 __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
@@ -116,6 +126,124 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
   const int64_t cap = (int64_t)a.max_blocks * a.block_size;
   const uint32_t n = len < cap ? (uint32_t)len : (uint32_t)cap;
   return (int)((n + BK - 1) / BK);
+}
+
+// Bounded waits, kept small: a launch runs its code cold, and every line of it
+// that is not needed costs several hundred cycles of instruction fetch.
+// POLL: a suspended try_wait wakes about 400 cycles after its phase completes;
+// the waits on a tile's way through the CTA poll instead, the others sleep.
+__device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* err) {
+  if (*abort_flag == 0) atomicAdd(err + ERR_TIMEOUT, 1u);
+  *abort_flag = 1;
+}
+template <bool POLL>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  while (true) {
+    uint32_t ok;
+    if constexpr (POLL)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+      ok = mbar_try_wait_sleep(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitTimeoutNs) {
+      give_up(abort_flag, err);
+      return false;
+    }
+  }
+}
+
+// TMA loads of cache rows that mark their lines first to go from L2: the cache
+// is read once and larger than L2, and would otherwise push out the kernel's
+// own code and tables.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void gather4_hint(uint32_t dst, const CUtensorMap* map, int x, const int4& r, uint64_t* bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Tensor-core issue by one elected lane of a converged warp: the loops around
+// it are warp-uniform, so descriptors and loop state stay in uniform registers
+// (issued from inside a one-lane branch, every operand is first moved there,
+// about 120 cycles per MMA instead of 45).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_x4_elected(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t da,
+                                               uint32_t db, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %11, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, 1;\n\t}"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "l"(a + da), "l"(b + db), "l"(a + 2ull * da),
+      "l"(b + 2ull * db), "l"(a + 3ull * da), "l"(b + 3ull * db), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+
+// The row of a page's at-th position, or -1 (counted).
+__device__ __forceinline__ int32_t row_at(const DecodeArgs& a, const int32_t* bt, uint32_t page, uint32_t at, int& bad) {
+  const int32_t blk = __ldg(bt + page);
+  const int64_t x = (int64_t)blk * a.block_size + at;
+  if (blk >= 0 && x < a.N) return (int32_t)x;
+  ++bad;
+  return -1;
+}
+
+// First tile of range g of ng ranges over total tiles: floor(g * total / ng).
+__device__ __forceinline__ uint32_t range_begin(uint32_t g, uint32_t total, uint32_t ng) {
+  if (total < (1u << 24)) return g * total / ng;   // (g <= 152)
+  return (uint32_t)((uint64_t)g * total / ng);
+}
+// The range that holds tile t.
+__device__ __forceinline__ uint32_t range_of(uint32_t t, uint32_t total, uint32_t ng) {
+  if (total < (1u << 24)) return ((t + 1) * ng - 1) / total;
+  return (uint32_t)(((uint64_t)(t + 1) * ng - 1) / total);
+}
+
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane_id() >= o) v += up;
+  }
+  return v;
 }
 
 template <int N, bool IS_MAX>
@@ -176,7 +304,6 @@ template <int HB, int NC>
 __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<HB, NC>;
   constexpr int HT = C::HT;
-  constexpr bool ROPE = (NC == 9);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
@@ -186,46 +313,46 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* tmem_base_ptr = misc + 0;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  int* sched = reinterpret_cast<int*>(misc + 2);                    // first request, its first tile here
+  int* plan = reinterpret_cast<int*>(misc + 2);                     // tiles here, first request, its first tile, its length
   volatile uint32_t* votes = misc + 16;                             // [parity][warpgroup][warp]
-  int64_t* scan = reinterpret_cast<int64_t*>(misc + 32);            // [24] per-warp tile counts
+  uint32_t* scan = misc + 32;                                       // [16] per-warp tile counts
   int32_t* rows = reinterpret_cast<int32_t*>(smem + C::OFF_ROWS);   // [NI][BK], -1 = masked
   int4* meta = reinterpret_cast<int4*>(smem + C::OFF_META);         // [NI] request, flags
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
   unsigned int* err = a.err;
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto poll = [&](int i, uint32_t parity) { return wait<true>(bar(i), parity, abort_flag, err); };
+  auto doze = [&](int i, uint32_t parity) { return wait<false>(bar(i), parity, abort_flag, err); };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int group = blockIdx.x / a.head_blocks;
-  const int hb = blockIdx.x - group * a.head_blocks;
-
-  // the joining kernel may be put on the GPU as soon as there is room
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int range = blockIdx.x / a.head_blocks;   // the CTA group
+  const int hb = blockIdx.x - range * a.head_blocks;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NI; ++i) {
       mbar_init(&bars[B_IDX_FULL + i], 1);
-      // 3 MMA warps, 2 softmax warpgroups, the unit producers, the RoPE producer
-      mbar_init(&bars[B_IDX_EMPTY + i], 3 + 2 + 2 * NU + (ROPE ? 1 : 0));
+      // 2 MMA warps, 2 softmax warpgroups, the producer warps, the q loader
+      mbar_init(&bars[B_IDX_EMPTY + i], 2 + 2 + NPROD + 1);
     }
+    mbar_init(&bars[B_Q_FULL], 1);
+    mbar_init(&bars[B_Q_EMPTY], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[B_Q_FULL + i], 1);
-      mbar_init(&bars[B_Q_EMPTY + i], 1);
       mbar_init(&bars[B_S_FULL + i], 1);
       mbar_init(&bars[B_S_EMPTY + i], 256);
-      mbar_init(&bars[B_O_FULL + i], 2);    // one commit per PV issuer
+      mbar_init(&bars[B_O_FULL + i], 1);
       mbar_init(&bars[B_O_EMPTY + i], 256);
       mbar_init(&bars[B_SMX + i], 128);
+      mbar_init(&bars[B_DRAIN + i], 1);
     }
+    mbar_init(&bars[B_PLAN], 1);
     mbar_init(&bars[B_P_FULL], 256);
-    mbar_init(&bars[B_P_EMPTY], 2);
-    for (int i = 0; i < 3; ++i) mbar_init(&bars[B_DRAIN + i], 1);
-    for (int i = 0; i < NU; ++i) {
-      mbar_init(&bars[B_U_FULL + i], 1);
-      mbar_init(&bars[B_U_EMPTY + i], 1);
+    mbar_init(&bars[B_P_EMPTY], 1);
+    for (int i = 0; i < 16; ++i) {
+      mbar_init(&bars[B_FULL + i], 1);
+      mbar_init(&bars[B_EMPTY + i], 1);
     }
-    mbar_init(&bars[B_R_FULL], 1);
-    mbar_init(&bars[B_R_EMPTY], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -233,71 +360,77 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     tmem_alloc(const_cast<uint32_t*>(tmem_base_ptr), C::TMEM_COLS);
     tmem_relinquish();
   }
-  // ---- this group's range of tiles: every thread counts the tiles of a run of
-  // requests, a block scan places the runs, and the run that holds the range's
-  // first tile names it
-  const int per = (a.B + NTHREADS - 1) / NTHREADS;
-  const int b_lo = min(a.B, (int)threadIdx.x * per), b_hi = min(a.B, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(a, __ldg(a.kv_lens + b));
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < NTHREADS / 32; ++w) {
-    const int64_t n = scan[w];
-    if (w < warp) before += n;
-    total += n;
-  }
-  const int64_t ng = total < a.groups ? total : a.groups;   // no group without a tile
-  const int64_t x0 = group < ng ? group * total / ng : 0;
-  const int64_t x1 = group < ng ? (group + 1) * total / ng : 0;
-  const int nt = (int)(x1 - x0);
-  if (nt > 0 && before <= x0 && x0 < before + mine) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int n = tiles_of(a, __ldg(a.kv_lens + b));
-      if (x0 < at + n) {
-        sched[0] = b;
-        sched[1] = (int)(x0 - at);
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
   const uint32_t tmem = *tmem_base_ptr;
   const int head0 = hb * HB;                                   // this CTA's first head
   const int heads = a.H - head0 < HB ? a.H - head0 : HB;       // the others are padding, never stored
   const int64_t heads_padded = (int64_t)a.head_blocks * HB;
 
+  // the joining kernel may be put on the GPU as soon as there is room
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   if (warp >= 8) {
     regs_dec<REGS_REST>();
+    // what earlier kernels wrote may be read from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // ---- this group's range of tiles: every thread counts the tiles of a run
+    // of requests, a scan over the sixteen warps places the runs, and the run
+    // that holds the range's first tile names it
+    const int tid = threadIdx.x - 256;
+    const int per = (a.B + 511) / 512;
+    const int b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
+    uint32_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(a, __ldg(a.kv_lens + b));
+    uint32_t incl = warp_scan(mine);
+    if (lane == 31) scan[warp - 8] = incl;
+    named_bar_sync(1, 512);
+    const uint32_t all = warp_scan(lane < 16 ? scan[lane] : 0u);
+    const uint32_t total = __shfl_sync(0xffffffffu, all, 15);
+    const uint32_t ahead = __shfl_sync(0xffffffffu, all, (warp - 9) & 31);
+    const uint32_t before = (warp > 8 ? ahead : 0u) + incl - mine;
+    const uint32_t ng = total < (uint32_t)a.groups ? total : (uint32_t)a.groups;   // no group without a tile
+    const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
+    const uint32_t x1 = (uint32_t)range < ng ? range_begin(range + 1, total, ng) : 0;
+    if (tid == 0) {
+      plan[0] = (int)(x1 - x0);
+      if (range == 0 && hb == 0) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
+    }
+    if (x1 > x0 && before <= x0 && x0 < before + mine) {
+      uint32_t at = before;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const int len = __ldg(a.kv_lens + b);
+        const uint32_t n = tiles_of(a, len);
+        if (x0 < at + n) {
+          plan[1] = b;
+          plan[2] = (int)(x0 - at);
+          plan[3] = len;
+          break;
+        }
+        at += n;
+      }
+    }
+    named_bar_sync(1, 512);
+    if (tid == 0) mbar_arrive(&bars[B_PLAN]);
+    const int nt = plan[0];
     if (warp == 11) {
       // ------------------------------------------------------------------
       // scheduler
       // ------------------------------------------------------------------
-      bool ok = true;
       int bad = 0;
-      int b = nt > 0 ? sched[0] : 0, j = nt > 0 ? sched[1] : 0;
-      int len = 0, n = 0;
-      bool enter = true;              // the next tile is the first of request b here
+      int b = nt > 0 ? plan[1] : 0, j = nt > 0 ? plan[2] : 0;
+      int len = nt > 0 ? plan[3] : 0, n = 0;
+      const bool from_start = j == 0;   // the range's first request begins in it
+      bool enter = true;                // the next tile is the first of request b here
       int seg = 0;                    // requests begun
-      int nq = 0;                     // q loads issued
       const int64_t cap = (int64_t)a.max_blocks * a.block_size;
       for (int it = 0; it < nt; ++it) {
         const int r = it % NI;
         if (enter) {
           // (requests without keys have no tile)
           while (true) {
-            len = __ldg(a.kv_lens + b);
+            if (it > 0) len = __ldg(a.kv_lens + b);
             n = tiles_of(a, len);
             if (n > 0) break;
             ++b;
@@ -307,63 +440,51 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
             len = (int)cap;
           }
         }
-        if (!mbar_wait_warp(&bars[B_IDX_EMPTY + r], ((it / NI) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
+        if (!doze(B_IDX_EMPTY + r, ((it / NI) & 1) ^ 1)) break;
         const int32_t* bt = a.block_table + (int64_t)b * a.max_blocks;
         int32_t row[4];
-        int32_t pos[4];
         const int e0 = j * BK + 4 * lane;   // (as unsigned: the last tile may end past 2^31)
+        if (a.idx == nullptr) {
+          uint32_t page = (uint32_t)e0 / (uint32_t)a.block_size, at = (uint32_t)e0 - page * (uint32_t)a.block_size;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a.idx != nullptr) {
-            pos[e] = (e0 + e < a.k) ? __ldg(a.idx + (int64_t)b * a.ld + e0 + e) : -1;
-            if (pos[e] < -1 || pos[e] >= len) {
-              ++bad;
-              pos[e] = -1;
-            }
-          } else {
-            const uint32_t p = (uint32_t)e0 + e;
-            pos[e] = p < (uint32_t)len ? (int32_t)p : -1;
+          for (int e = 0; e < 4; ++e) {
+            const bool there = (uint32_t)e0 + e < (uint32_t)len;
+            row[e] = -1;
+            if (there) row[e] = row_at(a, bt, page, at, bad);
+            if (++at == (uint32_t)a.block_size) { at = 0; ++page; }
           }
-        }
+        } else {
+          int32_t pos[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          row[e] = -1;
-          if (pos[e] >= 0) {
-            const int32_t page = pos[e] / a.block_size;
-            const int32_t blk = __ldg(bt + page);
-            const int64_t x = (int64_t)blk * a.block_size + (pos[e] - page * a.block_size);
-            if (blk < 0 || x >= a.N)
+          for (int e = 0; e < 4; ++e) pos[e] = (e0 + e < a.k) ? __ldg(a.idx + (int64_t)b * a.ld + e0 + e) : -1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            row[e] = -1;
+            if (pos[e] >= 0 && pos[e] < len) {
+              const uint32_t page = (uint32_t)pos[e] / (uint32_t)a.block_size;
+              row[e] = row_at(a, bt, page, (uint32_t)pos[e] - page * (uint32_t)a.block_size, bad);
+            } else if (pos[e] != -1) {
               ++bad;
-            else
-              row[e] = (int32_t)x;
+            }
           }
         }
         *reinterpret_cast<int4*>(rows + r * BK + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
+        const bool box = __all_sync(0xffffffffu, (row[0] | row[1] | row[2] | row[3]) >= 0) && a.box_rows > 0;
         const bool first = enter;
         const bool last = (it == nt - 1) || (j == n - 1);
         if (lane == 0) {
-          int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0);
+          int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (box ? F_BOX : 0);
           if (last) {
             // (the range's first request may have begun before it, its last may go on behind it)
-            const bool whole = (seg > 0 || sched[1] == 0) && j == n - 1;
+            const bool whole = (seg > 0 || from_start) && j == n - 1;
             if (!whole) flags |= F_PART | (seg > 0 ? F_SLOT1 : 0);
           }
           meta[r] = make_int4(b, flags, 0, 0);
+          // where the range ends, for the join: the request, its tile count, and its tiles so far
+          if (it == nt - 1 && hb == 0) a.borders[1 + range] = make_int4(b, n, j + 1, 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IDX_FULL + r]);
-        if (first) {
-          // q of request b: rows b*H + head0 ... of q viewed [B*H, D_QK], one box per swizzle column
-          const int qb = nq % C::NQ;
-          if (!mbar_wait_warp(&bars[B_Q_EMPTY + qb], ((nq / C::NQ) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars[B_Q_FULL + qb], C::Q_BYTES);
-            for (int c = 0; c < NC; ++c)
-              tma_load_2d(sbase + C::OFF_Q + qb * C::Q_BYTES + c * (HB * 128), &a.tmap_q, c * 64, b * a.H + head0,
-                          &bars[B_Q_FULL + qb]);
-          }
-          ++nq;
-        }
         enter = (j == n - 1);
         if (enter) {
           ++b;
@@ -373,67 +494,95 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
           ++j;
         }
       }
-      (void)ok;
       bad = __reduce_add_sync(0xffffffffu, bad);
-      if (lane == 0) {
-        if (bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
-        // let q copies in flight land before the CTA can exit
-        for (int p = nq - 1; p >= 0 && p > nq - 1 - C::NQ; --p)
-          mbar_wait_drain(&bars[B_Q_FULL + p % C::NQ], (uint32_t)(p / C::NQ) & 1, err);
-      }
-      __syncwarp();
-    } else if (warp >= 12 && warp < 12 + 2 * NU) {
+      if (lane == 0 && bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
+    } else if (warp >= 12) {
       // ------------------------------------------------------------------
-      // unit producers: warps 12 + 2s and 13 + 2s fill unit slot s, one
-      // 64-column chunk of it each (lane l: rows 4l .. 4l+3)
+      // row loads.  A warp issues row gathers one after another (about 80 cycles
+      // each), so they are dealt out: warp 12 + s owns K slot s and loads its
+      // chunks (a lane per 4 rows), the other warps share every V unit's 64.
+      // Where the keys lie in runs of box_rows rows a chunk is 128 / box_rows
+      // boxes instead, loaded by the slot's own warp.  A wait on parity cannot
+      // tell a phase from the one two before it, so a warp passes every phase
+      // of the slots it uses.
       // ------------------------------------------------------------------
-      const int slot = (warp - 12) >> 1, hf = (warp - 12) & 1;
-      const uint32_t dst = sbase + C::OFF_U + slot * C::UNIT_BYTES + hf * C::CHUNK_BYTES + lane * 512;
-      int64_t armed = -1;
+      const bool ks = warp < 12 + C::NK;
+      const int pw = ks ? warp - 12 : warp - 12 - C::NK;
+      const int nslots = ks ? C::NK : C::NV, stages = ks ? NC : 4, chunks = ks ? 1 : 2;
+      const uint32_t ring = sbase + (ks ? C::OFF_K : C::OFF_V), bytes = chunks * C::CHUNK_BYTES;
+      const int e = ks ? lane : pw * C::VL + lane;          // this lane's gather
+      const bool gathers = ks || (lane < C::VL && e < 64);
+      const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
+      const int bi = lane % boxes, bc = lane / boxes;       // this lane's box
+      const uint64_t policy = evict_first_policy();
+      const int b0 = ks ? 0 : 8;
+      int slot = 0;
+      uint32_t phase = 1, armed = 0;   // armed: 2 + the parity of the last phase this warp opened
       bool ok = true;
+#pragma unroll 1
       for (int it = 0; it < nt && ok; ++it) {
         const int r = it % NI;
-        if (!mbar_wait_warp(&bars[B_IDX_FULL + r], (it / NI) & 1, abort_flag, err)) break;
-        const int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
-        for (int m = 0; m < 4; ++m) {
-          const int64_t pos = 4ll * it + m;
-          if ((int)(pos % NU) != slot) continue;
-          if (!mbar_wait_warp(&bars[B_U_EMPTY + slot], ((uint32_t)(pos / NU) & 1) ^ 1, abort_flag, err)) {
-            ok = false;
-            break;
+        if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+        const bool box = (meta[r].y & F_BOX) != 0;
+        int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * (e & 31));
+        if (box) x.x = rows[r * BK + bi * a.box_rows];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+        const uint32_t within = box ? bc * C::CHUNK_BYTES + bi * a.box_rows * 128 : ((e >> 5) & 1) * C::CHUNK_BYTES + (e & 31) * 512;
+        int col = (box ? bc : (e >> 5) & 1) * 64;
+#pragma unroll 1
+        for (int st = 0; st < stages; ++st) {
+          if (!ks || slot == pw) {
+            if (!doze(B_EMPTY + b0 + slot, phase)) { ok = false; break; }
+            const bool lead = slot == pw;   // opens the slot's phases, and loads its boxes
+            uint64_t* full = &bars[B_FULL + b0 + slot];
+            if (lead && lane == 0) {
+              mbar_arrive_expect_tx(full, bytes);
+              if (ks && st == 0) DSA_TRACE(a.tr, it, 1);
+              if (ks && st == NC - 1) DSA_TRACE(a.tr, it, 2);
+            }
+            if (lead) armed = 2u | (phase ^ 1u);
+            const uint32_t dst = ring + slot * bytes + within;
+            if (box) {
+              if (lead && bc < chunks) load_2d_hint(dst, &a.tmap_box, col, x.x, full, policy);
+            } else if (gathers) {
+              gather4_hint(dst, &a.tmap_kv, col, x, full, policy);
+            }
           }
-          if (lane == 0 && hf == 0) mbar_arrive_expect_tx(&bars[B_U_FULL + slot], C::UNIT_BYTES);
-          tma_gather4(dst, &a.tmap_kv, (2 * m + hf) * 64, x.x, x.y, x.z, x.w, &bars[B_U_FULL + slot]);
-          armed = pos;
+          col += 64 * chunks;
+          if (++slot == nslots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
       }
-      // let copies in flight land before the CTA can exit
-      if (lane == 0 && hf == 0 && armed >= 0)
-        mbar_wait_drain(&bars[B_U_FULL + slot], (uint32_t)(armed / NU) & 1, err);
+      // let the slot's last copies land before the CTA can exit
+      if (lane == 0 && armed) mbar_wait_drain(&bars[B_FULL + b0 + pw], armed & 1u, err);
       __syncwarp();
-    } else if (warp == 22) {
-      if constexpr (ROPE) {
-        int armed = -1;
-        for (int it = 0; it < nt; ++it) {
-          const int r = it % NI;
-          if (!mbar_wait_warp(&bars[B_IDX_FULL + r], (it / NI) & 1, abort_flag, err)) break;
-          const int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
-          if (!mbar_wait_warp(&bars[B_R_EMPTY], (it & 1) ^ 1, abort_flag, err)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bars[B_R_FULL], C::CHUNK_BYTES);
-          __syncwarp();
-          tma_gather4(sbase + C::OFF_R + lane * 512, &a.tmap_kv, 512, x.x, x.y, x.z, x.w, &bars[B_R_FULL]);
-          armed = it;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
-        }
-        if (lane == 0 && armed >= 0) mbar_wait_drain(&bars[B_R_FULL], armed & 1, err);
+    } else if (warp == 10) {
+      // ------------------------------------------------------------------
+      // q of every request of the range, one box per swizzle column (rows b*H +
+      // head0 ... of q viewed [B*H, D_QK]); then the requests without keys
+      // ------------------------------------------------------------------
+      int nq = 0;
+      for (int it = 0; it < nt; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+        const int4 mt = meta[r];
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+        if (!(mt.y & F_FIRST)) continue;
+        if (!doze(B_Q_EMPTY, (nq & 1) ^ 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars[B_Q_FULL], C::Q_BYTES);
+        __syncwarp();
+        if (lane < NC)
+          tma_load_2d(sbase + C::OFF_Q + lane * (HB * 128), &a.tmap_q, lane * 64, mt.x * a.H + head0, &bars[B_Q_FULL]);
+        ++nq;
       }
-    } else if (warp == 23) {
+      if (lane == 0 && nq > 0) mbar_wait_drain(&bars[B_Q_FULL], (nq - 1) & 1, err);
+      __syncwarp();
       // requests without keys: out = 0, lse = -inf (dealt over the groups)
-      for (int b = group; b < a.B; b += a.groups) {
+      for (int b = range; b < a.B; b += a.groups) {
         if (tiles_of(a, __ldg(a.kv_lens + b)) > 0) continue;
         uint4* o = reinterpret_cast<uint4*>(a.out + ((int64_t)b * a.H + head0) * 512);
         for (int i = lane; i < heads * 64; i += 32) o[i] = make_uint4(0, 0, 0, 0);
@@ -441,96 +590,86 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       }
     } else if (warp == 8) {
       // ------------------------------------------------------------------
-      // QK issuer (one thread): the RoPE chunk, then the units as they land
+      // QK issuer: the chunks as they land
       // ------------------------------------------------------------------
-      if (lane == 0) {
-        constexpr uint32_t IDESC = idesc_bf16_f32(128, HB, false, false);
-        int nq = -1;
-        uint32_t qs = 0;
-        bool ok = true;
-        for (int it = 0; it < nt && ok; ++it) {
-          const int r = it % NI;
-          if (!mbar_wait(&bars[B_IDX_FULL + r], (it / NI) & 1, abort_flag, err)) break;
-          const int flags = meta[r].y;
-          mbar_arrive(&bars[B_IDX_EMPTY + r]);
-          if (flags & F_FIRST) {
-            ++nq;
-            const int qb = nq % C::NQ;
-            if (!mbar_wait(&bars[B_Q_FULL + qb], (nq / C::NQ) & 1, abort_flag, err)) break;
-            qs = sbase + C::OFF_Q + qb * C::Q_BYTES;
-          }
-          const int sb = it & 1;
-          const uint32_t d_s = tmem + C::COL_S + sb * HB;
-          if (!mbar_wait(&bars[B_S_EMPTY + sb], ((it >> 1) & 1) ^ 1, abort_flag, err)) break;
-          if constexpr (ROPE) {
-            if (!mbar_wait(&bars[B_R_FULL], it & 1, abort_flag, err)) break;
-            tc_fence_after();
-            mma_bf16_ss_x4(d_s, sdesc_sw128(sbase + C::OFF_R, 16, 1024), sdesc_sw128(qs + 8 * (HB * 128), 16, 1024),
-                           2u, 2u, IDESC, 0u);
-            mma_commit(&bars[B_R_EMPTY]);
-          }
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t pos = 4u * it + m, slot = pos % NU;
-            if (!mbar_wait(&bars[B_U_FULL + slot], (pos / NU) & 1, abort_flag, err)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t u = sbase + C::OFF_U + slot * C::UNIT_BYTES;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              mma_bf16_ss_x4(d_s, sdesc_sw128(u + hf * C::CHUNK_BYTES, 16, 1024),
-                             sdesc_sw128(qs + (2 * m + hf) * (HB * 128), 16, 1024), 2u, 2u, IDESC,
-                             (ROPE || m > 0 || hf > 0) ? 1u : 0u);
-          }
-          if (!ok) break;
-          mma_commit(&bars[B_S_FULL + sb]);
-          if (flags & F_LAST) mma_commit(&bars[B_Q_EMPTY + nq % C::NQ]);
+      constexpr uint32_t IDESC = idesc_bf16_f32(128, HB, false, false);
+      const uint32_t leader = elect_one();
+      const uint64_t k_desc = sdesc_sw128(sbase + C::OFF_K, 16, 1024), q_desc = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
+      int nq = -1;
+      uint32_t slot = 0, phase = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it < nt && ok; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+        const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
+        if (leader) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+        if (flags & F_FIRST) {
+          ++nq;
+          if (!poll(B_Q_FULL, nq & 1)) break;
         }
-        // every MMA issued above has completed
-        mma_commit(&bars[B_DRAIN + 0]);
-        mbar_wait_drain(&bars[B_DRAIN + 0], 0, err);
+        const int sb = it & 1;
+        if (!poll(B_S_EMPTY + sb, ((it >> 1) & 1) ^ 1)) break;
+#pragma unroll 1
+        for (int c = 0; c < NC; ++c) {
+          if (!poll(B_FULL + slot, phase)) { ok = false; break; }
+          tc_fence_after();
+          if (leader && c == 0) DSA_TRACE(a.tr, it, 3);
+          if (leader && c == NC - 1) DSA_TRACE(a.tr, it, 4);
+          mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)(slot * (C::CHUNK_BYTES >> 4)),
+                         q_desc + (uint64_t)(c * (HB * 128 >> 4)), 2u, 2u, IDESC, c > 0 ? 1u : 0u);
+          commit_elected(leader, &bars[B_EMPTY + slot]);
+          if (++slot == C::NK) { slot = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        commit_elected(leader, &bars[B_S_FULL + sb]);
+        if (flags & F_LAST) commit_elected(leader, &bars[B_Q_EMPTY]);
       }
+      // every MMA issued above has completed
+      commit_elected(leader, &bars[B_DRAIN + 0]);
+      if (leader) mbar_wait_drain(&bars[B_DRAIN + 0], 0, err);
       __syncwarp();
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == 9) {
       // ------------------------------------------------------------------
-      // PV issuers (one thread each): units 0, 2 and 1, 3 of every tile
+      // PV issuer: the units in order
       // ------------------------------------------------------------------
-      const int pvi = warp - 9;
-      if (lane == 0) {
-        constexpr uint32_t IDESC = idesc_bf16_f32(128, HB, true, false);
-        const uint32_t p_s = sbase + C::OFF_P;
-        int seg = -1;
-        bool ok = true;
-        for (int it = 0; it < nt && ok; ++it) {
-          const int r = it % NI;
-          if (!mbar_wait(&bars[B_IDX_FULL + r], (it / NI) & 1, abort_flag, err)) break;
-          const int flags = meta[r].y;
-          mbar_arrive(&bars[B_IDX_EMPTY + r]);
-          if (flags & F_FIRST) ++seg;
-          const int ob = seg & 1;
-          if (!mbar_wait(&bars[B_P_FULL], it & 1, abort_flag, err)) break;
-          if (flags & F_FIRST) {
-            if (!mbar_wait(&bars[B_O_EMPTY + ob], ((seg >> 1) & 1) ^ 1, abort_flag, err)) break;
-          }
-          for (int m = pvi; m < 4; m += 2) {
-            const uint32_t pos = 4u * it + m, slot = pos % NU;
-            // (landed before QK read it; the wait orders this thread's MMAs after the copy)
-            if (!mbar_wait(&bars[B_U_FULL + slot], (pos / NU) & 1, abort_flag, err)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t u = sbase + C::OFF_U + slot * C::UNIT_BYTES;
-            const uint32_t d_o = tmem + ob * (4 * HB) + m * HB;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              mma_bf16_ss_x4(d_o, sdesc_sw128(u + hf * 4 * 2048, C::CHUNK_BYTES, 1024),
-                             sdesc_sw128(p_s + hf * (HB * 128), 16, 1024), 128u, 2u, IDESC,
-                             (!(flags & F_FIRST) || hf > 0) ? 1u : 0u);
-            mma_commit(&bars[B_U_EMPTY + slot]);
-          }
-          if (!ok) break;
-          mma_commit(&bars[B_P_EMPTY]);
-          if (flags & F_LAST) mma_commit(&bars[B_O_FULL + ob]);
+      constexpr uint32_t IDESC = idesc_bf16_f32(128, HB, true, false);
+      const uint32_t leader = elect_one();
+      const uint64_t v_desc = sdesc_sw128(sbase + C::OFF_V, C::CHUNK_BYTES, 1024), p_desc = sdesc_sw128(sbase + C::OFF_P, 16, 1024);
+      int seg = -1;
+      uint32_t slot = 0, phase = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it < nt && ok; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+        const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
+        if (leader) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+        if (flags & F_FIRST) ++seg;
+        const int ob = seg & 1;
+        if (!poll(B_P_FULL, it & 1)) break;
+        if (leader) DSA_TRACE(a.tr, it, 0);
+        if ((flags & F_FIRST) && !poll(B_O_EMPTY + ob, ((seg >> 1) & 1) ^ 1)) break;
+        const uint32_t acc = (flags & F_FIRST) ? 0u : 1u;
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          if (!poll(B_FULL + 8 + slot, phase)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t v = v_desc + (uint64_t)(slot * (C::UNIT_BYTES >> 4));
+          const uint32_t d_o = tmem + ob * (4 * HB) + m * HB;
+          // 16 keys (2048 bytes of V^T) per MMA; P^T one 64-key swizzle column per half
+          mma_x4_elected(leader, d_o, v, p_desc, 128u, 2u, IDESC, acc);
+          mma_x4_elected(leader, d_o, v + 512u, p_desc + (uint64_t)(HB * 128 >> 4), 128u, 2u, IDESC, 1u);
+          commit_elected(leader, &bars[B_EMPTY + 8 + slot]);
+          if (++slot == C::NV) { slot = 0; phase ^= 1; }
         }
-        mma_commit(&bars[B_DRAIN + 1 + pvi]);
-        mbar_wait_drain(&bars[B_DRAIN + 1 + pvi], 0, err);
+        if (!ok) break;
+        if (leader) DSA_TRACE(a.tr, it, 7);
+        commit_elected(leader, &bars[B_P_EMPTY]);
+        if (flags & F_LAST) commit_elected(leader, &bars[B_O_FULL + ob]);
       }
+      commit_elected(leader, &bars[B_DRAIN + 1]);
+      if (leader) mbar_wait_drain(&bars[B_DRAIN + 1], 0, err);
       __syncwarp();
     }
   } else {
@@ -542,91 +681,113 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     const int wg = warp >> 2, w4 = warp & 3;
     const int key = threadIdx.x & 127;
     const float scale_log2 = a.scale * 1.4426950408889634f;
-    const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
-    uint8_t* p_tile = smem + C::OFF_P;
-    uint64_t* sync_bar = &bars[B_SMX + wg];
+    const uint32_t t_lane = tmem + ((uint32_t)(w4 * 32) << 16) + wg * HT;   // this thread's lane, its heads' columns
+    uint8_t* p_key = smem + C::OFF_P + (key >> 6) * (HB * 128) + wg * HT * 128 + (key & 7) * 2;
     uint32_t sync_phase = 0;
+    auto group = [&]() {   // the warpgroup's barrier
+      mbar_arrive(&bars[B_SMX + wg]);
+      const bool ok = poll(B_SMX + wg, sync_phase);
+      sync_phase ^= 1u;
+      return ok;
+    };
     int seg = -1;
+    // The running max starts at the lowest finite value, not at -inf, so that no
+    // difference of two of them is NaN: a rescale from it gives exactly 0.
     float m_run[HT], l_exact[HT], l_used[HT];
-    for (int it = 0; it < nt; ++it) {
-      const int r = it % NI;
-      if (!mbar_wait_warp(&bars[B_IDX_FULL + r], (it / NI) & 1, abort_flag, err)) break;
-      const bool valid = rows[r * BK + key] >= 0;
-      const int4 mt = meta[r];
+#pragma unroll
+    for (int h = 0; h < HT; ++h) { m_run[h] = -FLT_MAX; l_exact[h] = 0.f; l_used[h] = 0.f; }
+    // Tile -1 is a rehearsal on whatever tensor memory holds, storing nothing
+    // outside this CTA's own scratch: it brings the loop's code in while the
+    // first rows are on their way.
+    int nt = 1;
+#pragma unroll 1
+    for (int it = -1; it < nt; ++it) {
+      const bool dry = it < 0;
+      if (it == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!poll(B_PLAN, 0)) break;
+        nt = plan[0];
+        if (nt == 0) break;
+      }
+      const int r = it & (NI - 1);
+      const int sb = it & 1;
+      bool valid = true;
+      int4 mt = make_int4(0, F_LAST | F_PART, 0, 0);
+      if (!dry) {
+        if (!poll(B_IDX_FULL + r, (it / NI) & 1)) break;
+        valid = rows[r * BK + key] >= 0;
+        mt = meta[r];
+        if (!poll(B_S_FULL + sb, (it >> 1) & 1)) break;
+        if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 5);
+      }
       if (mt.y & F_FIRST) {
         ++seg;
 #pragma unroll
-        for (int h = 0; h < HT; ++h) { m_run[h] = -INFINITY; l_exact[h] = 0.f; l_used[h] = 0.f; }
+        for (int h = 0; h < HT; ++h) { m_run[h] = -FLT_MAX; l_exact[h] = 0.f; l_used[h] = 0.f; }
       }
-      const int ob = seg & 1, sb = it & 1;
-      if (!mbar_wait_warp(&bars[B_S_FULL + sb], (it >> 1) & 1, abort_flag, err)) break;
+      const int ob = seg & 1;
       tc_fence_after();
-      float s[HT];
-      tmem_ld_n<HT>(tmem + lane_off + C::COL_S + sb * HB + wg * HT, s);
+      float s[HT], d[HT];
+      tmem_ld_n<HT>(t_lane + C::COL_S + sb * HB, s);
       tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive(&bars[B_S_EMPTY + sb]);
-      bool mine_need = false;
+      if (!dry) mbar_arrive(&bars[B_S_EMPTY + sb]);
+      float top = -FLT_MAX;
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
-        s[h] = valid ? s[h] * scale_log2 : -INFINITY;
-        mine_need |= (s[h] > m_run[h] + kTau);
+        d[h] = s[h] * scale_log2 - m_run[h];
+        top = fmaxf(top, d[h]);
       }
       // Lazy rescale: a warp with a score above the running max by more than
       // kTau publishes its per-head max; the new reference is the max over
       // those warps, which bounds every score of the tile to within 2^kTau.
-      const bool wneed = __any_sync(0xffffffffu, mine_need);
-      float* redb = red + ((it & 1) * 2 + wg) * (4 * HT);
-      volatile uint32_t* vote = votes + ((it & 1) * 2 + wg) * 4;
+      // (A masked key's row is zeros, its score 0: it never asks.)
+      const bool wneed = dry || __any_sync(0xffffffffu, valid && top > kTau);
+      float* redb = red + (sb * 2 + wg) * (4 * HT);
+      volatile uint32_t* vote = votes + (sb * 2 + wg) * 4;
       if (wneed) {
         float x[HT];
 #pragma unroll
-        for (int h = 0; h < HT; ++h) x[h] = s[h];
+        for (int h = 0; h < HT; ++h) x[h] = valid ? s[h] * scale_log2 : -FLT_MAX;
         const float wmax = warp_transpose_reduce<HT, true>(x);
         if (lane < HT) redb[w4 * HT + lane] = wmax;
       }
       if (lane == 0) vote[w4] = wneed ? 1u : 0u;
-      if (!__all_sync(0xffffffffu, group_sync(sync_bar, sync_phase, abort_flag, err))) break;
-      if (key == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);   // (every thread of the warpgroup has read the tile's rows)
-      uint32_t vw[4];
-      bool need = false;
+      if (!group()) break;
+      if (key == 0 && !dry) mbar_arrive(&bars[B_IDX_EMPTY + r]);   // (every thread of the warpgroup has read the tile's rows)
+      uint32_t need = 0;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        vw[w] = vote[w];
-        need |= vw[w] != 0;
-      }
-      float alpha[HT];
+      for (int w = 0; w < 4; ++w) need |= vote[w] << w;
       if (need) {
-        float tmax[HT];
+        // (the old reference takes part as the warps that did not vote)
 #pragma unroll
-        for (int h = 0; h < HT; ++h) tmax[h] = m_run[h];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (vw[w]) {
-#pragma unroll
-            for (int h = 0; h < HT; h += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(redb + w * HT + h);
-              tmax[h + 0] = fmaxf(tmax[h + 0], x.x);
-              tmax[h + 1] = fmaxf(tmax[h + 1], x.y);
-              tmax[h + 2] = fmaxf(tmax[h + 2], x.z);
-              tmax[h + 3] = fmaxf(tmax[h + 3], x.w);
+        for (int h = 0; h < HT; h += 4) {
+          float mn[4] = {m_run[h], m_run[h + 1], m_run[h + 2], m_run[h + 3]};
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(redb + w * HT + h);
+            if (need >> w & 1) {
+              mn[0] = fmaxf(mn[0], x.x);
+              mn[1] = fmaxf(mn[1], x.y);
+              mn[2] = fmaxf(mn[2], x.z);
+              mn[3] = fmaxf(mn[3], x.w);
             }
           }
-        }
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          alpha[h] = (m_run[h] == -INFINITY) ? 0.f : exp2f(m_run[h] - tmax[h]);
-          m_run[h] = tmax[h];
-          l_exact[h] *= alpha[h];
-          l_used[h] *= alpha[h];
+          for (int i = 0; i < 4; ++i) {
+            const float alpha = exp2f(m_run[h + i] - mn[i]);
+            m_run[h + i] = mn[i];
+            l_exact[h + i] *= alpha;
+            l_used[h + i] *= alpha;
+            d[h + i] = s[h + i] * scale_log2 - mn[i];
+            s[h + i] = alpha;
+          }
         }
       }
       uint32_t pk[HT / 2];
 #pragma unroll
       for (int h = 0; h < HT; h += 2) {
-        const float m0 = (m_run[h] == -INFINITY) ? 0.f : m_run[h];
-        const float m1 = (m_run[h + 1] == -INFINITY) ? 0.f : m_run[h + 1];
-        const float p0 = exp2f(s[h] - m0), p1 = exp2f(s[h + 1] - m1);
+        const float p0 = valid ? exp2f(d[h]) : 0.f, p1 = valid ? exp2f(d[h + 1]) : 0.f;
         const uint32_t w = pack_bf16x2(p0, p1);
         l_exact[h] += p0;
         l_exact[h + 1] += p1;
@@ -635,87 +796,92 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         pk[h / 2] = w;
       }
       // the previous P.V must be done before P is overwritten or O rescaled
-      if (!mbar_wait_warp(&bars[B_P_EMPTY], (it & 1) ^ 1, abort_flag, err)) break;
+      if (!dry && !poll(B_P_EMPTY, sb ^ 1)) break;
       tc_fence_after();
       if (need && !(mt.y & F_FIRST)) {
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
           float o[HT];
-          const uint32_t ta = tmem + lane_off + ob * (4 * HB) + m * HB + wg * HT;
+          const uint32_t ta = t_lane + ob * (4 * HB) + m * HB;
           tmem_ld_n<HT>(ta, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < HT; ++h) o[h] *= alpha[h];
+          for (int h = 0; h < HT; ++h) o[h] *= s[h];
           tmem_st_n<HT>(ta, o);
         }
         tmem_st_wait();
       }
-      {
-        // P^T[h][key] (K-major swizzled, two columns of 64 keys)
-        const uint32_t kcol = key & 63;
-        uint8_t* pcol = p_tile + (key >> 6) * (HB * 128);
+      // P^T[h][key], K-major swizzled, two columns of 64 keys: row h at h * 128,
+      // 16-byte piece c at (c ^ (h & 7)) * 16
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
-          *reinterpret_cast<uint16_t*>(pcol + sw128_offset(wg * HT + h, kcol)) =
-              (uint16_t)((h & 1) ? (pk[h / 2] >> 16) : (pk[h / 2] & 0xffffu));
-      }
+      for (int h = 0; h < HT; ++h)
+        *reinterpret_cast<uint16_t*>(p_key + h * 128 + ((((key & 63) >> 3) ^ (h & 7)) << 4)) =
+            (uint16_t)((h & 1) ? (pk[h / 2] >> 16) : (pk[h / 2] & 0xffffu));
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&bars[B_P_FULL]);
+      if (!dry) mbar_arrive(&bars[B_P_FULL]);
+      if (threadIdx.x == 0 && !dry) DSA_TRACE(a.tr, it, 6);
       if (!(mt.y & F_LAST)) continue;
 
-      // ---- epilogue of the request's part in this range
+      // ---- epilogue of the request's part in this range: the warps' sums, then
+      // a lane per head for what the outputs are divided by and the log-sum-exp
+      // (in the reduction scratch of the other parity: its last readers passed
+      // the barrier above)
       const float ex = warp_transpose_reduce<HT, false>(l_exact);
       const float us = warp_transpose_reduce<HT, false>(l_used);
-      // (the reduction scratch of the other parity: its last readers passed the group sync above)
-      float* redx = red + (((it + 1) & 1) * 2 + wg) * (4 * HT);
+      float* redx = red + ((sb ^ 1) * 2 + wg) * (4 * HT);
       float* redu = redx + C::RED_FLOATS;
+      // the running max is the same in every thread: lane h keeps head h's
+      float mine = 0.f;
+#pragma unroll
+      for (int h = 0; h < HT; ++h) mine = lane == h ? m_run[h] : mine;
       if (lane < HT) {
         redx[w4 * HT + lane] = ex;
         redu[w4 * HT + lane] = us;
       }
-      if (!__all_sync(0xffffffffu, group_sync(sync_bar, sync_phase, abort_flag, err))) break;
-      float inv[HT];
+      if (!group()) break;
       const bool part = (mt.y & F_PART) != 0;
-      const int64_t slot = 2ll * group + ((mt.y & F_SLOT1) ? 1 : 0);
-#pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        const float lx = (redx[h] + redx[HT + h]) + (redx[2 * HT + h] + redx[3 * HT + h]);
-        const float lu = (redu[h] + redu[HT + h]) + (redu[2 * HT + h] + redu[3 * HT + h]);
-        inv[h] = (lu != 0.f) ? 1.0f / lu : 0.f;
-        const int hh = wg * HT + h;
-        if (key == h && hh < heads) {
-          const float l2 = (lx != 0.f) ? m_run[h] + log2f(lx) : -INFINITY;
+      const uint32_t row0 = (uint32_t)(2 * range + ((mt.y & F_SLOT1) ? 1 : 0)) * (uint32_t)heads_padded + head0;   // of the parts
+      const int left = heads - wg * HT;                                         // heads to store
+      float inv = 0.f;
+      if (lane < HT) {
+        const float lx = (redx[lane] + redx[HT + lane]) + (redx[2 * HT + lane] + redx[3 * HT + lane]);
+        const float lu = (redu[lane] + redu[HT + lane]) + (redu[2 * HT + lane] + redu[3 * HT + lane]);
+        inv = (lu != 0.f) ? 1.0f / lu : 0.f;
+        if (w4 == 0 && lane < left && !dry) {
+          const float l2 = (lx != 0.f) ? mine + log2f(lx) : -INFINITY;
           if (part)
-            a.part_lse[slot * heads_padded + head0 + hh] = l2;
+            a.part_lse[row0 + wg * HT + lane] = l2;
           else
-            a.lse[(int64_t)mt.x * a.H + head0 + hh] = l2 * 0.6931471805599453f;
+            a.lse[(int64_t)mt.x * a.H + head0 + wg * HT + lane] = l2 * 0.6931471805599453f;
         }
       }
       // (the next tile's vote and reduction use that scratch again)
-      if (!__all_sync(0xffffffffu, group_sync(sync_bar, sync_phase, abort_flag, err))) break;
-      if (!mbar_wait_warp(&bars[B_O_FULL + ob], (seg >> 1) & 1, abort_flag, err)) break;
+      if (!group()) break;
+      if (!dry && !poll(B_O_FULL + ob, (seg >> 1) & 1)) break;
       tc_fence_after();
-      uint16_t* out = a.out + ((int64_t)mt.x * a.H + head0) * 512 + key;
-      float* po = a.part_o + (slot * heads_padded + head0) * 512 + key;
+      uint16_t* out = a.out + ((int64_t)mt.x * a.H + head0 + wg * HT) * 512 + key;
+      float* po = a.part_o + (int64_t)(row0 + wg * HT) * 512 + key;
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
         float o[HT];
-        tmem_ld_n<HT>(tmem + lane_off + ob * (4 * HB) + m * HB + wg * HT, o);
+        tmem_ld_n<HT>(t_lane + ob * (4 * HB) + m * HB, o);
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-          const int hh = wg * HT + h;
-          if (hh < heads) {
+          const float v = o[h] * __shfl_sync(0xffffffffu, inv, h);
+          if (h < left && !dry) {
             if (part)
-              po[hh * 512 + m * 128] = o[h] * inv[h];
+              po[h * 512] = v;
             else
-              out[hh * 512 + m * 128] = f32_to_bf16_rn(o[h] * inv[h]);
+              out[h * 512] = f32_to_bf16_rn(v);
           }
         }
+        po += 128;
+        out += 128;
       }
       tc_fence_before();
-      mbar_arrive(&bars[B_O_EMPTY + ob]);
+      if (!dry) mbar_arrive(&bars[B_O_EMPTY + ob]);
     }
   }
 
@@ -729,137 +895,100 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
 // Join: out = sum_s 2^(L_s - M) O_s / sum_s 2^(L_s - M) over the parts of a cut
 // request (L_s base-2 log-sum-exp, O_s normalised), lse = M + log2 of that sum.
 //
-// One CTA per range border.  The borders inside one request share its H * 512
-// outputs evenly, so one long context is joined by all CTAs and a cut batch by
-// one CTA per cut, and every CTA reads about as much as its range's CTA wrote.
-// The parts are summed in order, whatever CTA stored them first.
+// The borders inside one request share its heads' outputs evenly, JOIN_Y CTAs to
+// a border, so one long context and a cut batch are both joined by as many CTAs
+// as there is work for.  A piece is 128 float4 outputs (a head), a thread each;
+// with eight parts or more 32 of them with a warp per quarter of the parts.  The
+// loads of the parts do not wait for the weights.  Small CTAs (128 threads of 32
+// registers fit beside a CTA of the first kernel), so that they are in place when
+// it ends.  The parts are summed in order, whatever CTA stored them first.
 // --------------------------------------------------------------------------
-constexpr int NT_JOIN = 512;
-constexpr int JOIN_ITEMS = 128;   // float4 outputs at a time with four threads each
-constexpr int JOIN_W = 1024;
+constexpr int NT_JOIN = 128;
+constexpr int JOIN_Y = 8;
 
-__global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
-  __shared__ int64_t scan[NT_JOIN / 32];
-  __shared__ int64_t found[2];       // request, tiles before it
-  __shared__ int found_n;
-  __shared__ float wgt[JOIN_W];
-  __shared__ float4 acc[3][JOIN_ITEMS];
+__global__ void __launch_bounds__(NT_JOIN, 16) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
+  __shared__ float4 acc[3][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the lengths were there before the first kernel: this part overlaps its end
-  const int per = (a.B + NT_JOIN - 1) / NT_JOIN;
-  const int b_lo = min(a.B, (int)threadIdx.x * per), b_hi = min(a.B, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(a, __ldg(a.kv_lens + b));
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) scan[warp] = incl;
-  if (threadIdx.x == 0) found_n = 0;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < NT_JOIN / 32; ++w) {
-    const int64_t n = scan[w];
-    if (w < warp) before += n;
-    total += n;
-  }
-  const int64_t ng = total < a.groups ? total : a.groups;
-  const int64_t g = blockIdx.x;                       // the border between ranges g and g + 1
-  const int64_t x = g + 1 < ng ? (g + 1) * total / ng : 0;
-  if (x > 0 && before <= x && x < before + mine) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int n = tiles_of(a, __ldg(a.kv_lens + b));
-      if (x < at + n) {
-        found[0] = b;
-        found[1] = at;
-        found_n = n;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-  // wait for the first kernel's stores
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (found_n == 0 || found[1] == x) return;          // no border here, or between two requests
-  const int64_t p0 = found[1], p1 = p0 + found_n;
-  const int64_t b = found[0];
-  // the ranges that hold the request's first and last tiles, and this CTA's share
-  const int g0 = (int)(((p0 + 1) * ng - 1) / total), g1 = (int)((p1 * ng - 1) / total);
+  const uint2 head = reinterpret_cast<const uint2*>(a.borders)[0];
+  const int4 at = a.borders[1 + blockIdx.x];            // the end of range blockIdx.x
+  const uint32_t total = head.x, ng = head.y, g = blockIdx.x;
+  if (g + 1 >= ng || at.z == at.y) return;              // no border, or one between two requests
+  const uint32_t end = range_begin(g + 1, total, ng);   // tiles up to here
+  const uint32_t p0 = end - (uint32_t)at.z;             // tiles before the request
+  const int64_t b = at.x;
+  const int g0 = (int)range_of(p0, total, ng), g1 = (int)range_of(p0 + at.y - 1, total, ng);
   const int S = g1 - g0 + 1, nb = S - 1, rank = (int)g - g0;
-  const int first_slot = 2 * g0 + ((int64_t)g0 * total / ng == p0 ? 0 : 1);
-  auto slot_of = [&](int s) { return s == 0 ? (int64_t)first_slot : 2ll * (g0 + s); };
-  const int64_t items = (int64_t)a.H * 128;
-  const int i0 = (int)(items * rank / nb), i1 = (int)(items * (rank + 1) / nb);
-  if (i0 >= i1) return;
-  const int ha = i0 >> 7, hz = (i1 - 1) >> 7;
-  const int hstep = JOIN_W / S < hz - ha + 1 ? JOIN_W / S : hz - ha + 1;   // heads whose weights fit
-  const bool wide = S >= 8;   // four threads per output, a quarter of the parts each
-  for (int h0 = ha; h0 <= hz; h0 += hstep) {
-    const int h1 = min(h0 + hstep - 1, hz);
-    // weights of these heads, one warp per head
-    for (int h = h0 + warp; h <= h1; h += NT_JOIN / 32) {
-      float m = -INFINITY;
-      for (int s = lane; s < S; s += 32) m = fmaxf(m, a.part_lse[slot_of(s) * heads_padded + h]);
-      m = warp_max(m);
-      const float mr = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-      for (int s = lane; s < S; s += 32) {
-        const float w = exp2f(a.part_lse[slot_of(s) * heads_padded + h] - mr);
-        wgt[(h - h0) * S + s] = w;
-        sum += w;
-      }
-      sum = warp_sum(sum);
-      const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-      for (int s = lane; s < S; s += 32) wgt[(h - h0) * S + s] *= inv;
-      if (lane == 0 && (h << 7) >= i0 && (h << 7) < i1)
-        a.lse[b * a.H + h] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  const int first_slot = 2 * g0 + (range_begin(g0, total, ng) == p0 ? 0 : 1);
+  const bool wide = S >= 8;
+  const int pieces = wide ? a.H * 4 : a.H;
+  const int c0 = pieces * rank / nb, c1 = pieces * (rank + 1) / nb;
+  const uint32_t pitch = (uint32_t)heads_padded;        // heads of a slot (all offsets are below 2^23)
+  const int s0 = wide ? S * warp / 4 : 0, s1 = wide ? S * (warp + 1) / 4 : S;
+#pragma unroll 1
+  for (int c = c0 + (int)blockIdx.y; c < c1; c += JOIN_Y) {
+    const int h = wide ? c >> 2 : c;
+    const int i = wide ? (c & 3) * 32 + lane : (int)threadIdx.x;   // float4 of the head
+    const float* pl = a.part_lse + h;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int s = lane; s < S; s += 32) m = fmaxf(m, pl[(uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch]);
+    m = warp_max(m);
+    const float mr = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int s = lane; s < S; s += 32) sum += exp2f(pl[(uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch] - mr);
+    sum = warp_sum(sum);
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + h * 128 + i;
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+      const uint32_t slot = (uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch;
+      const float4 v = src[slot * 128];
+      const float w = exp2f(pl[slot] - mr);
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
     }
-    __syncthreads();
-    const int lo = max(i0, h0 << 7), hi = min(i1, (h1 + 1) << 7);
-    const int quarter = wide ? (int)threadIdx.x / JOIN_ITEMS : 0;
-    const int step = wide ? JOIN_ITEMS : NT_JOIN;
-    const int s0 = wide ? S * quarter / 4 : 0, s1 = wide ? S * (quarter + 1) / 4 : S;
-    for (int base = lo; base < hi; base += step) {
-      const int i = base + (int)threadIdx.x % step;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < hi) {
-        const int h = i >> 7;
-        const float* src = a.part_o + 4ll * i;
-        const float* w = wgt + (h - h0) * S;
-#pragma unroll 8
-        for (int s = s0; s < s1; ++s) {
-          const float4 v = *reinterpret_cast<const float4*>(src + slot_of(s) * heads_padded * 512);
-          const float f = w[s];
-          o.x += f * v.x;
-          o.y += f * v.y;
-          o.z += f * v.z;
-          o.w += f * v.w;
-        }
-      }
-      if (wide) {
-        if (quarter > 0) acc[quarter - 1][threadIdx.x % JOIN_ITEMS] = o;
-        __syncthreads();
-        if (quarter == 0) {
+    if (wide) {
+      if (warp > 0) acc[warp - 1][lane] = o;
+      __syncthreads();
+      if (warp == 0) {
 #pragma unroll
-          for (int qd = 0; qd < 3; ++qd) {
-            const float4 v = acc[qd][threadIdx.x];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-          }
+        for (int q = 0; q < 3; ++q) {
+          const float4 v = acc[q][lane];
+          o.x += v.x;
+          o.y += v.y;
+          o.z += v.z;
+          o.w += v.w;
         }
       }
-      if (i < hi && quarter == 0)
-        *reinterpret_cast<uint2*>(a.out + b * a.H * 512 + 4ll * i) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-      if (wide) __syncthreads();
     }
-    __syncthreads();
+    if (!wide || warp == 0)
+      *reinterpret_cast<uint2*>(a.out + (b * a.H + h) * 512 + 4 * i) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (threadIdx.x == 0 && i == 0)
+      a.lse[b * a.H + h] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (wide) __syncthreads();
   }
+}
+
+template <typename... P, typename... A>
+static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
 }
 
 template <int HB, int NC>
@@ -874,8 +1003,8 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
       return -1;
     attr_set[dev] = 1;
   }
-  decode_kernel<HB, NC><<<a.groups * a.head_blocks, NTHREADS, C::SMEM_BYTES, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
+  return launch_after(decode_kernel<HB, NC>, dim3((unsigned)(a.groups * a.head_blocks)), NTHREADS, C::SMEM_BYTES, stream, a);
 }
 
 }  // namespace decode
@@ -889,16 +1018,7 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   else r = d_rope ? launch_t<32, 9>(a, stream) : launch_t<32, 8>(a, stream);
   if (r != 0) return r;
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.groups - 1));
-  cfg.blockDim = dim3(NT_JOIN);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, a, a.head_blocks * hb) == cudaSuccess ? 0 : -1;
+  return launch_after(join_kernel, dim3((unsigned)(a.groups - 1), JOIN_Y), NT_JOIN, 0, stream, a, a.head_blocks * hb);
 }
 
 }  // namespace dsa

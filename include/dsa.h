@@ -571,8 +571,8 @@ int dsa_debug_wait_timeout(dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostic timeline (no counterpart on the pages; a profiling aid).  While
- * a buffer is set, the first two CTAs of every per-token, grouped and masked
- * launch write clock64() stamps of up to 8 pipeline events for each of their
+ * a buffer is set, the first two CTAs of every per-token, grouped, masked and
+ * decode launch write clock64() stamps of up to 8 pipeline events for each of their
  * first `capacity` tiles into it: u64 slot [(cta * capacity + tile) * 8 +
  * event]; untouched slots keep their contents.  `device_buffer` is caller-owned
  * device memory of at least 2 * capacity * 8 * 8 bytes; NULL (or capacity 0)
