@@ -57,7 +57,6 @@ namespace decode {
 constexpr int BK = 128;          // keys per tile (the MMA's M)
 constexpr int NTHREADS = 768;
 constexpr int NI = 4;            // tiles of rows ahead
-constexpr int NPROD = 12;        // warps that load the rows
 constexpr float kTau = 8.0f;     // lazy-rescale threshold (log2 units)
 // 768 threads launched at 80 registers: 256 * 144 + 512 * 48 = 768 * 80
 constexpr int REGS_SOFTMAX = 144;
@@ -69,8 +68,8 @@ struct Cfg {
   // K ring: 64-column chunks; V ring: 128-column units (what shared memory leaves beside q and P)
   static constexpr int NK = HB == 16 ? 6 : 5;
   static constexpr int NV = 3;
-  static constexpr int VW = NPROD - NK;                  // warps that load V
-  static constexpr int VL = (64 + VW - 1) / VW;          // row gathers of a unit per V warp
+  static constexpr int NPROD = NK + 2 * NV;              // warps that load the rows
+  static_assert(NPROD <= 12, "warps");
   static constexpr uint32_t CHUNK_BYTES = BK * 128u;     // 128 keys x 64 columns
   static constexpr uint32_t UNIT_BYTES = 2u * CHUNK_BYTES;
   static constexpr uint32_t Q_BYTES = NC * HB * 128u;
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     for (int i = 0; i < NI; ++i) {
       mbar_init(&bars[B_IDX_FULL + i], 1);
       // 2 MMA warps, 2 softmax warpgroups, the producer warps, the q loader
-      mbar_init(&bars[B_IDX_EMPTY + i], 2 + 2 + NPROD + 1);
+      mbar_init(&bars[B_IDX_EMPTY + i], 2 + 2 + C::NPROD + 1);
     }
     mbar_init(&bars[B_Q_FULL], 1);
     mbar_init(&bars[B_Q_EMPTY], 1);
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     mbar_init(&bars[B_P_FULL], 256);
     mbar_init(&bars[B_P_EMPTY], 1);
     for (int i = 0; i < 16; ++i) {
-      mbar_init(&bars[B_FULL + i], 1);
+      mbar_init(&bars[B_FULL + i], i < 8 ? 1 : 2);   // a V unit is two warps' work
       mbar_init(&bars[B_EMPTY + i], 1);
     }
     *abort_flag = 0;
@@ -498,67 +497,61 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       if (lane == 0 && bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
     } else if (warp >= 12) {
       // ------------------------------------------------------------------
-      // row loads.  A warp issues row gathers one after another (about 80 cycles
-      // each), so they are dealt out: warp 12 + s owns K slot s and loads its
-      // chunks (a lane per 4 rows), the other warps share every V unit's 64.
-      // Where the keys lie in runs of box_rows rows a chunk is 128 / box_rows
-      // boxes instead, loaded by the slot's own warp.  A wait on parity cannot
-      // tell a phase from the one two before it, so a warp passes every phase
-      // of the slots it uses.
+      // row loads: a warp per 64-column chunk in flight, since a warp issues row
+      // gathers one after another (about 80 cycles each).  Warp 12 + s owns K
+      // slot s, the two warps after those a half of V slot 0, and so on: lane l
+      // gathers rows 4l .. 4l+3, or where the keys lie in runs of box_rows rows
+      // lane l loads box l of 128 / box_rows.  Each warp opens its chunk's share
+      // of every phase of its slot: none can fall behind it, which a wait on
+      // parity would not notice.
       // ------------------------------------------------------------------
       const bool ks = warp < 12 + C::NK;
-      const int pw = ks ? warp - 12 : warp - 12 - C::NK;
-      const int nslots = ks ? C::NK : C::NV, stages = ks ? NC : 4, chunks = ks ? 1 : 2;
-      const uint32_t ring = sbase + (ks ? C::OFF_K : C::OFF_V), bytes = chunks * C::CHUNK_BYTES;
-      const int e = ks ? lane : pw * C::VL + lane;          // this lane's gather
-      const bool gathers = ks || (lane < C::VL && e < 64);
-      const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
-      const int bi = lane % boxes, bc = lane / boxes;       // this lane's box
-      const uint64_t policy = evict_first_policy();
-      const int b0 = ks ? 0 : 8;
-      int slot = 0;
-      uint32_t phase = 1, armed = 0;   // armed: 2 + the parity of the last phase this warp opened
-      bool ok = true;
+      const int vw = warp - 12 - C::NK;
+      if (ks || vw < 2 * C::NV) {
+        const int mine_slot = ks ? warp - 12 : vw >> 1, hf = ks ? 0 : vw & 1;
+        const int nslots = ks ? C::NK : C::NV, stages = ks ? NC : 4;
+        const uint32_t dst = sbase + (ks ? C::OFF_K + mine_slot * C::CHUNK_BYTES
+                                         : C::OFF_V + mine_slot * C::UNIT_BYTES + hf * C::CHUNK_BYTES);
+        uint64_t* full = &bars[B_FULL + (ks ? 0 : 8) + mine_slot];
+        const int empty = B_EMPTY + (ks ? 0 : 8) + mine_slot;
+        const int col_step = ks ? 64 : 128;
+        const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
+        const uint64_t policy = evict_first_policy();
+        int slot = 0;
+        uint32_t used = 0;   // phases of the slot so far
+        bool ok = true;
 #pragma unroll 1
-      for (int it = 0; it < nt && ok; ++it) {
-        const int r = it % NI;
-        if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
-        const bool box = (meta[r].y & F_BOX) != 0;
-        int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * (e & 31));
-        if (box) x.x = rows[r * BK + bi * a.box_rows];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
-        const uint32_t within = box ? bc * C::CHUNK_BYTES + bi * a.box_rows * 128 : ((e >> 5) & 1) * C::CHUNK_BYTES + (e & 31) * 512;
-        int col = (box ? bc : (e >> 5) & 1) * 64;
+        for (int it = 0; it < nt && ok; ++it) {
+          const int r = it % NI;
+          if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+          const bool box = (meta[r].y & F_BOX) != 0;
+          int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
+          if (box) x.x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+          int col = hf * 64;
 #pragma unroll 1
-        for (int st = 0; st < stages; ++st) {
-          if (!ks || slot == pw) {
-            if (!doze(B_EMPTY + b0 + slot, phase)) { ok = false; break; }
-            const bool lead = slot == pw;   // opens the slot's phases, and loads its boxes
-            uint64_t* full = &bars[B_FULL + b0 + slot];
-            if (lead && lane == 0) {
-              mbar_arrive_expect_tx(full, bytes);
+          for (int st = 0; st < stages; ++st, col += col_step) {
+            const bool mine_now = slot == mine_slot;
+            if (++slot == nslots) slot = 0;
+            if (!mine_now) continue;
+            if (!doze(empty, (used & 1) ^ 1)) { ok = false; break; }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
               if (ks && st == 0) DSA_TRACE(a.tr, it, 1);
               if (ks && st == NC - 1) DSA_TRACE(a.tr, it, 2);
             }
-            if (lead) armed = 2u | (phase ^ 1u);
-            const uint32_t dst = ring + slot * bytes + within;
-            if (box) {
-              if (lead && bc < chunks) load_2d_hint(dst, &a.tmap_box, col, x.x, full, policy);
-            } else if (gathers) {
-              gather4_hint(dst, &a.tmap_kv, col, x, full, policy);
-            }
-          }
-          col += 64 * chunks;
-          if (++slot == nslots) {
-            slot = 0;
-            phase ^= 1;
+            if (!box)
+              gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+            else if (lane < boxes)
+              load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+            ++used;
           }
         }
+        // let the slot's last copies land before the CTA can exit
+        if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
+        __syncwarp();
       }
-      // let the slot's last copies land before the CTA can exit
-      if (lane == 0 && armed) mbar_wait_drain(&bars[B_FULL + b0 + pw], armed & 1u, err);
-      __syncwarp();
     } else if (warp == 10) {
       // ------------------------------------------------------------------
       // q of every request of the range, one box per swizzle column (rows b*H +
