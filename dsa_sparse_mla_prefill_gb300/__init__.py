@@ -113,7 +113,7 @@ _SIGNATURES = {
     "dsa_rope": (_I, [_VP, _L, _L, _VP, _L, _L, _I, _VP, _I, _I, ctypes.POINTER(RopeFreqs), _I, _VP]),
     "dsa_kv_append": (_I, [_VP, _L, _VP, _L, _I, _I, _VP, _VP, _VP, _I, _I, _I, ctypes.POINTER(RopeFreqs), _VP, _I, _I,
                            _I, _VP]),
-    "dsa_paged_decode_workspace": (_L, [_I, _I]),
+    "dsa_paged_decode_workspace": (_L, [_I, _I, _L]),
     "dsa_paged_decode": (_I, [_VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP,
                               _L, _VP]),
     "dsa_form_calibration_default": (_I, [ctypes.POINTER(FormCalibration)]),
@@ -576,42 +576,51 @@ def dsa_sparse_prefill_fp8(q, kv_fp8, idx, k: int, scale: float, d_rope: int = 6
 
 
 # ---------------------------------------------------------------------------
-# the decode step
+# the decode step: calls of a few microseconds of GPU work, so the checks are
+# written out flat (a call through these functions costs the host about twice
+# the bare library call)
 # ---------------------------------------------------------------------------
-def _on_device(t, fn, stream):
-    """Calls fn(stream handle) with t's device current.  A library call works on
-    the current device, so a tensor of another one needs it switched."""
+_torch = _raw_stream = _current_device = None
+
+
+def _load_torch():
+    global _torch, _raw_stream, _current_device
     import torch
-    index = t.device.index
-    if index == torch.cuda.current_device():
-        return fn(_raw_stream(stream, index))
-    with torch.cuda.device(index):
-        return fn(_raw_stream(stream, index))
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
+    return torch
 
 
-def _raw_stream(stream, index):
-    import torch
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _made_for(stream, *tensors):
-    """Tensors made here on the current stream and used on another one: their
-    memory must not be handed out again before that stream is done."""
+def _queue(fn, where, args, dev, stream):
+    """Calls the library function on `stream` (None: the current one) with `dev` current, which a
+    library call works on."""
     if stream is not None:
-        import torch
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        cur = torch.cuda.current_stream(tensors[0].device)
-        if s.cuda_stream != cur.cuda_stream:
-            for t in tensors:
-                t.record_stream(s)
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == _current_device():
+        st = fn(*args, _raw_stream(dev) if stream is None else stream)
+    else:
+        with _torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev) if stream is None else stream)
+    if st:
+        raise DSAError(st, where)
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+def _made_for(stream, tensors):
+    """Tensors made here on the current stream and used on another one: their memory must not be
+    handed out again before that stream is done."""
+    s = stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream))
+    if s.cuda_stream != _torch.cuda.current_stream(tensors[0].device).cuda_stream:
+        for t in tensors:
+            t.record_stream(s)
+
+
+def _int_tensor(t, name, ndim, dev):
+    if not isinstance(t, _torch.Tensor) or t.dtype is not _torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.dim() != ndim or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-D tensor on CUDA device {dev}")
 
 
 @functools.lru_cache(maxsize=64)
@@ -640,42 +649,51 @@ def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, s
     or view of the same shape and dtype, x itself for in place; a new contiguous one if None.
     gradient=True turns back: the gradient of the forward with respect to x, given the gradient
     of its result.  Returns out."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+    torch = _torch or _load_torch()
+    if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a bf16 or fp32 tensor")
-    if not x.is_cuda or x.dim() != 3 or x.stride(2) != 1:
-        raise ValueError("x must be a 3-D CUDA tensor with unit stride in its last dimension")
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("x must be a bf16 or fp32 tensor")
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 3:
+        raise ValueError("x must be a 3-D CUDA tensor")
     if not isinstance(freqs, RopeFreqs):
         raise TypeError("freqs must come from dsa_rope_freqs")
-    _need(positions, torch.int32, "positions", 1)
-    T, H, d = x.shape
-    if d != freqs.d_rope:
-        raise ValueError(f"x has {d} columns, the frequencies {freqs.d_rope}")
-    if positions.shape[0] != T:
-        raise ValueError("positions must have one entry per token")
+    _int_tensor(positions, "positions", 1, dev)
+    shape = x.shape
+    T, H, d = shape
+    xs = x.stride()
+    if d != freqs.d_rope or positions.shape[0] != T:
+        raise ValueError(f"x is {tuple(shape)}: it must have {freqs.d_rope} columns, and positions one entry per token")
     if out is None:
-        out = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
-        _made_for(stream, out)
-    elif out.dtype != x.dtype or out.shape != x.shape or (d > 1 and out.stride(2) != 1):
-        raise ValueError("out must have x's shape and dtype and unit stride in its last dimension")
-    _same_device(x, positions=positions, out=out)
-    xs, ys = x.stride(), out.stride()
-    _check(_on_device(x, lambda s: lib().dsa_rope(
-        x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], 1 if x.dtype == torch.float32 else 0,
-        positions.data_ptr(), T, H, ctypes.byref(freqs), 1 if gradient else 0, s), stream), "dsa_rope")
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        if stream is not None:
+            _made_for(stream, (out,))
+    elif out.dtype is not dtype or out.shape != shape or out.get_device() != dev:
+        raise ValueError("out must have x's shape, dtype and device")
+    ys = out.stride()
+    if xs[2] != 1 or ys[2] != 1:
+        raise ValueError("x and out must have unit stride in their last dimension")
+    _queue(lib().dsa_rope, "dsa_rope",
+           (x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], 1 if dtype is torch.float32 else 0,
+            positions.data_ptr(), T, H, freqs, 1 if gradient else 0), dev, stream)
     return out
 
 
-def _cache_of(cache, d_rope):
+def _cache_of(cache, d_rope, dev):
     """(format, rows, ld) of a bf16 or FP8 cache tensor."""
-    import torch
-    if isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8:
-        _need(cache, torch.uint8, "cache", 2)
-        if cache.shape[1] != dsa_kv_fp8_row_bytes(d_rope):
-            raise ValueError("FP8 cache rows must be dsa_kv_fp8_row_bytes(d_rope) bytes")
-        return 1, cache.shape[0], 0
-    _need(cache, torch.bfloat16, "cache", 2)
-    return 0, cache.shape[0], cache.shape[1]
+    if not isinstance(cache, _torch.Tensor) or cache.dim() != 2 or cache.get_device() != dev or \
+            not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous 2-D CUDA tensor on the device of the other arguments")
+    N, ld = cache.shape
+    if cache.dtype is _torch.bfloat16:
+        return 0, N, ld
+    if cache.dtype is not _torch.uint8:
+        raise TypeError("cache must be bf16 rows or FP8 rows as uint8")
+    if ld != 528 + 2 * d_rope:
+        raise ValueError("FP8 cache rows must be dsa_kv_fp8_row_bytes(d_rope) bytes")
+    return 1, N, 0
 
 
 def dsa_kv_append(c_kv, k_pe, positions, block_table, block_size: int, cache, rope: RopeFreqs = None, token_req=None,
@@ -685,40 +703,48 @@ def dsa_kv_append(c_kv, k_pe, positions, block_table, block_size: int, cache, ro
     block_size + p % block_size.  c_kv [T, 512] and k_pe [T, d_rope] bf16 (row-strided views, k_pe
     None without RoPE columns) are stored with k_pe rotated by ``rope`` (None: as it is).  cache:
     bf16 [N, ld_kv] or FP8 rows [N, dsa_kv_fp8_row_bytes(d_rope)] uint8.  Returns cache."""
-    import torch
-    for name, x in (("c_kv", c_kv), ("k_pe", k_pe)):
-        if x is None and name == "k_pe":
-            continue
-        if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be a bf16 tensor")
-        if not x.is_cuda or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-            raise ValueError(f"{name} must be a 2-D CUDA tensor with unit stride in its last dimension")
+    torch = _torch or _load_torch()
+    if not isinstance(c_kv, torch.Tensor) or c_kv.dtype is not torch.bfloat16:
+        raise TypeError("c_kv must be a bf16 tensor")
+    dev = c_kv.get_device()
+    cs = c_kv.stride()
+    if dev < 0 or c_kv.dim() != 2 or c_kv.shape[1] != 512 or cs[1] != 1:
+        raise ValueError("c_kv must be a [T, 512] CUDA tensor with unit stride in its last dimension")
     T = c_kv.shape[0]
-    d_rope = 0 if k_pe is None else k_pe.shape[1]
-    if c_kv.shape[1] != 512 or (k_pe is not None and k_pe.shape[0] != T):
-        raise ValueError("c_kv must be [T, 512] and k_pe [T, d_rope]")
+    d_rope = pe = ps = 0
+    if k_pe is not None:
+        if not isinstance(k_pe, torch.Tensor) or k_pe.dtype is not torch.bfloat16:
+            raise TypeError("k_pe must be a bf16 tensor")
+        if k_pe.dim() != 2 or k_pe.shape[0] != T or k_pe.get_device() != dev:
+            raise ValueError("k_pe must be a [T, d_rope] tensor on c_kv's device")
+        d_rope = k_pe.shape[1]
+        if d_rope:
+            pe = k_pe.data_ptr()
+            ps, last = k_pe.stride()
+            if last != 1:
+                raise ValueError("k_pe must have unit stride in its last dimension")
     if rope is not None and not isinstance(rope, RopeFreqs):
         raise TypeError("rope must come from dsa_rope_freqs")
-    _need(positions, torch.int32, "positions", 1)
-    _need(block_table, torch.int32, "block_table", 2)
+    _int_tensor(positions, "positions", 1, dev)
+    _int_tensor(block_table, "block_table", 2, dev)
     if token_req is not None:
-        _need(token_req, torch.int32, "token_req", 1)
+        _int_tensor(token_req, "token_req", 1, dev)
     if positions.shape[0] != T or (token_req is not None and token_req.shape[0] != T):
         raise ValueError("positions and token_req must have one entry per token")
-    fmt, N, ld = _cache_of(cache, d_rope)
-    _same_device(cache, c_kv=c_kv, k_pe=k_pe, positions=positions, block_table=block_table, token_req=token_req)
-    pe = k_pe if d_rope else None
-    _check(_on_device(cache, lambda s: lib().dsa_kv_append(
-        c_kv.data_ptr(), c_kv.stride(0), None if pe is None else pe.data_ptr(), 0 if pe is None else pe.stride(0), T,
-        d_rope, positions.data_ptr(), None if token_req is None else token_req.data_ptr(), block_table.data_ptr(),
-        block_table.shape[0], block_table.shape[1], int(block_size), None if rope is None else ctypes.byref(rope),
-        cache.data_ptr(), fmt, N, ld, s), stream), "dsa_kv_append")
+    fmt, N, ld = _cache_of(cache, d_rope, dev)
+    num_req, max_blocks = block_table.shape
+    _queue(lib().dsa_kv_append, "dsa_kv_append",
+           (c_kv.data_ptr(), cs[0], pe, ps, T, d_rope, positions.data_ptr(),
+            None if token_req is None else token_req.data_ptr(), block_table.data_ptr(), num_req, max_blocks,
+            int(block_size), rope, cache.data_ptr(), fmt, N, ld), dev, stream)
     return cache
 
 
-def dsa_paged_decode_workspace(B: int, H: int) -> int:
-    """Device workspace bytes dsa_paged_decode needs."""
-    n = int(lib().dsa_paged_decode_workspace(int(B), int(H)))
+@functools.lru_cache(maxsize=1024)
+def dsa_paged_decode_workspace(B: int, H: int, max_positions: int) -> int:
+    """Device workspace bytes dsa_paged_decode needs for B requests of H heads; max_positions: k with
+    idx, else the block table's columns * block_size."""
+    n = int(lib().dsa_paged_decode_workspace(B, H, max_positions))
     if n < 0:
         raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_paged_decode_workspace")
     return n
@@ -730,48 +756,59 @@ def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: flo
     576 or 512, H <= 128), cache bf16 [N, ld_kv] or FP8 rows uint8, block_table [B, max_blocks] and
     kv_lens [B] int32 on the device.  idx [B, ld] int32 (first k columns): the token's own top-k
     positions instead of the whole context.  workspace: a CUDA uint8 tensor of
-    dsa_paged_decode_workspace(B, H) bytes (calls sharing one must not overlap on the GPU); one per
+    dsa_paged_decode_workspace(...) bytes (calls sharing one must not overlap on the GPU); one per
     call if None.  Returns (out [B, H, 512] bf16, lse [B, H] fp32)."""
-    import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(kv_lens, torch.int32, "kv_lens", 1)
+    torch = _torch or _load_torch()
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.bfloat16:
+        raise TypeError("q must be a bf16 tensor")
+    dev = q.get_device()
+    if dev < 0 or q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous 3-D CUDA tensor")
     B, H, d_qk = q.shape
-    if d_qk not in (512, 576):
+    if d_qk != 576 and d_qk != 512 or d_v != 512:
         raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_paged_decode")
-    fmt, N, ld_kv = _cache_of(cache, d_qk - 512)
-    if block_table.shape[0] != B or kv_lens.shape[0] != B:
+    _int_tensor(block_table, "block_table", 2, dev)
+    _int_tensor(kv_lens, "kv_lens", 1, dev)
+    fmt, N, ld_kv = _cache_of(cache, d_qk - 512, dev)
+    block_size = int(block_size)
+    rows, max_blocks = block_table.shape
+    if rows != B or kv_lens.shape[0] != B:
         raise ValueError("block_table and kv_lens must have one row per request")
-    ld = 0
+    ld, idx_ptr = 0, None
     if idx is not None:
-        _need(idx, torch.int32, "idx", 2)
-        if idx.shape[0] != B:
+        _int_tensor(idx, "idx", 2, dev)
+        rows, ld = idx.shape
+        if rows != B:
             raise ValueError("idx must have one row per request")
-        ld = idx.shape[1]
+        idx_ptr = idx.data_ptr()
         k = ld if k is None else int(k)
     elif k is not None:
         raise ValueError("k without idx")
+    device = q.device
     made = []
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=device)
         made.append(out)
-    elif _need(out, torch.bfloat16, "out", 3).shape != (B, H, d_v):
-        raise ValueError("out must be [B, H, d_v]")
+    elif out.dtype is not torch.bfloat16 or out.shape != (B, H, 512) or out.get_device() != dev or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 [B, H, 512] tensor on q's device")
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, H), dtype=torch.float32, device=device)
         made.append(lse)
-    elif _need(lse, torch.float32, "lse", 2).shape != (B, H):
-        raise ValueError("lse must be [B, H]")
+    elif lse.dtype is not torch.float32 or lse.shape != (B, H) or lse.get_device() != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, H] tensor on q's device")
     if workspace is None:
-        workspace = torch.empty(dsa_paged_decode_workspace(B, H), dtype=torch.uint8, device=q.device)
+        nbytes = dsa_paged_decode_workspace(B, H, max_blocks * block_size if idx is None else k)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         made.append(workspace)
-    _need(workspace, torch.uint8, "workspace", 1)
-    _same_device(q, cache=cache, block_table=block_table, kv_lens=kv_lens, idx=idx, out=out, lse=lse,
-                 workspace=workspace)
-    if made:
-        _made_for(stream, *made)
-    _check(_on_device(q, lambda s: lib().dsa_paged_decode(
-        q.data_ptr(), cache.data_ptr(), fmt, N, ld_kv, block_table.data_ptr(), block_table.shape[1], int(block_size),
-        kv_lens.data_ptr(), None if idx is None else idx.data_ptr(), k or 0, ld, B, H, d_qk, d_v, float(scale),
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), s), stream), "dsa_paged_decode")
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    else:
+        nbytes = workspace.numel()
+    if stream is not None and made:
+        _made_for(stream, made)
+    _queue(lib().dsa_paged_decode, "dsa_paged_decode",
+           (q.data_ptr(), cache.data_ptr(), fmt, N, ld_kv, block_table.data_ptr(), max_blocks, block_size,
+            kv_lens.data_ptr(), idx_ptr, k or 0, ld, B, H, d_qk, 512, float(scale), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), nbytes), dev, stream)
     return out, lse

@@ -622,20 +622,29 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
                                                                                                         : DSA_ERR_CUDA;
 }
 
-// workspace: where the ranges end, then two partial results per CTA group
-// (log-sum-exp, then outputs)
-static int64_t decode_part_bytes(int H, int64_t* lse_at, int64_t* out_at) {
-  const int64_t hp = (int64_t)dsa::decode_head_blocks(H) * dsa::decode_heads_per_cta(H);
-  const int64_t slots = 2 * (dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H));
-  *lse_at = (16 * (1 + dsa::kDecodeMaxCtas) + 255) / 256 * 256;
-  *out_at = *lse_at + (slots * hp * 4 + 255) / 256 * 256;
-  return *out_at + slots * hp * 512 * 4;
+// Key tiles of a request that may attend to `positions`, and the CTA groups of
+// a call: no more than tiles, one CTA per SM.
+static int64_t decode_tiles(int64_t positions) {
+  return ((positions < INT32_MAX ? positions : INT32_MAX) + 127) / 128;
+}
+static int decode_groups(int B, int H, int64_t max_tiles) {
+  const int64_t tiles = B * max_tiles, most = dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H);
+  return (int)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
 }
 
-int64_t dsa_paged_decode_workspace(int B, int H) {
-  if (B < 0 || H < 1 || H > 128) return -1;
+// workspace: where the ranges end, then two partial results per CTA group
+// (log-sum-exp, then outputs)
+static int64_t decode_part_bytes(int H, int groups, int64_t* lse_at, int64_t* out_at) {
+  const int64_t hp = (int64_t)dsa::decode_head_blocks(H) * dsa::decode_heads_per_cta(H);
+  *lse_at = (16 * (1 + groups) + 255) / 256 * 256;
+  *out_at = *lse_at + (2 * groups * hp * 4 + 255) / 256 * 256;
+  return *out_at + 2 * groups * hp * 512 * 4;
+}
+
+int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
+  if (B < 0 || H < 1 || H > 128 || max_positions < 0) return -1;
   int64_t l, o;
-  return decode_part_bytes(H, &l, &o);
+  return decode_part_bytes(H, decode_groups(B, H, decode_tiles(max_positions)), &l, &o);
 }
 
 int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
@@ -650,18 +659,17 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   if (idx && (k < 0 || ld < k)) return DSA_ERR_INVALID_ARG;
   if ((int64_t)B * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   // key tiles of a request at most, and of all (counted in 32 bits)
-  const int64_t most = idx ? k : ((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
-  const int64_t max_tiles = (most + 127) / 128;
-  const int64_t tiles = (int64_t)B * max_tiles;
-  if (tiles > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int64_t max_tiles = decode_tiles(idx ? k : (int64_t)max_blocks * block_size);
+  if (B * max_tiles > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (B == 0) return DSA_OK;
   if (!q || (!cache && N > 0) || !block_table || !kv_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||
       !aligned16(out) || !aligned4(lse))
     return DSA_ERR_INVALID_ARG;
+  const int groups = decode_groups(B, H, max_tiles);
   int64_t lse_at, out_at;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < decode_part_bytes(H, &lse_at, &out_at))
+      workspace_bytes < decode_part_bytes(H, groups, &lse_at, &out_at))
     return DSA_ERR_INVALID_ARG;
   DevInfo* d;
   if (!dev_info(&d)) return DSA_ERR_CUDA;
@@ -691,9 +699,9 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   a.scale = scale;
   a.tr = g_trace;
   a.head_blocks = dsa::decode_head_blocks(H);
-  const int ctas = d->num_sms < dsa::kDecodeMaxCtas ? d->num_sms : dsa::kDecodeMaxCtas;
-  a.groups = ctas / a.head_blocks;
-  if (tiles < a.groups) a.groups = tiles > 0 ? (int)tiles : 1;
+  // (a GPU with fewer SMs than the workspace is sized for runs fewer ranges)
+  const int most = d->num_sms / a.head_blocks;
+  a.groups = groups < most ? groups : (most > 0 ? most : 1);
   // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
   const bool none = N == 0;
   const bool mapped = fp8 ? dsa::make_row_gather_map_u8(&a.tmap_kv, none ? (const void*)q : cache,

@@ -62,13 +62,18 @@ constexpr float kTau = 8.0f;     // lazy-rescale threshold (log2 units)
 constexpr int REGS_SOFTMAX = 144;
 constexpr int REGS_REST = 48;
 
-template <int HB, int NC>
+template <int HB, int NC, bool F8>
 struct Cfg {
   static constexpr int HT = HB / 2;                      // heads per softmax thread
-  // K ring: 64-column chunks; V ring: 128-column units (what shared memory leaves beside q and P)
-  static constexpr int NK = HB == 16 ? 6 : 5;
-  static constexpr int NV = 3;
-  static constexpr int NPROD = NK + 2 * NV;              // warps that load the rows
+  // What shared memory leaves beside q and P.  bf16 rows: a ring of NK 64-column
+  // K chunks and one of NV 128-column V units.  FP8 rows: NK slots of codes (128
+  // rows x 128), NV units of converted columns that QK and P.V both read, and a
+  // slot for the RoPE columns.
+  static constexpr int NK = F8 ? (HB == 16 ? 3 : 2) : (HB == 16 ? 6 : 5);
+  static constexpr int NV = F8 ? 4 : 3;
+  static constexpr bool ROPE_SLOT = F8 && NC == 9;
+  // warps that read the row ring: the loaders, and for FP8 rows the converters
+  static constexpr int NPROD = F8 ? NK + (ROPE_SLOT ? 1 : 0) + 8 : NK + 2 * NV;
   static_assert(NPROD <= 12, "warps");
   static constexpr uint32_t CHUNK_BYTES = BK * 128u;     // 128 keys x 64 columns
   static constexpr uint32_t UNIT_BYTES = 2u * CHUNK_BYTES;
@@ -77,13 +82,14 @@ struct Cfg {
   static constexpr uint32_t RED_FLOATS = 2u * 2u * 4u * HT;   // [parity][warpgroup][warp][head]
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + NK * CHUNK_BYTES;
-  static constexpr uint32_t OFF_Q = OFF_V + NV * UNIT_BYTES;
+  static constexpr uint32_t OFF_R = OFF_V + NV * UNIT_BYTES;
+  static constexpr uint32_t OFF_Q = OFF_R + (ROPE_SLOT ? CHUNK_BYTES : 0u);
   static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
   static constexpr uint32_t OFF_ROWS = OFF_P + P_BYTES;
   static constexpr uint32_t OFF_META = OFF_ROWS + NI * BK * 4u;
   static constexpr uint32_t OFF_RED = OFF_META + NI * 16u;
   static constexpr uint32_t OFF_BAR = OFF_RED + 2u * RED_FLOATS * 4u;   // two sums in the epilogue
-  static constexpr int NBAR = 58;
+  static constexpr int NBAR = 60;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
   static constexpr uint32_t MISC_BYTES = 192u;
   static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024u;
@@ -107,8 +113,10 @@ enum {
   B_SMX = 22,        // [2] one per softmax warpgroup
   B_PLAN = 9,
   B_DRAIN = 24,      // [2] one per MMA issuer
-  B_FULL = 26,       // [16] K slots from 0, V slots from 8
+  B_FULL = 26,       // [16] K (or code) slots from 0, V units from 8
   B_EMPTY = 42,      // [16]
+  B_R_FULL = 11,     // RoPE columns (FP8 rows)
+  B_R_EMPTY = 58,
 };
 
 // flags of a tile
@@ -299,9 +307,9 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float* v) {
   }
 }
 
-template <int HB, int NC>
+template <int HB, int NC, bool F8>
 __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using C = Cfg<HB, NC>;
+  using C = Cfg<HB, NC, F8>;
   constexpr int HT = C::HT;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -349,9 +357,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     mbar_init(&bars[B_P_FULL], 256);
     mbar_init(&bars[B_P_EMPTY], 1);
     for (int i = 0; i < 16; ++i) {
-      mbar_init(&bars[B_FULL + i], i < 8 ? 1 : 2);   // a V unit is two warps' work
-      mbar_init(&bars[B_EMPTY + i], 1);
+      // a V unit is two loading warps' work; codes are read, and units of FP8
+      // rows filled, by eight converting warps
+      mbar_init(&bars[B_FULL + i], i < 8 ? 1 : (F8 ? 8 : 2));
+      mbar_init(&bars[B_EMPTY + i], F8 && i < 8 ? 8 : 1);
     }
+    mbar_init(&bars[B_R_FULL], 1);
+    mbar_init(&bars[B_R_EMPTY], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -496,6 +508,110 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
     } else if (warp >= 12) {
+      if constexpr (F8) {
+        // ----------------------------------------------------------------
+        // FP8 rows.  Warp 12 + s owns code slot s and loads 128-code blocks into
+        // it, warp 12 + NK the RoPE columns (bf16, byte 528 of the row) into
+        // their slot; lanes as for bf16 rows.
+        // Warps 16-23 convert: thread = row and half of the block, 64 codes into
+        // the half's 64-column chunk of the unit, in the layout in which the bf16
+        // rows would have landed, by the arithmetic of the dequantize kernel.
+        // ----------------------------------------------------------------
+        const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
+        if (warp < 12 + C::NK + (C::ROPE_SLOT ? 1 : 0)) {
+          const bool rope = C::ROPE_SLOT && warp == 12 + C::NK;
+          const int own = warp - 12, nslots = rope ? 1 : C::NK, stages = rope ? 1 : 4;
+          const uint32_t dst = sbase + (rope ? C::OFF_R : C::OFF_K + own * C::CHUNK_BYTES);
+          uint64_t* full = &bars[rope ? B_R_FULL : B_FULL + own];
+          const int empty = rope ? B_R_EMPTY : B_EMPTY + own;
+          const uint64_t policy = evict_first_policy();
+          int slot = 0;
+          uint32_t used = 0;
+          bool ok = true;
+#pragma unroll 1
+          for (int it = 0; it < nt && ok; ++it) {
+            const int r = it % NI;
+            if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
+            const bool box = (meta[r].y & F_BOX) != 0;
+            int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
+            if (box) x.x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+#pragma unroll 1
+            for (int st = 0; st < stages; ++st) {
+              const bool mine_now = rope || slot == own;
+              if (++slot == nslots) slot = 0;
+              if (!mine_now) continue;
+              if (!doze(empty, (used & 1) ^ 1)) { ok = false; break; }
+              if (lane == 0) {
+                mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
+                if (!rope && st == 0) DSA_TRACE(a.tr, it, 1);
+                if (!rope && st == 3) DSA_TRACE(a.tr, it, 2);
+              }
+              const int col = rope ? 528 : 128 * st;
+              if (!box)
+                gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+              else if (lane < boxes)
+                load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+              ++used;
+            }
+          }
+          if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
+          __syncwarp();
+        } else if (warp >= 16) {
+          const int row = (warp & 3) * 32 + lane, hf = (warp - 16) >> 2;
+          const uint32_t rsw = (uint32_t)(row & 7);   // 128B swizzle phase of this row
+          uint32_t cs = 0, cphase = 0, us = 0, uphase = 1;   // code slot and unit, their phases
+          // the four block scales of the row, loaded a tile ahead (zero for a masked row)
+          auto scales = [&](int it) {
+            const int r = it % NI;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (it < nt && doze(B_IDX_FULL + r, (it / NI) & 1)) {
+              const int x = rows[r * BK + row];
+              if (x >= 0) s = __ldg(reinterpret_cast<const float4*>(a.rows_base + (int64_t)x * a.row_bytes + 512));
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+            }
+            return s;
+          };
+          float4 next = scales(0);
+          bool ok = true;
+#pragma unroll 1
+          for (int it = 0; it < nt && ok; ++it) {
+            float4 sc = next;
+            next = scales(it + 1);
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+              if (!doze(B_FULL + cs, cphase) || !doze(B_EMPTY + 8 + us, uphase)) { ok = false; break; }
+              const uint32_t src = sbase + C::OFF_K + cs * C::CHUNK_BYTES + row * 128;
+              const uint32_t dst = sbase + C::OFF_V + us * C::UNIT_BYTES + hf * C::CHUNK_BYTES + row * 128;
+              uint4 w[4];
+#pragma unroll
+              for (int pp = 0; pp < 4; ++pp) w[pp] = lds128(src + ((((uint32_t)(4 * hf + pp)) ^ rsw) << 4));
+              // every code this warp reads is in registers
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_EMPTY + cs]);
+#pragma unroll
+              for (int pp = 0; pp < 4; ++pp) {
+                uint32_t v[8];
+                e4m3x4_dequant_bf16x4(w[pp].x, sc.x, v[0], v[1]);
+                e4m3x4_dequant_bf16x4(w[pp].y, sc.x, v[2], v[3]);
+                e4m3x4_dequant_bf16x4(w[pp].z, sc.x, v[4], v[5]);
+                e4m3x4_dequant_bf16x4(w[pp].w, sc.x, v[6], v[7]);
+                sts128(dst + ((((uint32_t)(2 * pp)) ^ rsw) << 4), v[0], v[1], v[2], v[3]);
+                sts128(dst + ((((uint32_t)(2 * pp + 1)) ^ rsw) << 4), v[4], v[5], v[6], v[7]);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_FULL + 8 + us]);
+              sc = make_float4(sc.y, sc.z, sc.w, 0.f);
+              if (++cs == C::NK) { cs = 0; cphase ^= 1; }
+              if (++us == C::NV) { us = 0; uphase ^= 1; }
+            }
+          }
+          __syncwarp();
+        }
+      } else {
       // ------------------------------------------------------------------
       // row loads: a warp per 64-column chunk in flight, since a warp issues row
       // gathers one after another (about 80 cycles each).  Warp 12 + s owns K
@@ -552,6 +668,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
         __syncwarp();
       }
+      }
     } else if (warp == 10) {
       // ------------------------------------------------------------------
       // q of every request of the range, one box per swizzle column (rows b*H +
@@ -603,8 +720,31 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         }
         const int sb = it & 1;
         if (!poll(B_S_EMPTY + sb, ((it >> 1) & 1) ^ 1)) break;
+        if constexpr (F8) {
+          // the units that P.V reads too, which it gives back; then the RoPE chunk
 #pragma unroll 1
-        for (int c = 0; c < NC; ++c) {
+          for (int m = 0; m < 4; ++m) {
+            if (!poll(B_FULL + 8 + slot, phase)) { ok = false; break; }
+            tc_fence_after();
+            if (leader && m == 0) DSA_TRACE(a.tr, it, 3);
+            if (leader && m == 3) DSA_TRACE(a.tr, it, 4);
+            const uint64_t u = k_desc + (uint64_t)((C::OFF_V - C::OFF_K + slot * C::UNIT_BYTES) >> 4);
+            const uint64_t qd = q_desc + (uint64_t)(2 * m * (HB * 128) >> 4);
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, u, qd, 2u, 2u, IDESC, m > 0 ? 1u : 0u);
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, u + (C::CHUNK_BYTES >> 4), qd + (uint64_t)(HB * 128 >> 4), 2u,
+                           2u, IDESC, 1u);
+            if (++slot == C::NV) { slot = 0; phase ^= 1; }
+          }
+          if (ok && NC == 9) {
+            if (!poll(B_R_FULL, it & 1)) break;
+            tc_fence_after();
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)((C::OFF_R - C::OFF_K) >> 4),
+                           q_desc + (uint64_t)(8 * (HB * 128) >> 4), 2u, 2u, IDESC, 1u);
+            commit_elected(leader, &bars[B_R_EMPTY]);
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < (F8 ? 0 : NC); ++c) {
           if (!poll(B_FULL + slot, phase)) { ok = false; break; }
           tc_fence_after();
           if (leader && c == 0) DSA_TRACE(a.tr, it, 3);
@@ -984,31 +1124,35 @@ static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
 }
 
-template <int HB, int NC>
+template <int HB, int NC, bool F8>
 static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
-  using C = Cfg<HB, NC>;
+  using C = Cfg<HB, NC, F8>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(decode_kernel<HB, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
       return -1;
     attr_set[dev] = 1;
   }
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
-  return launch_after(decode_kernel<HB, NC>, dim3((unsigned)(a.groups * a.head_blocks)), NTHREADS, C::SMEM_BYTES, stream, a);
+  return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), NTHREADS, C::SMEM_BYTES, stream, a);
 }
 
 }  // namespace decode
 
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream) {
   using namespace decode;
-  if (fp8) return -2;
   const int hb = decode_heads_per_cta(a.H);
   int r = -2;
-  if (hb == 16) r = d_rope ? launch_t<16, 9>(a, stream) : launch_t<16, 8>(a, stream);
-  else r = d_rope ? launch_t<32, 9>(a, stream) : launch_t<32, 8>(a, stream);
+  if (hb == 16) {
+    if (fp8) r = d_rope ? launch_t<16, 9, true>(a, stream) : launch_t<16, 8, true>(a, stream);
+    else r = d_rope ? launch_t<16, 9, false>(a, stream) : launch_t<16, 8, false>(a, stream);
+  } else {
+    if (fp8) r = d_rope ? launch_t<32, 9, true>(a, stream) : launch_t<32, 8, true>(a, stream);
+    else r = d_rope ? launch_t<32, 9, false>(a, stream) : launch_t<32, 8, false>(a, stream);
+  }
   if (r != 0) return r;
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
   return launch_after(join_kernel, dim3((unsigned)(a.groups - 1), JOIN_Y), NT_JOIN, 0, stream, a, a.head_blocks * hb);

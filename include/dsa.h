@@ -483,7 +483,9 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
  * idx          DEVICE int32 [B, ld] or NULL; k <= ld.
  * out, lse     bf16 [B, H, 512] (16-byte aligned), fp32 [B, H].
  * workspace    DEVICE scratch, 256-byte aligned, of at least
- *              dsa_paged_decode_workspace(B, H) bytes.  Nothing in it has to
+ *              dsa_paged_decode_workspace(B, H, max_positions) bytes, where
+ *              max_positions is what the call's shapes allow one request: k
+ *              with idx, else max_blocks * block_size.  Nothing in it has to
  *              survive between calls or start at zero; calls that share it
  *              (captured graphs among them) must not overlap on the GPU.
  * A request without any valid key gets out = 0 and lse = -inf.  Positions
@@ -491,8 +493,10 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
  * -1 nor in [0, kv_lens[b]), are treated as absent and counted.  Cache rows
  * that no position names are never read into a result, whatever they hold.
  * Two kernels are queued on `stream` (one when no request can hold more than
- * 128 keys).  scale must be finite.  The same inputs give the same bits. */
-int64_t dsa_paged_decode_workspace(int B, int H);
+ * 128 keys).  scale must be finite.  The same inputs give the same bits.
+ * DSA_ERR_UNSUPPORTED also when B requests of max_positions have 2^31 tiles of
+ * 128 keys or more. */
+int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions);
 int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
                      const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
                      const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,

@@ -172,7 +172,7 @@ WS = 64 << 20
     (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(k=9), INVALID), (dict(k=-1), INVALID),
     (dict(q=None), INVALID), (dict(cache=None), INVALID), (dict(bt=None), INVALID), (dict(lens=None), INVALID),
     (dict(out=None), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID), (dict(ws=4096 + 128), INVALID),
-    (dict(wsb=1000), INVALID), (dict(q=4104), INVALID), (dict(cache=4104), INVALID), (dict(out=4104), INVALID),
+    (dict(wsb=100000), INVALID), (dict(q=4104), INVALID), (dict(cache=4104), INVALID), (dict(out=4104), INVALID),
     (dict(idx=4098), INVALID), (dict(lens=4097), INVALID), (dict(bt=4098), INVALID), (dict(lse=4098), INVALID),
     (dict(B=1 << 25, H=128), UNSUPPORTED), (dict(B=1 << 20, mb=1 << 20, bs=1 << 10, H=1, idx=None), UNSUPPORTED)])
 def test_decode_refusals(lib, change, want):
@@ -184,11 +184,14 @@ def test_decode_refusals(lib, change, want):
 
 
 def test_workspace_sizes(lib):
-    # two partial results per range, all heads padded to whole head blocks, plus their log-sum-exp and a little
-    for H, hp, groups in [(1, 16, 152), (16, 16, 152), (17, 32, 152), (32, 32, 152), (33, 64, 76), (128, 128, 38)]:
-        need = 2 * groups * hp * 4 * (512 + 1)
-        assert need <= dsa.dsa_paged_decode_workspace(4, H) < need + 4096
-    for bad in [(-1, 16), (1, 0), (1, 129)]:
+    # two partial results per range, all heads padded to whole head blocks, plus their log-sum-exp and a
+    # little; a range per SM and head block, but no more than there are tiles of 128 positions
+    for H, hp, most in [(1, 16, 152), (16, 16, 152), (17, 32, 152), (32, 32, 152), (33, 64, 76), (128, 128, 38)]:
+        for B, positions in [(1, 1), (1, 777), (4, 128), (3, 100000), (0, 5), (2, 0)]:
+            ranges = max(1, min(most, B * -(-positions // 128)))
+            need = 2 * ranges * hp * 4 * (512 + 1)
+            assert need <= dsa.dsa_paged_decode_workspace(B, H, positions) < need + 4096
+    for bad in [(-1, 16, 1), (1, 0, 1), (1, 129, 1), (1, 16, -1)]:
         with pytest.raises(dsa.DSAError):
             dsa.dsa_paged_decode_workspace(*bad)
 

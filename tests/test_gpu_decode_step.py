@@ -340,7 +340,7 @@ class Decode:
         assert (lerr <= ltol).all(), float((lerr / ltol).max())
 
 
-FMTS = ["bf16"]
+FMTS = ["bf16", "fp8"]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -442,7 +442,7 @@ def test_decode_same_bits_and_shared_workspace(fmt):
     """The same call twice, in a workspace full of NaN that another shape has used in between."""
     import dsa_sparse_mla_prefill_gb300 as dsa
     d, e = Decode(14, [3000, 777, 129], 32, fmt=fmt), Decode(15, [2500], 32, fmt=fmt)
-    ws = torch.full((dsa.dsa_paged_decode_workspace(3, 32),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((dsa.dsa_paged_decode_workspace(3, 32, d.bt.shape[1] * 16),), 255, dtype=torch.uint8, device="cuda")
     a = d.run(workspace=ws)
     e.check(e.run(workspace=ws))
     b = d.run(workspace=ws)
