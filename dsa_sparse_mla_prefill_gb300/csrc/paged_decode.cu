@@ -88,10 +88,10 @@ struct Cfg {
   static constexpr uint32_t OFF_ROWS = OFF_P + P_BYTES;
   static constexpr uint32_t OFF_META = OFF_ROWS + NI * BK * 4u;
   static constexpr uint32_t OFF_RED = OFF_META + NI * 16u;
-  static constexpr uint32_t OFF_BAR = OFF_RED + 2u * RED_FLOATS * 4u;   // two sums in the epilogue
+  static constexpr uint32_t OFF_BAR = OFF_RED + (2u * RED_FLOATS + HB) * 4u;   // (two sums and a factor per head in the epilogue)
   static constexpr int NBAR = 60;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
-  static constexpr uint32_t MISC_BYTES = 192u;
+  static constexpr uint32_t MISC_BYTES = 128u;
   static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024u;
   static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
   // TMEM columns: O^T double buffer (2 x 4 HB), S^T double buffer (2 x HB)
@@ -166,12 +166,18 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   }
 }
 
-// TMA loads of cache rows that mark their lines first to go from L2: the cache
-// is read once and larger than L2, and would otherwise push out the kernel's
-// own code and tables.
+// TMA loads with an L2 hint.  The rows of a tile are read twice, for K and then
+// for V: the first read caches them as usual, the second marks them first to go.
+// (Marked on the first read, a sixth to a third of them were gone by the second,
+// pushed out by each other while older lines of other tensors stayed.)
 __device__ __forceinline__ uint64_t evict_first_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t evict_normal_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 __device__ __forceinline__ void gather4_hint(uint32_t dst, const CUtensorMap* map, int x, const int4& r, uint64_t* bar,
@@ -320,9 +326,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* tmem_base_ptr = misc + 0;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  int* plan = reinterpret_cast<int*>(misc + 2);                     // tiles here, first request, its first tile, its length
+  volatile int* plan = reinterpret_cast<volatile int*>(misc + 2);   // tiles of this range
   volatile uint32_t* votes = misc + 16;                             // [parity][warpgroup][warp]
-  uint32_t* scan = misc + 32;                                       // [16] per-warp tile counts
   int32_t* rows = reinterpret_cast<int32_t*>(smem + C::OFF_ROWS);   // [NI][BK], -1 = masked
   int4* meta = reinterpret_cast<int4*>(smem + C::OFF_META);         // [NI] request, flags
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -386,52 +391,43 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     regs_dec<REGS_REST>();
     // what earlier kernels wrote may be read from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // ---- this group's range of tiles: every thread counts the tiles of a run
-    // of requests, a scan over the sixteen warps places the runs, and the run
-    // that holds the range's first tile names it
-    const int tid = threadIdx.x - 256;
-    const int per = (a.B + 511) / 512;
-    const int b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
-    uint32_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(a, __ldg(a.kv_lens + b));
-    uint32_t incl = warp_scan(mine);
-    if (lane == 31) scan[warp - 8] = incl;
-    named_bar_sync(1, 512);
-    const uint32_t all = warp_scan(lane < 16 ? scan[lane] : 0u);
-    const uint32_t total = __shfl_sync(0xffffffffu, all, 15);
-    const uint32_t ahead = __shfl_sync(0xffffffffu, all, (warp - 9) & 31);
-    const uint32_t before = (warp > 8 ? ahead : 0u) + incl - mine;
-    const uint32_t ng = total < (uint32_t)a.groups ? total : (uint32_t)a.groups;   // no group without a tile
-    const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
-    const uint32_t x1 = (uint32_t)range < ng ? range_begin(range + 1, total, ng) : 0;
-    if (tid == 0) {
-      plan[0] = (int)(x1 - x0);
-      if (range == 0 && hb == 0) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
-    }
-    if (x1 > x0 && before <= x0 && x0 < before + mine) {
-      uint32_t at = before;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const int len = __ldg(a.kv_lens + b);
-        const uint32_t n = tiles_of(a, len);
-        if (x0 < at + n) {
-          plan[1] = b;
-          plan[2] = (int)(x0 - at);
-          plan[3] = len;
-          break;
-        }
-        at += n;
-      }
-    }
-    named_bar_sync(1, 512);
-    if (tid == 0) mbar_arrive(&bars[B_PLAN]);
-    const int nt = plan[0];
     if (warp == 11) {
       // ------------------------------------------------------------------
       // scheduler
       // ------------------------------------------------------------------
+      // The range's tiles: every lane counts those of a run of requests, a scan
+      // places the runs, and the lane whose run holds the first tile finds it.
+      const int per = (a.B + 31) / 32;
+      const int b_lo = min(a.B, lane * per), b_hi = min(a.B, b_lo + per);
+      uint32_t mine = 0;
+#pragma unroll 4
+      for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(a, __ldg(a.kv_lens + i));
+      const uint32_t incl = warp_scan(mine), total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+      const uint32_t ng = total < (uint32_t)a.groups ? total : (uint32_t)a.groups;   // no range without a tile
+      const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
+      const int nt = (uint32_t)range < ng ? (int)(range_begin(range + 1, total, ng) - x0) : 0;
+      if (lane == 0) {
+        *plan = nt;
+        mbar_arrive(&bars[B_PLAN]);
+        if (range == 0 && hb == 0) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
+      }
+      int b = 0, j = 0, len = 0, n = 0;
+      const bool holds = nt > 0 && before <= x0 && x0 < before + mine;
+      if (holds) {
+        uint32_t at = before;
+        for (b = b_lo;; ++b) {
+          len = __ldg(a.kv_lens + b);
+          n = tiles_of(a, len);
+          if (x0 < at + n) break;
+          at += n;
+        }
+        j = (int)(x0 - at);
+      }
+      const int holder = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+      b = __shfl_sync(0xffffffffu, b, holder & 31);
+      j = __shfl_sync(0xffffffffu, j, holder & 31);
+      len = __shfl_sync(0xffffffffu, len, holder & 31);
       int bad = 0;
-      int b = nt > 0 ? plan[1] : 0, j = nt > 0 ? plan[2] : 0;
-      int len = nt > 0 ? plan[3] : 0, n = 0;
       const bool from_start = j == 0;   // the range's first request begins in it
       bool enter = true;                // the next tile is the first of request b here
       int seg = 0;                    // requests begun
@@ -507,7 +503,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       }
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
-    } else if (warp >= 12) {
+    } else if (const int nt = poll(B_PLAN, 0) ? *plan : 0; warp >= 12) {
       if constexpr (F8) {
         // ----------------------------------------------------------------
         // FP8 rows.  Warp 12 + s owns code slot s and loads 128-code blocks into
@@ -632,7 +628,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         const int empty = B_EMPTY + (ks ? 0 : 8) + mine_slot;
         const int col_step = ks ? 64 : 128;
         const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
-        const uint64_t policy = evict_first_policy();
+        const uint64_t policy = ks ? evict_normal_policy() : evict_first_policy();
         int slot = 0;
         uint32_t used = 0;   // phases of the slot so far
         bool ok = true;
@@ -829,30 +825,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     float m_run[HT], l_exact[HT], l_used[HT];
 #pragma unroll
     for (int h = 0; h < HT; ++h) { m_run[h] = -FLT_MAX; l_exact[h] = 0.f; l_used[h] = 0.f; }
-    // Tile -1 is a rehearsal on whatever tensor memory holds, storing nothing
-    // outside this CTA's own scratch: it brings the loop's code in while the
-    // first rows are on their way.
-    int nt = 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int nt = poll(B_PLAN, 0) ? *plan : 0;
 #pragma unroll 1
-    for (int it = -1; it < nt; ++it) {
-      const bool dry = it < 0;
-      if (it == 0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (!poll(B_PLAN, 0)) break;
-        nt = plan[0];
-        if (nt == 0) break;
-      }
+    for (int it = 0; it < nt; ++it) {
       const int r = it & (NI - 1);
       const int sb = it & 1;
-      bool valid = true;
-      int4 mt = make_int4(0, F_LAST | F_PART, 0, 0);
-      if (!dry) {
-        if (!poll(B_IDX_FULL + r, (it / NI) & 1)) break;
-        valid = rows[r * BK + key] >= 0;
-        mt = meta[r];
-        if (!poll(B_S_FULL + sb, (it >> 1) & 1)) break;
-        if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 5);
-      }
+      if (!poll(B_IDX_FULL + r, (it / NI) & 1)) break;
+      const bool valid = rows[r * BK + key] >= 0;
+      const int4 mt = meta[r];
+      if (!poll(B_S_FULL + sb, (it >> 1) & 1)) break;
+      if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 5);
       if (mt.y & F_FIRST) {
         ++seg;
 #pragma unroll
@@ -864,7 +847,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       tmem_ld_n<HT>(t_lane + C::COL_S + sb * HB, s);
       tmem_ld_wait();
       tc_fence_before();
-      if (!dry) mbar_arrive(&bars[B_S_EMPTY + sb]);
+      mbar_arrive(&bars[B_S_EMPTY + sb]);
       float top = -FLT_MAX;
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
@@ -874,37 +857,34 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       // Lazy rescale: a warp with a score above the running max by more than
       // kTau publishes its per-head max; the new reference is the max over
       // those warps, which bounds every score of the tile to within 2^kTau.
+      // (One that does not ask publishes the lowest value.)
       // (A masked key's row is zeros, its score 0: it never asks.)
-      const bool wneed = dry || __any_sync(0xffffffffu, valid && top > kTau);
+      const bool wneed = __any_sync(0xffffffffu, valid && top > kTau);
       float* redb = red + (sb * 2 + wg) * (4 * HT);
       volatile uint32_t* vote = votes + (sb * 2 + wg) * 4;
+      float wmax = -FLT_MAX;
       if (wneed) {
         float x[HT];
 #pragma unroll
         for (int h = 0; h < HT; ++h) x[h] = valid ? s[h] * scale_log2 : -FLT_MAX;
-        const float wmax = warp_transpose_reduce<HT, true>(x);
-        if (lane < HT) redb[w4 * HT + lane] = wmax;
+        wmax = warp_transpose_reduce<HT, true>(x);
       }
+      if (lane < HT) redb[w4 * HT + lane] = wmax;
       if (lane == 0) vote[w4] = wneed ? 1u : 0u;
       if (!group()) break;
-      if (key == 0 && !dry) mbar_arrive(&bars[B_IDX_EMPTY + r]);   // (every thread of the warpgroup has read the tile's rows)
-      uint32_t need = 0;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) need |= vote[w] << w;
+      if (key == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);   // (every thread of the warpgroup has read the tile's rows)
+      const uint32_t need = vote[0] | vote[1] | vote[2] | vote[3];
       if (need) {
-        // (the old reference takes part as the warps that did not vote)
 #pragma unroll
         for (int h = 0; h < HT; h += 4) {
           float mn[4] = {m_run[h], m_run[h + 1], m_run[h + 2], m_run[h + 3]};
-#pragma unroll 1
+#pragma unroll
           for (int w = 0; w < 4; ++w) {
             const float4 x = *reinterpret_cast<const float4*>(redb + w * HT + h);
-            if (need >> w & 1) {
-              mn[0] = fmaxf(mn[0], x.x);
-              mn[1] = fmaxf(mn[1], x.y);
-              mn[2] = fmaxf(mn[2], x.z);
-              mn[3] = fmaxf(mn[3], x.w);
-            }
+            mn[0] = fmaxf(mn[0], x.x);
+            mn[1] = fmaxf(mn[1], x.y);
+            mn[2] = fmaxf(mn[2], x.z);
+            mn[3] = fmaxf(mn[3], x.w);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -929,7 +909,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         pk[h / 2] = w;
       }
       // the previous P.V must be done before P is overwritten or O rescaled
-      if (!dry && !poll(B_P_EMPTY, sb ^ 1)) break;
+      if (!poll(B_P_EMPTY, sb ^ 1)) break;
       tc_fence_after();
       if (need && !(mt.y & F_FIRST)) {
 #pragma unroll 1
@@ -952,8 +932,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
             (uint16_t)((h & 1) ? (pk[h / 2] >> 16) : (pk[h / 2] & 0xffffu));
       fence_proxy_async_smem();
       tc_fence_before();
-      if (!dry) mbar_arrive(&bars[B_P_FULL]);
-      if (threadIdx.x == 0 && !dry) DSA_TRACE(a.tr, it, 6);
+      mbar_arrive(&bars[B_P_FULL]);
+      if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
       if (!(mt.y & F_LAST)) continue;
 
       // ---- epilogue of the request's part in this range: the warps' sums, then
@@ -964,6 +944,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       const float us = warp_transpose_reduce<HT, false>(l_used);
       float* redx = red + ((sb ^ 1) * 2 + wg) * (4 * HT);
       float* redu = redx + C::RED_FLOATS;
+      float* redi = red + 2 * C::RED_FLOATS + wg * HT;
       // the running max is the same in every thread: lane h keeps head h's
       float mine = 0.f;
 #pragma unroll
@@ -976,23 +957,33 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       const bool part = (mt.y & F_PART) != 0;
       const uint32_t row0 = (uint32_t)(2 * range + ((mt.y & F_SLOT1) ? 1 : 0)) * (uint32_t)heads_padded + head0;   // of the parts
       const int left = heads - wg * HT;                                         // heads to store
-      float inv = 0.f;
       if (lane < HT) {
         const float lx = (redx[lane] + redx[HT + lane]) + (redx[2 * HT + lane] + redx[3 * HT + lane]);
         const float lu = (redu[lane] + redu[HT + lane]) + (redu[2 * HT + lane] + redu[3 * HT + lane]);
-        inv = (lu != 0.f) ? 1.0f / lu : 0.f;
-        if (w4 == 0 && lane < left && !dry) {
-          const float l2 = (lx != 0.f) ? mine + log2f(lx) : -INFINITY;
-          if (part)
-            a.part_lse[row0 + wg * HT + lane] = l2;
-          else
-            a.lse[(int64_t)mt.x * a.H + head0 + wg * HT + lane] = l2 * 0.6931471805599453f;
+        if (w4 == 0) {
+          redi[lane] = (lu != 0.f) ? 1.0f / lu : 0.f;
+          if (lane < left) {
+            const float l2 = (lx != 0.f) ? mine + log2f(lx) : -INFINITY;
+            if (part)
+              a.part_lse[row0 + wg * HT + lane] = l2;
+            else
+              a.lse[(int64_t)mt.x * a.H + head0 + wg * HT + lane] = l2 * 0.6931471805599453f;
+          }
         }
       }
       // (the next tile's vote and reduction use that scratch again)
       if (!group()) break;
-      if (!dry && !poll(B_O_FULL + ob, (seg >> 1) & 1)) break;
+      if (!poll(B_O_FULL + ob, (seg >> 1) & 1)) break;
       tc_fence_after();
+      float inv[HT];
+#pragma unroll
+      for (int h = 0; h < HT; h += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(redi + h);
+        inv[h] = x.x;
+        inv[h + 1] = x.y;
+        inv[h + 2] = x.z;
+        inv[h + 3] = x.w;
+      }
       uint16_t* out = a.out + ((int64_t)mt.x * a.H + head0 + wg * HT) * 512 + key;
       float* po = a.part_o + (int64_t)(row0 + wg * HT) * 512 + key;
 #pragma unroll 1
@@ -1002,8 +993,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-          const float v = o[h] * __shfl_sync(0xffffffffu, inv, h);
-          if (h < left && !dry) {
+          const float v = o[h] * inv[h];
+          if (h < left) {
             if (part)
               po[h * 512] = v;
             else
@@ -1014,7 +1005,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         out += 128;
       }
       tc_fence_before();
-      if (!dry) mbar_arrive(&bars[B_O_EMPTY + ob]);
+      mbar_arrive(&bars[B_O_EMPTY + ob]);
     }
   }
 
@@ -1030,16 +1021,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
 //
 // The borders inside one request share its heads' outputs evenly, JOIN_Y CTAs to
 // a border, so one long context and a cut batch are both joined by as many CTAs
-// as there is work for.  A piece is 128 float4 outputs (a head), a thread each;
-// with eight parts or more 32 of them with a warp per quarter of the parts.  The
-// loads of the parts do not wait for the weights.  Small CTAs (128 threads of 32
-// registers fit beside a CTA of the first kernel), so that they are in place when
-// it ends.  The parts are summed in order, whatever CTA stored them first.
+// as there is work for.  The threads of a CTA stand 128 / G wide over float4
+// outputs of a head and G deep over the parts, G = 1, 4 or 16 by their number, so
+// that a thread sums about ten; the loads of the parts do not wait for the
+// weights.  The parts are summed in one order, whatever CTA stored them first.
 // --------------------------------------------------------------------------
 constexpr int NT_JOIN = 128;
 constexpr int JOIN_Y = 8;
 
-__global__ void __launch_bounds__(NT_JOIN, 16) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
+__global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
   __shared__ float4 acc[3][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1054,58 +1044,87 @@ __global__ void __launch_bounds__(NT_JOIN, 16) join_kernel(const __grid_constant
   const int g0 = (int)range_of(p0, total, ng), g1 = (int)range_of(p0 + at.y - 1, total, ng);
   const int S = g1 - g0 + 1, nb = S - 1, rank = (int)g - g0;
   const int first_slot = 2 * g0 + (range_begin(g0, total, ng) == p0 ? 0 : 1);
-  const bool wide = S >= 8;
-  const int pieces = wide ? a.H * 4 : a.H;
+  const int lg = S < 8 ? 0 : (S < 32 ? 2 : 4);          // log2 of G
+  const int wide = 128 >> lg;                           // float4 outputs of a piece
+  const int pieces = a.H << lg;
   const int c0 = pieces * rank / nb, c1 = pieces * (rank + 1) / nb;
   const uint32_t pitch = (uint32_t)heads_padded;        // heads of a slot (all offsets are below 2^23)
-  const int s0 = wide ? S * warp / 4 : 0, s1 = wide ? S * (warp + 1) / 4 : S;
+  const int deep = (int)threadIdx.x >> (7 - lg);
+  const int s0 = (S * deep) >> lg, s1 = (S * (deep + 1)) >> lg;
 #pragma unroll 1
   for (int c = c0 + (int)blockIdx.y; c < c1; c += JOIN_Y) {
-    const int h = wide ? c >> 2 : c;
-    const int i = wide ? (c & 3) * 32 + lane : (int)threadIdx.x;   // float4 of the head
+    const int h = c >> lg;
+    const int i = (c & ((1 << lg) - 1)) * wide + ((int)threadIdx.x & (wide - 1));   // float4 of the head
     const float* pl = a.part_lse + h;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + h * 128 + i;
+    auto slot_of = [&](int s) { return (uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch; };
+    constexpr int AHEAD = 4;
+    float4 v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) v[k] = src[slot_of(min(s0 + k, s1 - 1)) * 128];
     float m = -INFINITY;
-#pragma unroll 1
-    for (int s = lane; s < S; s += 32) m = fmaxf(m, pl[(uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch]);
+#pragma unroll 5
+    for (int s = lane; s < S; s += 32) m = fmaxf(m, pl[slot_of(s)]);
     m = warp_max(m);
     const float mr = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll 1
-    for (int s = lane; s < S; s += 32) sum += exp2f(pl[(uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch] - mr);
+    for (int s = lane; s < S; s += 32) sum += exp2f(pl[slot_of(s)] - mr);
     sum = warp_sum(sum);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + h * 128 + i;
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-      const uint32_t slot = (uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch;
-      const float4 v = src[slot * 128];
-      const float w = exp2f(pl[slot] - mr);
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
+#pragma unroll 1
+    for (int s = s0; s < s1; s += AHEAD) {
+      float w[AHEAD];
+      float4 x[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        w[k] = exp2f(pl[slot_of(min(s + k, s1 - 1))] - mr);
+        x[k] = v[k];
+      }
+      if (s + AHEAD < s1) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) v[k] = src[slot_of(min(s + AHEAD + k, s1 - 1)) * 128];
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (s + k < s1) {
+          o.x += w[k] * x[k].x;
+          o.y += w[k] * x[k].y;
+          o.z += w[k] * x[k].z;
+          o.w += w[k] * x[k].w;
+        }
+      }
     }
-    if (wide) {
+    if (lg == 4) {   // four depths in a warp
+#pragma unroll
+      for (int d = 8; d <= 16; d <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+      }
+    }
+    if (lg > 0) {
       if (warp > 0) acc[warp - 1][lane] = o;
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-          const float4 v = acc[q][lane];
-          o.x += v.x;
-          o.y += v.y;
-          o.z += v.z;
-          o.w += v.w;
+          const float4 y = acc[q][lane];
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
         }
       }
     }
-    if (!wide || warp == 0)
+    if ((int)threadIdx.x < wide)
       *reinterpret_cast<uint2*>(a.out + (b * a.H + h) * 512 + 4 * i) =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (threadIdx.x == 0 && i == 0)
       a.lse[b * a.H + h] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    if (wide) __syncthreads();
+    if (lg > 0) __syncthreads();
   }
 }
 
