@@ -58,13 +58,17 @@ constexpr int BK = 128;          // keys per tile (the MMA's M)
 constexpr int NTHREADS = 768;
 constexpr int NI = 4;            // tiles of rows ahead
 constexpr float kTau = 8.0f;     // lazy-rescale threshold (log2 units)
-// 768 threads launched at 80 registers: 256 * 144 + 512 * 48 = 768 * 80
-constexpr int REGS_SOFTMAX = 144;
-constexpr int REGS_REST = 48;
+// 768 threads launched at 80 registers
+constexpr int REGS_LAUNCH = 80;
 
 template <int HB, int NC, bool F8>
 struct Cfg {
   static constexpr int HT = HB / 2;                      // heads per softmax thread
+  // registers of the eight softmax warps and of the others (converters of FP8
+  // rows want room for several conversions at once)
+  static constexpr int REGS_SOFTMAX = F8 ? (HB == 16 ? 96 : 128) : 144;
+  static constexpr int REGS_REST = F8 ? (HB == 16 ? 72 : 56) : 48;
+  static_assert(256 * REGS_SOFTMAX + 512 * REGS_REST <= NTHREADS * REGS_LAUNCH, "registers");
   // What shared memory leaves beside q and P.  bf16 rows: a ring of NK 64-column
   // K chunks and one of NV 128-column V units.  FP8 rows: NK slots of codes (128
   // rows x 128), NV units of converted columns that QK and P.V both read, and a
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) {
-    regs_dec<REGS_REST>();
+    regs_dec<C::REGS_REST>();
     // what earlier kernels wrote may be read from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 11) {
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
             next = scales(it + 1);
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
-              if (!doze(B_FULL + cs, cphase) || !doze(B_EMPTY + 8 + us, uphase)) { ok = false; break; }
+              if (!poll(B_FULL + cs, cphase) || !poll(B_EMPTY + 8 + us, uphase)) { ok = false; break; }
               const uint32_t src = sbase + C::OFF_K + cs * C::CHUNK_BYTES + row * 128;
               const uint32_t dst = sbase + C::OFF_V + us * C::UNIT_BYTES + hf * C::CHUNK_BYTES + row * 128;
               uint4 w[4];
@@ -717,7 +721,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         const int sb = it & 1;
         if (!poll(B_S_EMPTY + sb, ((it >> 1) & 1) ^ 1)) break;
         if constexpr (F8) {
-          // the units that P.V reads too, which it gives back; then the RoPE chunk
+          if constexpr (NC == 9) {
+            if (!poll(B_R_FULL, it & 1)) break;
+            tc_fence_after();
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)((C::OFF_R - C::OFF_K) >> 4),
+                           q_desc + (uint64_t)(8 * (HB * 128) >> 4), 2u, 2u, IDESC, 0u);
+            commit_elected(leader, &bars[B_R_EMPTY]);
+          }
+          // the units that P.V reads too, which it gives back
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
             if (!poll(B_FULL + 8 + slot, phase)) { ok = false; break; }
@@ -726,17 +737,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
             if (leader && m == 3) DSA_TRACE(a.tr, it, 4);
             const uint64_t u = k_desc + (uint64_t)((C::OFF_V - C::OFF_K + slot * C::UNIT_BYTES) >> 4);
             const uint64_t qd = q_desc + (uint64_t)(2 * m * (HB * 128) >> 4);
-            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, u, qd, 2u, 2u, IDESC, m > 0 ? 1u : 0u);
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, u, qd, 2u, 2u, IDESC, (NC == 9 || m > 0) ? 1u : 0u);
             mma_x4_elected(leader, tmem + C::COL_S + sb * HB, u + (C::CHUNK_BYTES >> 4), qd + (uint64_t)(HB * 128 >> 4), 2u,
                            2u, IDESC, 1u);
             if (++slot == C::NV) { slot = 0; phase ^= 1; }
-          }
-          if (ok && NC == 9) {
-            if (!poll(B_R_FULL, it & 1)) break;
-            tc_fence_after();
-            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)((C::OFF_R - C::OFF_K) >> 4),
-                           q_desc + (uint64_t)(8 * (HB * 128) >> 4), 2u, 2u, IDESC, 1u);
-            commit_elected(leader, &bars[B_R_EMPTY]);
           }
         }
 #pragma unroll 1
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       __syncwarp();
     }
   } else {
-    regs_inc<REGS_SOFTMAX>();
+    regs_inc<C::REGS_SOFTMAX>();
     // --------------------------------------------------------------------
     // softmax and epilogue: thread = key (TMEM lane), warpgroup wg = heads
     // wg*HT .. wg*HT + HT - 1
