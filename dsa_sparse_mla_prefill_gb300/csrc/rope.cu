@@ -155,9 +155,12 @@ template <typename E, bool HALF, bool VEC>
 static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int PPT = pairs_per_thread<E, HALF, VEC>();
   const int64_t per_group = (int64_t)a.T * (a.d / (2 * PPT));   // threads of one head group
-  // enough threads for every SM's 2048 slots, no more groups than heads
-  const int64_t want = (2048ll * num_sms + per_group - 1) / per_group;
-  a.head_groups = (int)(want < a.H ? want : a.H);
+  // as many heads per thread, in powers of two, as leave threads for every
+  // SM's 2048 slots (16384 tokens of 32 heads: 8 each, 25.7 us; 11 each 27.3,
+  // 4 each 27.0, 2 each 36.6, the cos and sin being worked out per thread)
+  int each = 1;
+  while (2 * each <= a.H && (a.H + 2 * each - 1) / (2 * each) * per_group >= 2048ll * num_sms) each *= 2;
+  a.head_groups = (a.H + each - 1) / each;
   const int64_t blocks = (per_group * a.head_groups + NT - 1) / NT;
   if (blocks * NT > 0xffffffffll) return -2;
   rope_kernel<E, HALF, VEC><<<(unsigned)blocks, NT, 0, stream>>>(a);
@@ -176,11 +179,11 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
 // block of the row each (lane l: columns 4l .. 4l+3, the layout of the block
 // quantization), warp 4 the RoPE columns (lane = pair), so that the RoPE
 // arithmetic runs beside the copy; ROWS tokens per CTA have their loads in
-// flight together (4 for a prompt chunk; 1 while the tokens do not fill the
+// flight together (2 for a prompt chunk; 1 while the tokens do not fill the
 // GPU, where more CTAs are worth more than more loads per thread).
 // --------------------------------------------------------------------------
 constexpr int NT_APPEND = 160;
-constexpr int ROWS_LONG = 4;
+constexpr int ROWS_LONG = 2;
 
 // The physical row of token t, or -1 (a padding token, or a bad entry: *bad).
 __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int t, int32_t& pos, bool& bad) {
@@ -203,15 +206,19 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
   const int t0 = blockIdx.x * ROWS;
   int64_t row[ROWS];
   int32_t pos[ROWS];
+  // (called once the token's own data is on its way: the two loads behind each
+  // other that find the row then overlap it)
+  auto find_rows = [&]() {
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    row[r] = -1;
-    if (t0 + r < a.T) {
-      bool bad;
-      row[r] = row_of(a, t0 + r, pos[r], bad);
-      if (bad && threadIdx.x == 0) atomicAdd(a.err + ERR_BAD_INDEX, 1u);
+    for (int r = 0; r < ROWS; ++r) {
+      row[r] = -1;
+      if (t0 + r < a.T) {
+        bool bad;
+        row[r] = row_of(a, t0 + r, pos[r], bad);
+        if (bad && threadIdx.x == 0) atomicAdd(a.err + ERR_BAD_INDEX, 1u);
+      }
     }
-  }
+  };
   uint8_t* cache = static_cast<uint8_t*>(a.cache);
   const int64_t row_bytes = F8 ? 528 + 2 * a.d_rope : 2ll * a.ld_kv;
   if (w < 4) {
@@ -219,9 +226,10 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       raw[r] = make_uint2(0, 0);
-      if (row[r] >= 0)
+      if (t0 + r < a.T)
         raw[r] = *reinterpret_cast<const uint2*>(a.c_kv + (int64_t)(t0 + r) * a.c_stride + 128 * w + 4 * lane);
     }
+    find_rows();
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (row[r] < 0) continue;   // (uniform over the CTA)
@@ -242,12 +250,13 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       p[r] = q[r] = 0;
-      if (row[r] >= 0) {
+      if (t0 + r < a.T) {
         const uint16_t* src = a.k_pe + (int64_t)(t0 + r) * a.pe_stride;
         p[r] = src[lo];
         q[r] = src[up];
       }
     }
+    find_rows();
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (row[r] < 0) continue;
