@@ -696,6 +696,7 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   a.ld = ld;
   a.max_blocks = max_blocks;
   a.block_size = block_size;
+  a.cap = (int)((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
   a.scale = scale;
   a.tr = g_trace;
   a.head_blocks = dsa::decode_head_blocks(H);

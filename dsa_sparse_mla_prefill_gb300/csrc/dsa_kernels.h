@@ -113,6 +113,7 @@ struct DecodeArgs {
   float* part_lse;            // [2 groups][heads padded] their log-sum-exp, base 2
   unsigned int* err;
   int B, H, N, k, ld, max_blocks, block_size;
+  int cap;                    // positions that the block table has room for
   int groups;                 // CTA groups (each of head_blocks CTAs)
   int head_blocks;            // CTAs of a group, each with its own heads
   float scale;

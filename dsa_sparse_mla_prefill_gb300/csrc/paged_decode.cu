@@ -133,10 +133,7 @@ constexpr int F_BOX = 16;     // every key there, in runs of box_rows rows: load
 // key tiles of a request
 __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
   if (len <= 0) return 0;
-  if (a.idx != nullptr) return (a.k + BK - 1) / BK;
-  const int64_t cap = (int64_t)a.max_blocks * a.block_size;
-  const uint32_t n = len < cap ? (uint32_t)len : (uint32_t)cap;
-  return (int)((n + BK - 1) / BK);
+  return ((uint32_t)(a.idx != nullptr ? a.k : min(len, a.cap)) + BK - 1) / BK;
 }
 
 // Bounded waits, kept small: a launch runs its code cold, and every line of it
@@ -346,34 +343,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
   const int range = blockIdx.x / a.head_blocks;   // the CTA group
   const int hb = blockIdx.x - range * a.head_blocks;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NI; ++i) {
-      mbar_init(&bars[B_IDX_FULL + i], 1);
-      // 2 MMA warps, 2 softmax warpgroups, the producer warps, the q loader
-      mbar_init(&bars[B_IDX_EMPTY + i], 2 + 2 + C::NPROD + 1);
-    }
-    mbar_init(&bars[B_Q_FULL], 1);
-    mbar_init(&bars[B_Q_EMPTY], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[B_S_FULL + i], 1);
-      mbar_init(&bars[B_S_EMPTY + i], 256);
-      mbar_init(&bars[B_O_FULL + i], 1);
-      mbar_init(&bars[B_O_EMPTY + i], 256);
-      mbar_init(&bars[B_SMX + i], 128);
-      mbar_init(&bars[B_DRAIN + i], 1);
-    }
-    mbar_init(&bars[B_PLAN], 1);
-    mbar_init(&bars[B_P_FULL], 256);
-    mbar_init(&bars[B_P_EMPTY], 1);
-    for (int i = 0; i < 16; ++i) {
+  if (warp == 0) {
+    // a lane per barrier and round: sixty of them one after another by one
+    // thread are 700 cycles
+    for (int i = lane; i < C::NBAR; i += 32) {
+      uint32_t n = 1;
+      // 2 MMA warps, 2 softmax warpgroups, the loading (converting) warps, the q loader
+      if (i >= B_IDX_EMPTY && i < B_IDX_EMPTY + NI) n = 2 + 2 + C::NPROD + 1;
+      if (i == B_S_EMPTY || i == B_S_EMPTY + 1 || i == B_O_EMPTY || i == B_O_EMPTY + 1 || i == B_P_FULL) n = 256;
+      if (i == B_SMX || i == B_SMX + 1) n = 128;
       // a V unit is two loading warps' work; codes are read, and units of FP8
       // rows filled, by eight converting warps
-      mbar_init(&bars[B_FULL + i], i < 8 ? 1 : (F8 ? 8 : 2));
-      mbar_init(&bars[B_EMPTY + i], F8 && i < 8 ? 8 : 1);
+      if (i >= B_FULL + 8 && i < B_FULL + 16) n = F8 ? 8 : 2;
+      if (F8 && i >= B_EMPTY && i < B_EMPTY + 8) n = 8;
+      mbar_init(&bars[i], n);
     }
-    mbar_init(&bars[B_R_FULL], 1);
-    mbar_init(&bars[B_R_EMPTY], 1);
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 4) {
@@ -435,7 +420,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       const bool from_start = j == 0;   // the range's first request begins in it
       bool enter = true;                // the next tile is the first of request b here
       int seg = 0;                    // requests begun
-      const int64_t cap = (int64_t)a.max_blocks * a.block_size;
       for (int it = 0; it < nt; ++it) {
         const int r = it % NI;
         if (enter) {
@@ -446,9 +430,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
             if (n > 0) break;
             ++b;
           }
-          if (len > cap) {
+          if (len > a.cap) {
             if (j == 0 && lane == 0) ++bad;
-            len = (int)cap;
+            len = a.cap;
           }
         }
         if (!doze(B_IDX_EMPTY + r, ((it / NI) & 1) ^ 1)) break;
@@ -1024,17 +1008,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
 // request (L_s base-2 log-sum-exp, O_s normalised), lse = M + log2 of that sum.
 //
 // The borders inside one request share its heads' outputs evenly, JOIN_Y CTAs to
-// a border, so one long context and a cut batch are both joined by as many CTAs
+// a border and head block, so one long context and a cut batch are both joined by as many CTAs
 // as there is work for.  The threads of a CTA stand 128 / G wide over float4
 // outputs of a head and G deep over the parts, G = 1, 4 or 16 by their number, so
-// that a thread sums about ten; the loads of the parts do not wait for the
-// weights.  The parts are summed in one order, whatever CTA stored them first.
+// that a thread has ten at most: it loads them all at once, beside the
+// log-sum-exps that weight them.  The parts are summed in one order, whatever CTA
+// stored them first.
 // --------------------------------------------------------------------------
 constexpr int NT_JOIN = 128;
-constexpr int JOIN_Y = 8;
+constexpr int JOIN_Y = 8;          // CTAs per border and head block
+constexpr int MOST = 10;           // parts of a thread
+constexpr int LSE = 5;             // of a lane
+static_assert(kDecodeMaxCtas <= 16 * (MOST - 1) + 15 && kDecodeMaxCtas <= 32 * LSE, "parts of a request");
 
 __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
   __shared__ float4 acc[3][32];
+  __shared__ float wgt[4][32 * LSE];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1055,49 +1044,41 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   const uint32_t pitch = (uint32_t)heads_padded;        // heads of a slot (all offsets are below 2^23)
   const int deep = (int)threadIdx.x >> (7 - lg);
   const int s0 = (S * deep) >> lg, s1 = (S * (deep + 1)) >> lg;
+  auto slot_of = [&](int s) { return (uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch; };
 #pragma unroll 1
-  for (int c = c0 + (int)blockIdx.y; c < c1; c += JOIN_Y) {
+  for (int c = c0 + (int)blockIdx.y; c < c1; c += (int)gridDim.y) {
     const int h = c >> lg;
     const int i = (c & ((1 << lg) - 1)) * wide + ((int)threadIdx.x & (wide - 1));   // float4 of the head
-    const float* pl = a.part_lse + h;
     const float4* src = reinterpret_cast<const float4*>(a.part_o) + h * 128 + i;
-    auto slot_of = [&](int s) { return (uint32_t)(s == 0 ? first_slot : 2 * (g0 + s)) * pitch; };
-    constexpr int AHEAD = 4;
-    float4 v[AHEAD];
+    float4 v[MOST];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) v[k] = src[slot_of(min(s0 + k, s1 - 1)) * 128];
-    float m = -INFINITY;
-#pragma unroll 5
-    for (int s = lane; s < S; s += 32) m = fmaxf(m, pl[slot_of(s)]);
+    for (int k = 0; k < MOST; ++k) v[k] = s0 + k < s1 ? src[slot_of(s0 + k) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float l[LSE], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < LSE; ++k) l[k] = lane + 32 * k < S ? a.part_lse[slot_of(lane + 32 * k) + h] : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < LSE; ++k) m = fmaxf(m, l[k]);
     m = warp_max(m);
     const float mr = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-#pragma unroll 1
-    for (int s = lane; s < S; s += 32) sum += exp2f(pl[slot_of(s)] - mr);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < LSE; ++k) {
+      l[k] = exp2f(l[k] - mr);
+      sum += l[k];
+      wgt[warp][lane + 32 * k] = l[k];
+    }
+    __syncwarp();
     sum = warp_sum(sum);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int s = s0; s < s1; s += AHEAD) {
-      float w[AHEAD];
-      float4 x[AHEAD];
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        w[k] = exp2f(pl[slot_of(min(s + k, s1 - 1))] - mr);
-        x[k] = v[k];
-      }
-      if (s + AHEAD < s1) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) v[k] = src[slot_of(min(s + AHEAD + k, s1 - 1)) * 128];
-      }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        if (s + k < s1) {
-          o.x += w[k] * x[k].x;
-          o.y += w[k] * x[k].y;
-          o.z += w[k] * x[k].z;
-          o.w += w[k] * x[k].w;
-        }
+    for (int k = 0; k < MOST; ++k) {
+      if (s0 + k < s1) {
+        const float w = wgt[warp][s0 + k];
+        o.x += w * v[k].x;
+        o.y += w * v[k].y;
+        o.z += w * v[k].z;
+        o.w += w * v[k].w;
       }
     }
     if (lg == 4) {   // four depths in a warp
@@ -1178,7 +1159,7 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   }
   if (r != 0) return r;
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
-  return launch_after(join_kernel, dim3((unsigned)(a.groups - 1), JOIN_Y), NT_JOIN, 0, stream, a, a.head_blocks * hb);
+  return launch_after(join_kernel, dim3((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks)), NT_JOIN, 0, stream, a, a.head_blocks * hb);
 }
 
 }  // namespace dsa
