@@ -1011,16 +1011,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
 // a border and head block, so one long context and a cut batch are both joined by as many CTAs
 // as there is work for.  The threads of a CTA stand 128 / G wide over float4
 // outputs of a head and G deep over the parts, G = 1, 4 or 16 by their number, so
-// that a thread has ten at most: it loads them all at once, beside the
-// log-sum-exps that weight them.  The parts are summed in one order, whatever CTA
+// that a thread has ten at most.  It loads MOST of them at once, the first ones
+// beside the log-sum-exps that weight them: 10 where few requests are cut into
+// many parts (a context of 131072 positions: 40 against 44 us with 5), else 5,
+// whose registers leave room for more CTAs (64 ragged requests: 72 against 74).  The parts are summed in one order, whatever CTA
 // stored them first.
 // --------------------------------------------------------------------------
 constexpr int NT_JOIN = 128;
 constexpr int JOIN_Y = 8;          // CTAs per border and head block
-constexpr int MOST = 10;           // parts of a thread
 constexpr int LSE = 5;             // of a lane
-static_assert(kDecodeMaxCtas <= 16 * (MOST - 1) + 15 && kDecodeMaxCtas <= 32 * LSE, "parts of a request");
+static_assert(kDecodeMaxCtas <= 32 * LSE, "parts of a request");
 
+template <int MOST>
 __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ DecodeArgs a, int heads_padded) {
   __shared__ float4 acc[3][32];
   __shared__ float wgt[4][32 * LSE];
@@ -1037,7 +1039,7 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   const int g0 = (int)range_of(p0, total, ng), g1 = (int)range_of(p0 + at.y - 1, total, ng);
   const int S = g1 - g0 + 1, nb = S - 1, rank = (int)g - g0;
   const int first_slot = 2 * g0 + (range_begin(g0, total, ng) == p0 ? 0 : 1);
-  const int lg = S < 8 ? 0 : (S < 32 ? 2 : 4);          // log2 of G
+  const int lg = S <= 5 ? 0 : (S <= 20 ? 2 : 4);        // log2 of G
   const int wide = 128 >> lg;                           // float4 outputs of a piece
   const int pieces = a.H << lg;
   const int c0 = pieces * rank / nb, c1 = pieces * (rank + 1) / nb;
@@ -1071,24 +1073,26 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
     sum = warp_sum(sum);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s = s0; s < s1; s += MOST) {
 #pragma unroll
-    for (int k = 0; k < MOST; ++k) {
-      if (s0 + k < s1) {
-        const float w = wgt[warp][s0 + k];
-        o.x += w * v[k].x;
-        o.y += w * v[k].y;
-        o.z += w * v[k].z;
-        o.w += w * v[k].w;
+      for (int k = 0; k < MOST; ++k) {
+        if (s + k < s1) {
+          const float w = wgt[warp][s + k];
+          o.x += w * v[k].x;
+          o.y += w * v[k].y;
+          o.z += w * v[k].z;
+          o.w += w * v[k].w;
+          if (s + MOST + k < s1) v[k] = src[slot_of(s + MOST + k) * 128];
+        }
       }
     }
-    if (lg == 4) {   // four depths in a warp
-#pragma unroll
-      for (int d = 8; d <= 16; d <<= 1) {
-        o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
-        o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
-        o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
-        o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
-      }
+    // (the depths that share a warp)
+    for (int d = wide; d < 32; d <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
     }
     if (lg > 0) {
       if (warp > 0) acc[warp - 1][lane] = o;
@@ -1159,7 +1163,10 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   }
   if (r != 0) return r;
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
-  return launch_after(join_kernel, dim3((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks)), NT_JOIN, 0, stream, a, a.head_blocks * hb);
+  const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
+  const int pad = a.head_blocks * hb;
+  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, pad)
+                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, pad);
 }
 
 }  // namespace dsa
