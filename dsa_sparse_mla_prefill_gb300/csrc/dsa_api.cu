@@ -627,15 +627,15 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
 static int64_t decode_tiles(int64_t positions) {
   return ((positions < INT32_MAX ? positions : INT32_MAX) + 127) / 128;
 }
-static int decode_groups(int B, int H, int64_t max_tiles) {
-  const int64_t tiles = B * max_tiles, most = dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H);
+static int decode_groups(int B, int H, bool fp8, int64_t max_tiles) {
+  const int64_t tiles = B * max_tiles, most = dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H, fp8);
   return (int)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
 }
 
 // workspace: where the ranges end, then two partial results per CTA group
 // (log-sum-exp, then outputs)
-static int64_t decode_part_bytes(int H, int groups, int64_t* lse_at, int64_t* out_at) {
-  const int64_t hp = (int64_t)dsa::decode_head_blocks(H) * dsa::decode_heads_per_cta(H);
+static int64_t decode_part_bytes(int H, bool fp8, int groups, int64_t* lse_at, int64_t* out_at) {
+  const int64_t hp = (int64_t)dsa::decode_head_blocks(H, fp8) * dsa::decode_heads_per_cta(H, fp8);
   *lse_at = (16 * (1 + groups) + 255) / 256 * 256;
   *out_at = *lse_at + (2 * groups * hp * 4 + 255) / 256 * 256;
   return *out_at + 2 * groups * hp * 512 * 4;
@@ -643,8 +643,12 @@ static int64_t decode_part_bytes(int H, int groups, int64_t* lse_at, int64_t* ou
 
 int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
   if (B < 0 || H < 1 || H > 128 || max_positions < 0) return -1;
-  int64_t l, o;
-  return decode_part_bytes(H, decode_groups(B, H, decode_tiles(max_positions)), &l, &o);
+  int64_t l, o, most = 0;   // of either cache format
+  for (int fp8 = 0; fp8 < 2; ++fp8) {
+    const int64_t n = decode_part_bytes(H, fp8, decode_groups(B, H, fp8, decode_tiles(max_positions)), &l, &o);
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
@@ -666,16 +670,16 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||
       !aligned16(out) || !aligned4(lse))
     return DSA_ERR_INVALID_ARG;
-  const int groups = decode_groups(B, H, max_tiles);
+  const bool fp8 = cache_format == DSA_CACHE_FP8;
+  const int groups = decode_groups(B, H, fp8, max_tiles);
   int64_t lse_at, out_at;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < decode_part_bytes(H, groups, &lse_at, &out_at))
+      workspace_bytes < decode_part_bytes(H, fp8, groups, &lse_at, &out_at))
     return DSA_ERR_INVALID_ARG;
   DevInfo* d;
   if (!dev_info(&d)) return DSA_ERR_CUDA;
   dsa::DecodeArgs a;
   memset(&a, 0, sizeof(a));
-  const bool fp8 = cache_format == DSA_CACHE_FP8;
   const int d_rope = d_qk - 512;
   a.rows_base = static_cast<const uint8_t*>(cache);
   a.row_bytes = fp8 ? 528 + 2 * d_rope : 2 * ld_kv;
@@ -699,7 +703,7 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   a.cap = (int)((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
   a.scale = scale;
   a.tr = g_trace;
-  a.head_blocks = dsa::decode_head_blocks(H);
+  a.head_blocks = dsa::decode_head_blocks(H, fp8);
   // (a GPU with fewer SMs than the workspace is sized for runs fewer ranges)
   const int most = d->num_sms / a.head_blocks;
   a.groups = groups < most ? groups : (most > 0 ? most : 1);
@@ -718,7 +722,7 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;
-  if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H))) return DSA_ERR_CUDA;
+  if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H, fp8))) return DSA_ERR_CUDA;
   const int r = dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
 }

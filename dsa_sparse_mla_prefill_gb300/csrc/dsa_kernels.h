@@ -206,9 +206,12 @@ int launch_kv_fp8(const Fp8KvArgs& a, bool quantize, int num_sms, cudaStream_t s
 int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t stream);
 int launch_kv_append(const AppendArgs& a, bool fp8, int num_sms, cudaStream_t stream);
 
-// Heads per CTA of the decode kernel and the CTAs its heads take.
-inline int decode_heads_per_cta(int H) { return H <= 16 ? 16 : 32; }
-inline int decode_head_blocks(int H) { return (H + decode_heads_per_cta(H) - 1) / decode_heads_per_cta(H); }
+// Heads per CTA of the decode kernel and the CTAs its heads take.  (FP8 rows: the
+// units they are converted into leave no room for more than 32 heads' q and P.)
+inline int decode_heads_per_cta(int H, bool fp8) { return H <= 16 ? 16 : (H <= 32 || fp8 ? 32 : 64); }
+inline int decode_head_blocks(int H, bool fp8) {
+  return (H + decode_heads_per_cta(H, fp8) - 1) / decode_heads_per_cta(H, fp8);
+}
 constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
 // max_tiles: an upper bound of a request's key tiles (1: nothing is split).
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);

@@ -55,35 +55,39 @@ namespace dsa {
 namespace decode {
 
 constexpr int BK = 128;          // keys per tile (the MMA's M)
-constexpr int NTHREADS = 768;
 constexpr int NI = 4;            // tiles of rows ahead
 constexpr float kTau = 8.0f;     // lazy-rescale threshold (log2 units)
-// 768 threads launched at 80 registers
-constexpr int REGS_LAUNCH = 80;
 
 template <int HB, int NC, bool F8>
 struct Cfg {
-  static constexpr int HT = HB / 2;                      // heads per softmax thread
-  // registers of the eight softmax warps and of the others (converters of FP8
-  // rows want room for several conversions at once)
-  static constexpr int REGS_SOFTMAX = F8 ? (HB == 16 ? 96 : 128) : 144;
-  static constexpr int REGS_REST = F8 ? (HB == 16 ? 72 : 56) : 48;
-  static_assert(256 * REGS_SOFTMAX + 512 * REGS_REST <= NTHREADS * REGS_LAUNCH, "registers");
+  static constexpr int SWG = HB == 64 ? 4 : 2;           // softmax warpgroups
+  static constexpr int HT = HB / SWG;                    // heads per softmax thread
+  // warps: the softmax warpgroups, one each for QK, P.V, q and the schedule, then
+  // the loaders (and converters)
+  static constexpr int W_QK = 4 * SWG, W_PV = W_QK + 1, W_Q = W_QK + 2, W_SCHED = W_QK + 3, W_LOAD = W_QK + 4;
+  static constexpr int NWARPS = W_LOAD + (HB == 64 ? 8 : 12);
+  static constexpr int NTHREADS = 32 * NWARPS;
+  // registers: at launch, of the softmax warps and of the others (converters of
+  // FP8 rows want room for several conversions at once)
+  static constexpr int REGS_LAUNCH = HB == 64 ? 72 : 80;
+  static constexpr int REGS_SOFTMAX = HB == 64 ? 96 : (F8 ? (HB == 16 ? 96 : 128) : 144);
+  static constexpr int REGS_REST = HB == 64 ? 40 : (F8 ? (HB == 16 ? 72 : 56) : 48);
+  static_assert(128 * SWG * REGS_SOFTMAX + (NTHREADS - 128 * SWG) * REGS_REST <= NTHREADS * REGS_LAUNCH, "registers");
   // What shared memory leaves beside q and P.  bf16 rows: a ring of NK 64-column
   // K chunks and one of NV 128-column V units.  FP8 rows: NK slots of codes (128
   // rows x 128), NV units of converted columns that QK and P.V both read, and a
   // slot for the RoPE columns.
-  static constexpr int NK = F8 ? (HB == 16 ? 3 : 2) : (HB == 16 ? 6 : 5);
-  static constexpr int NV = F8 ? 4 : 3;
+  static constexpr int NK = F8 ? (HB == 16 ? 3 : 2) : (HB == 16 ? 6 : (HB == 32 ? 5 : 4));
+  static constexpr int NV = F8 ? 4 : (HB == 64 ? 2 : 3);
   static constexpr bool ROPE_SLOT = F8 && NC == 9;
   // warps that read the row ring: the loaders, and for FP8 rows the converters
   static constexpr int NPROD = F8 ? NK + (ROPE_SLOT ? 1 : 0) + 8 : NK + 2 * NV;
-  static_assert(NPROD <= 12, "warps");
+  static_assert(NPROD <= NWARPS - W_LOAD, "warps");
   static constexpr uint32_t CHUNK_BYTES = BK * 128u;     // 128 keys x 64 columns
   static constexpr uint32_t UNIT_BYTES = 2u * CHUNK_BYTES;
   static constexpr uint32_t Q_BYTES = NC * HB * 128u;
   static constexpr uint32_t P_BYTES = 2u * HB * 128u;
-  static constexpr uint32_t RED_FLOATS = 2u * 2u * 4u * HT;   // [parity][warpgroup][warp][head]
+  static constexpr uint32_t RED_FLOATS = 2u * SWG * 4u * HT;   // [parity][warpgroup][warp][head]
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + NK * CHUNK_BYTES;
   static constexpr uint32_t OFF_R = OFF_V + NV * UNIT_BYTES;
@@ -93,14 +97,16 @@ struct Cfg {
   static constexpr uint32_t OFF_META = OFF_ROWS + NI * BK * 4u;
   static constexpr uint32_t OFF_RED = OFF_META + NI * 16u;
   static constexpr uint32_t OFF_BAR = OFF_RED + (2u * RED_FLOATS + HB) * 4u;   // (two sums and a factor per head in the epilogue)
-  static constexpr int NBAR = 60;
+  static constexpr int NBAR = 64;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
-  static constexpr uint32_t MISC_BYTES = 128u;
+  static constexpr uint32_t MISC_BYTES = 256u;
   static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + 1024u;
   static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
-  // TMEM columns: O^T double buffer (2 x 4 HB), S^T double buffer (2 x HB)
-  static constexpr uint32_t COL_S = 8u * HB;
-  static constexpr uint32_t TMEM_COLS = (10u * HB <= 256u) ? 256u : 512u;
+  // TMEM columns: O^T (4 HB, twice where they fit, so that an epilogue overlaps
+  // the next request), S^T double buffer (2 x HB)
+  static constexpr int NO = HB == 64 ? 1 : 2;
+  static constexpr uint32_t COL_S = NO * 4u * HB;
+  static constexpr uint32_t TMEM_COLS = (COL_S + 2u * HB <= 256u) ? 256u : 512u;
 };
 
 enum {
@@ -114,7 +120,7 @@ enum {
   B_P_EMPTY = 17,
   B_O_FULL = 18,     // [2]
   B_O_EMPTY = 20,    // [2]
-  B_SMX = 22,        // [2] one per softmax warpgroup
+  B_SMX = 60,        // [4] one per softmax warpgroup
   B_PLAN = 9,
   B_DRAIN = 24,      // [2] one per MMA issuer
   B_FULL = 26,       // [16] K (or code) slots from 0, V units from 8
@@ -315,7 +321,7 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float* v) {
 }
 
 template <int HB, int NC, bool F8>
-__global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<HB, NC, F8>;
   constexpr int HT = C::HT;
   extern __shared__ uint8_t smem_raw[];
@@ -348,10 +354,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
     // thread are 700 cycles
     for (int i = lane; i < C::NBAR; i += 32) {
       uint32_t n = 1;
-      // 2 MMA warps, 2 softmax warpgroups, the loading (converting) warps, the q loader
-      if (i >= B_IDX_EMPTY && i < B_IDX_EMPTY + NI) n = 2 + 2 + C::NPROD + 1;
-      if (i == B_S_EMPTY || i == B_S_EMPTY + 1 || i == B_O_EMPTY || i == B_O_EMPTY + 1 || i == B_P_FULL) n = 256;
-      if (i == B_SMX || i == B_SMX + 1) n = 128;
+      // 2 MMA warps, the softmax warpgroups, the loading (converting) warps, the q loader
+      if (i >= B_IDX_EMPTY && i < B_IDX_EMPTY + NI) n = 2 + C::SWG + C::NPROD + 1;
+      if (i == B_S_EMPTY || i == B_S_EMPTY + 1 || i == B_O_EMPTY || i == B_O_EMPTY + 1 || i == B_P_FULL) n = 128 * C::SWG;
+      if (i >= B_SMX && i < B_SMX + 4) n = 128;
       // a V unit is two loading warps' work; codes are read, and units of FP8
       // rows filled, by eight converting warps
       if (i >= B_FULL + 8 && i < B_FULL + 16) n = F8 ? 8 : 2;
@@ -376,11 +382,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
   // the joining kernel may be put on the GPU as soon as there is room
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp >= 8) {
+  if (warp >= C::W_QK) {
     regs_dec<C::REGS_REST>();
     // what earlier kernels wrote may be read from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 11) {
+    if (warp == C::W_SCHED) {
       // ------------------------------------------------------------------
       // scheduler
       // ------------------------------------------------------------------
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       }
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && hb == 0) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
-    } else if (const int nt = poll(B_PLAN, 0) ? *plan : 0; warp >= 12) {
+    } else if (const int nt = poll(B_PLAN, 0) ? *plan : 0; warp >= C::W_LOAD) {
       if constexpr (F8) {
         // ----------------------------------------------------------------
         // FP8 rows.  Warp 12 + s owns code slot s and loads 128-code blocks into
@@ -502,9 +508,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         // rows would have landed, by the arithmetic of the dequantize kernel.
         // ----------------------------------------------------------------
         const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
-        if (warp < 12 + C::NK + (C::ROPE_SLOT ? 1 : 0)) {
-          const bool rope = C::ROPE_SLOT && warp == 12 + C::NK;
-          const int own = warp - 12, nslots = rope ? 1 : C::NK, stages = rope ? 1 : 4;
+        if (warp < C::W_LOAD + C::NK + (C::ROPE_SLOT ? 1 : 0)) {
+          const bool rope = C::ROPE_SLOT && warp == C::W_LOAD + C::NK;
+          const int own = warp - C::W_LOAD, nslots = rope ? 1 : C::NK, stages = rope ? 1 : 4;
           const uint32_t dst = sbase + (rope ? C::OFF_R : C::OFF_K + own * C::CHUNK_BYTES);
           uint64_t* full = &bars[rope ? B_R_FULL : B_FULL + own];
           const int empty = rope ? B_R_EMPTY : B_EMPTY + own;
@@ -542,8 +548,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
           }
           if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
           __syncwarp();
-        } else if (warp >= 16) {
-          const int row = (warp & 3) * 32 + lane, hf = (warp - 16) >> 2;
+        } else if (warp >= C::NWARPS - 8) {
+          const int row = (warp & 3) * 32 + lane, hf = (warp - (C::NWARPS - 8)) >> 2;
           const uint32_t rsw = (uint32_t)(row & 7);   // 128B swizzle phase of this row
           uint32_t cs = 0, cphase = 0, us = 0, uphase = 1;   // code slot and unit, their phases
           // the four block scales of the row, loaded a tile ahead (zero for a masked row)
@@ -605,10 +611,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       // of every phase of its slot: none can fall behind it, which a wait on
       // parity would not notice.
       // ------------------------------------------------------------------
-      const bool ks = warp < 12 + C::NK;
-      const int vw = warp - 12 - C::NK;
+      const bool ks = warp < C::W_LOAD + C::NK;
+      const int vw = warp - C::W_LOAD - C::NK;
       if (ks || vw < 2 * C::NV) {
-        const int mine_slot = ks ? warp - 12 : vw >> 1, hf = ks ? 0 : vw & 1;
+        const int mine_slot = ks ? warp - C::W_LOAD : vw >> 1, hf = ks ? 0 : vw & 1;
         const int nslots = ks ? C::NK : C::NV, stages = ks ? NC : 4;
         const uint32_t dst = sbase + (ks ? C::OFF_K + mine_slot * C::CHUNK_BYTES
                                          : C::OFF_V + mine_slot * C::UNIT_BYTES + hf * C::CHUNK_BYTES);
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         __syncwarp();
       }
       }
-    } else if (warp == 10) {
+    } else if (warp == C::W_Q) {
       // ------------------------------------------------------------------
       // q of every request of the range, one box per swizzle column (rows b*H +
       // head0 ... of q viewed [B*H, D_QK]); then the requests without keys
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         for (int i = lane; i < heads * 64; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         for (int h = lane; h < heads; h += 32) a.lse[(int64_t)b * a.H + head0 + h] = -INFINITY;
       }
-    } else if (warp == 8) {
+    } else if (warp == C::W_QK) {
       // ------------------------------------------------------------------
       // QK issuer: the chunks as they land
       // ------------------------------------------------------------------
@@ -746,7 +752,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       commit_elected(leader, &bars[B_DRAIN + 0]);
       if (leader) mbar_wait_drain(&bars[B_DRAIN + 0], 0, err);
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == C::W_PV) {
       // ------------------------------------------------------------------
       // PV issuer: the units in order
       // ------------------------------------------------------------------
@@ -763,10 +769,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
         if (leader) mbar_arrive(&bars[B_IDX_EMPTY + r]);
         if (flags & F_FIRST) ++seg;
-        const int ob = seg & 1;
+        const int ob = C::NO == 2 ? seg & 1 : 0, turn = seg / C::NO;   // O buffer and its use
         if (!poll(B_P_FULL, it & 1)) break;
         if (leader) DSA_TRACE(a.tr, it, 0);
-        if ((flags & F_FIRST) && !poll(B_O_EMPTY + ob, ((seg >> 1) & 1) ^ 1)) break;
+        if ((flags & F_FIRST) && !poll(B_O_EMPTY + ob, (turn & 1) ^ 1)) break;
         const uint32_t acc = (flags & F_FIRST) ? 0u : 1u;
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
@@ -829,17 +835,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < HT; ++h) { m_run[h] = -FLT_MAX; l_exact[h] = 0.f; l_used[h] = 0.f; }
       }
-      const int ob = seg & 1;
+      const int ob = C::NO == 2 ? seg & 1 : 0;
       tc_fence_after();
-      float s[HT], d[HT];
-      tmem_ld_n<HT>(t_lane + C::COL_S + sb * HB, s);
+      const uint32_t t_s = t_lane + C::COL_S + sb * HB;
+      float d[HT];   // scores less the running max, base 2
+      tmem_ld_n<HT>(t_s, d);
       tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(&bars[B_S_EMPTY + sb]);
       float top = -FLT_MAX;
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
-        d[h] = s[h] * scale_log2 - m_run[h];
+        d[h] = d[h] * scale_log2 - m_run[h];
         top = fmaxf(top, d[h]);
       }
       // Lazy rescale: a warp with a score above the running max by more than
@@ -848,13 +853,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       // (One that does not ask publishes the lowest value.)
       // (A masked key's row is zeros, its score 0: it never asks.)
       const bool wneed = __any_sync(0xffffffffu, valid && top > kTau);
-      float* redb = red + (sb * 2 + wg) * (4 * HT);
-      volatile uint32_t* vote = votes + (sb * 2 + wg) * 4;
+      float* redb = red + (sb * C::SWG + wg) * (4 * HT);
+      volatile uint32_t* vote = votes + (sb * C::SWG + wg) * 4;
       float wmax = -FLT_MAX;
       if (wneed) {
         float x[HT];
+        tmem_ld_n<HT>(t_s, x);
+        tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < HT; ++h) x[h] = valid ? s[h] * scale_log2 : -FLT_MAX;
+        for (int h = 0; h < HT; ++h) x[h] = valid ? x[h] * scale_log2 : -FLT_MAX;
         wmax = warp_transpose_reduce<HT, true>(x);
       }
       if (lane < HT) redb[w4 * HT + lane] = wmax;
@@ -863,6 +870,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       if (key == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);   // (every thread of the warpgroup has read the tile's rows)
       const uint32_t need = vote[0] | vote[1] | vote[2] | vote[3];
       if (need) {
+        float alpha[HT];
 #pragma unroll
         for (int h = 0; h < HT; h += 4) {
           float mn[4] = {m_run[h], m_run[h + 1], m_run[h + 2], m_run[h + 3]};
@@ -876,15 +884,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float alpha = exp2f(m_run[h + i] - mn[i]);
+            alpha[h + i] = exp2f(m_run[h + i] - mn[i]);
             m_run[h + i] = mn[i];
-            l_exact[h + i] *= alpha;
-            l_used[h + i] *= alpha;
-            d[h + i] = s[h + i] * scale_log2 - mn[i];
-            s[h + i] = alpha;
+            l_exact[h + i] *= alpha[h + i];
+            l_used[h + i] *= alpha[h + i];
           }
         }
+        if (!(mt.y & F_FIRST)) {
+          // O in tensor memory, once the previous P.V is done with it
+          if (!poll(B_P_EMPTY, sb ^ 1)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            float o[HT];
+            const uint32_t ta = t_lane + ob * (4 * HB) + m * HB;
+            tmem_ld_n<HT>(ta, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < HT; ++h) o[h] *= alpha[h];
+            tmem_st_n<HT>(ta, o);
+          }
+          tmem_st_wait();
+        }
+        // (read again rather than kept: the registers are the softmax warps' limit)
+        tmem_ld_n<HT>(t_s, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < HT; ++h) d[h] = d[h] * scale_log2 - m_run[h];
       }
+      tc_fence_before();
+      mbar_arrive(&bars[B_S_EMPTY + sb]);
       uint32_t pk[HT / 2];
 #pragma unroll
       for (int h = 0; h < HT; h += 2) {
@@ -896,22 +925,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
         l_used[h + 1] += __uint_as_float(w & 0xffff0000u);
         pk[h / 2] = w;
       }
-      // the previous P.V must be done before P is overwritten or O rescaled
+      // the previous P.V must be done before P is overwritten
       if (!poll(B_P_EMPTY, sb ^ 1)) break;
-      tc_fence_after();
-      if (need && !(mt.y & F_FIRST)) {
-#pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          float o[HT];
-          const uint32_t ta = t_lane + ob * (4 * HB) + m * HB;
-          tmem_ld_n<HT>(ta, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < HT; ++h) o[h] *= s[h];
-          tmem_st_n<HT>(ta, o);
-        }
-        tmem_st_wait();
-      }
       // P^T[h][key], K-major swizzled, two columns of 64 keys: row h at h * 128,
       // 16-byte piece c at (c ^ (h & 7)) * 16
 #pragma unroll
@@ -930,7 +945,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       // the barrier above)
       const float ex = warp_transpose_reduce<HT, false>(l_exact);
       const float us = warp_transpose_reduce<HT, false>(l_used);
-      float* redx = red + ((sb ^ 1) * 2 + wg) * (4 * HT);
+      float* redx = red + ((sb ^ 1) * C::SWG + wg) * (4 * HT);
       float* redu = redx + C::RED_FLOATS;
       float* redi = red + 2 * C::RED_FLOATS + wg * HT;
       // the running max is the same in every thread: lane h keeps head h's
@@ -961,7 +976,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) decode_kernel(const __grid_consta
       }
       // (the next tile's vote and reduction use that scratch again)
       if (!group()) break;
-      if (!poll(B_O_FULL + ob, (seg >> 1) & 1)) break;
+      if (!poll(B_O_FULL + ob, (seg / C::NO) & 1)) break;
       tc_fence_after();
       float inv[HT];
 #pragma unroll
@@ -1145,16 +1160,18 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
     attr_set[dev] = 1;
   }
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
-  return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), NTHREADS, C::SMEM_BYTES, stream, a);
+  return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES, stream, a);
 }
 
 }  // namespace decode
 
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream) {
   using namespace decode;
-  const int hb = decode_heads_per_cta(a.H);
+  const int hb = decode_heads_per_cta(a.H, fp8);
   int r = -2;
-  if (hb == 16) {
+  if (hb == 64) {
+    r = d_rope ? launch_t<64, 9, false>(a, stream) : launch_t<64, 8, false>(a, stream);
+  } else if (hb == 16) {
     if (fp8) r = d_rope ? launch_t<16, 9, true>(a, stream) : launch_t<16, 8, true>(a, stream);
     else r = d_rope ? launch_t<16, 9, false>(a, stream) : launch_t<16, 8, false>(a, stream);
   } else {

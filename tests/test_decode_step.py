@@ -185,8 +185,8 @@ def test_decode_refusals(lib, change, want):
 
 def test_workspace_sizes(lib):
     # two partial results per range, all heads padded to whole head blocks, plus their log-sum-exp and a
-    # little; a range per SM and head block, but no more than there are tiles of 128 positions
-    for H, hp, most in [(1, 16, 152), (16, 16, 152), (17, 32, 152), (32, 32, 152), (33, 64, 76), (128, 128, 38)]:
+    # little; a range per SM and head block (of 64 heads), but no more than there are tiles of 128 positions
+    for H, hp, most in [(1, 16, 152), (16, 16, 152), (17, 32, 152), (32, 32, 152), (33, 64, 152), (128, 128, 76)]:
         for B, positions in [(1, 1), (1, 777), (4, 128), (3, 100000), (0, 5), (2, 0)]:
             ranges = max(1, min(most, B * -(-positions // 128)))
             need = 2 * ranges * hp * 4 * (512 + 1)
