@@ -167,9 +167,9 @@ def _host_i32(arr):
 
 
 def _stream(stream, device):
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        torch = _torch or _load_torch()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if device.index is None else device.index))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 

@@ -618,7 +618,7 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
   a.ld_kv = ld_kv;
   a.rotate = freqs != nullptr;
   if (freqs) a.table = *freqs;
-  return dsa::launch_kv_append(a, cache_format == DSA_CACHE_FP8, d->num_sms, (cudaStream_t)stream) == 0 ? DSA_OK
+  return dsa::launch_kv_append(a, cache_format == DSA_CACHE_FP8, (cudaStream_t)stream) == 0 ? DSA_OK
                                                                                                         : DSA_ERR_CUDA;
 }
 

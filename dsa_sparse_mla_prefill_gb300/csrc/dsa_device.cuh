@@ -294,6 +294,15 @@ __device__ __forceinline__ float abs_ieee(float a) {
   asm("abs.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+// The scale of a block by its largest magnitude (+0 or positive: a zero bit
+// pattern is an all-zero block), and the codes of a bf16 pair (low byte: the low
+// half's).
+__device__ __forceinline__ float e4m3_block_scale(float amax) {
+  return __float_as_uint(amax) != 0u ? div_ieee(amax, 448.f) : 1.f;
+}
+__device__ __forceinline__ uint16_t e4m3_quantize2(uint32_t pair, float scale) {
+  return f32x2_to_e4m3x2(div_ieee(__uint_as_float(pair << 16), scale), div_ieee(__uint_as_float(pair & 0xffff0000u), scale));
+}
 // One warp quantizes one 128-column block: lane l holds columns 4l .. 4l+3
 // as bf16 bits and gets their four codes (byte i = column 4l + i) and the
 // block's scale.  Every lane of the warp calls it.
@@ -303,11 +312,8 @@ __device__ __forceinline__ uint32_t e4m3_quantize_block(uint2 raw, float& scale)
   float amax = max_ieee(max_ieee(abs_ieee(v[0]), abs_ieee(v[1])), max_ieee(abs_ieee(v[2]), abs_ieee(v[3])));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  // (amax is +0 or positive: a zero bit pattern is an all-zero block)
-  scale = __float_as_uint(amax) != 0u ? div_ieee(amax, 448.f) : 1.f;
-  const uint32_t lo = f32x2_to_e4m3x2(div_ieee(v[0], scale), div_ieee(v[1], scale));
-  const uint32_t hi = f32x2_to_e4m3x2(div_ieee(v[2], scale), div_ieee(v[3], scale));
-  return lo | (hi << 16);
+  scale = e4m3_block_scale(amax);
+  return e4m3_quantize2(raw.x, scale) | (uint32_t)e4m3_quantize2(raw.y, scale) << 16;
 }
 
 // cp.async of 4 bytes (src_bytes = 0: zero fill), and an arrival on an

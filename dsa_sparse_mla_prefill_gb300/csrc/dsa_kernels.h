@@ -204,7 +204,7 @@ int launch_masked_mha(const MaskedArgs& a, int num_sms, cudaStream_t stream);
 int launch_wait_timeout(unsigned int* err, cudaStream_t stream);
 int launch_kv_fp8(const Fp8KvArgs& a, bool quantize, int num_sms, cudaStream_t stream);
 int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t stream);
-int launch_kv_append(const AppendArgs& a, bool fp8, int num_sms, cudaStream_t stream);
+int launch_kv_append(const AppendArgs& a, bool fp8, cudaStream_t stream);
 
 // Heads per CTA of the decode kernel and the CTAs its heads take.  (FP8 rows: the
 // units they are converted into leave no room for more than 32 heads' q and P.)

@@ -155,11 +155,13 @@ template <typename E, bool HALF, bool VEC>
 static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int PPT = pairs_per_thread<E, HALF, VEC>();
   const int64_t per_group = (int64_t)a.T * (a.d / (2 * PPT));   // threads of one head group
-  // as many heads per thread, in powers of two, as leave threads for every
-  // SM's 2048 slots (16384 tokens of 32 heads: 8 each, 25.7 us; 11 each 27.3,
-  // 4 each 27.0, 2 each 36.6, the cos and sin being worked out per thread)
+  // as many heads per thread, in powers of two, as leave threads for half of
+  // every SM's 2048 slots (16384 tokens of 32 heads, interleaved bf16: 8 heads
+  // each 25.7 us, 32 each 26.5, 11 each 27.3, 4 each 27.0, 2 each 36.6; 8191 of
+  // 16 heads, fp32 halves: 4 each 13.6 us, 2 each 15.3, the cos and sin being
+  // worked out per thread)
   int each = 1;
-  while (2 * each <= a.H && (a.H + 2 * each - 1) / (2 * each) * per_group >= 2048ll * num_sms) each *= 2;
+  while (2 * each <= a.H && (a.H + 2 * each - 1) / (2 * each) * per_group >= 1024ll * num_sms) each *= 2;
   a.head_groups = (a.H + each - 1) / each;
   const int64_t blocks = (per_group * a.head_groups + NT - 1) / NT;
   if (blocks * NT > 0xffffffffll) return -2;
@@ -172,18 +174,15 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
 // columns turned) into row table[r][p / block_size] * block_size + p %
 // block_size of the cache, r being the token's request and p its position.
 // The FP8 row is the one the quantize kernel writes for the same bf16 row
-// (shared e4m3_quantize_block), the RoPE columns being rounded to bf16 first.
+// (the same scale and conversion, e4m3_block_scale and e4m3_quantize2), the RoPE columns being rounded to bf16 first.
 //
 // Bound: HBM; a decode step's handful of tokens by the launch and two
-// dependent loads (position, then block id).  Warps 0-3 take a 128-column
-// block of the row each (lane l: columns 4l .. 4l+3, the layout of the block
-// quantization), warp 4 the RoPE columns (lane = pair), so that the RoPE
-// arithmetic runs beside the copy; ROWS tokens per CTA have their loads in
-// flight together (2 for a prompt chunk; 1 while the tokens do not fill the
-// GPU, where more CTAs are worth more than more loads per thread).
+// dependent loads (position, then block id).  One warp per token: lane l holds
+// columns 16 l .. 16 l + 15 (eight lanes are a 128-column block of the
+// quantization) and pair l of the RoPE columns, all loaded before the row is
+// looked up.
 // --------------------------------------------------------------------------
-constexpr int NT_APPEND = 160;
-constexpr int ROWS_LONG = 2;
+constexpr int NT_APPEND = 64;   // (2 tokens: 16384 of them 4 % faster than 4 or 8 per CTA)
 
 // The physical row of token t, or -1 (a padding token, or a bad entry: *bad).
 __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int t, int32_t& pos, bool& bad) {
@@ -200,76 +199,59 @@ __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int t, int32_t& p
   return row;
 }
 
-template <bool F8, int ROWS>
+template <bool F8>
 __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant__ AppendArgs a) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * ROWS;
-  int64_t row[ROWS];
-  int32_t pos[ROWS];
-  // (called once the token's own data is on its way: the two loads behind each
-  // other that find the row then overlap it)
-  auto find_rows = [&]() {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * (NT_APPEND / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.c_kv + t * a.c_stride) + 2 * lane;
+  const uint4 w0 = src[0], w1 = src[1];
+  const bool half = a.table.layout == DSA_ROPE_HALF;
+  const bool pe = 2 * lane < a.d_rope;
+  const int lo = half ? lane : 2 * lane, up = half ? lane + a.d_rope / 2 : lo + 1;
+  uint16_t p = 0, q = 0;
+  if (pe) {
+    p = a.k_pe[t * a.pe_stride + lo];
+    q = a.k_pe[t * a.pe_stride + up];
+  }
+  int32_t pos;
+  bool bad;
+  const int64_t row = row_of(a, (int)t, pos, bad);
+  if (bad && lane == 0) atomicAdd(a.err + ERR_BAD_INDEX, 1u);
+  if (row < 0) return;   // (the whole warp)
+  uint8_t* dst = static_cast<uint8_t*>(a.cache) + row * (F8 ? 528 + 2 * a.d_rope : 2ll * a.ld_kv);
+  if constexpr (F8) {
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    float amax = 0.f;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      row[r] = -1;
-      if (t0 + r < a.T) {
-        bool bad;
-        row[r] = row_of(a, t0 + r, pos[r], bad);
-        if (bad && threadIdx.x == 0) atomicAdd(a.err + ERR_BAD_INDEX, 1u);
-      }
+    for (int i = 0; i < 8; ++i) amax = max_ieee(amax, max_ieee(abs_ieee(lo_f32(w[i])), abs_ieee(hi_f32(w[i]))));
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float scale = e4m3_block_scale(amax);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3_quantize2(w[2 * i], scale) | (uint32_t)e4m3_quantize2(w[2 * i + 1], scale) << 16;
+    reinterpret_cast<uint4*>(dst)[lane] = make_uint4(c[0], c[1], c[2], c[3]);
+    if ((lane & 7) == 0) *reinterpret_cast<float*>(dst + 512 + (lane >> 1)) = scale;
+  } else {
+    reinterpret_cast<uint4*>(dst)[2 * lane] = w0;
+    reinterpret_cast<uint4*>(dst)[2 * lane + 1] = w1;
+  }
+  if (pe) {
+    if (a.rotate) {
+      float c, s;
+      cos_sin(a.table.turns[lane], pos, a.table.mscale, c, s);
+      const float x = bf16_to_f32(p), y = bf16_to_f32(q);
+      p = f32_to_bf16_rn(x * c - y * s);
+      q = f32_to_bf16_rn(x * s + y * c);
     }
-  };
-  uint8_t* cache = static_cast<uint8_t*>(a.cache);
-  const int64_t row_bytes = F8 ? 528 + 2 * a.d_rope : 2ll * a.ld_kv;
-  if (w < 4) {
-    uint2 raw[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      raw[r] = make_uint2(0, 0);
-      if (t0 + r < a.T)
-        raw[r] = *reinterpret_cast<const uint2*>(a.c_kv + (int64_t)(t0 + r) * a.c_stride + 128 * w + 4 * lane);
-    }
-    find_rows();
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (row[r] < 0) continue;   // (uniform over the CTA)
-      uint8_t* dst = cache + row[r] * row_bytes;
-      if constexpr (F8) {
-        float scale;
-        const uint32_t codes = e4m3_quantize_block(raw[r], scale);
-        *reinterpret_cast<uint32_t*>(dst + 128 * w + 4 * lane) = codes;
-        if (lane == 0) *reinterpret_cast<float*>(dst + 512 + 4 * w) = scale;
-      } else {
-        *reinterpret_cast<uint2*>(dst + 256 * w + 8 * lane) = raw[r];
-      }
-    }
-  } else if (2 * lane < a.d_rope) {
-    const bool half = a.table.layout == DSA_ROPE_HALF;
-    const int lo = half ? lane : 2 * lane, up = half ? lane + a.d_rope / 2 : lo + 1;
-    uint16_t p[ROWS], q[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      p[r] = q[r] = 0;
-      if (t0 + r < a.T) {
-        const uint16_t* src = a.k_pe + (int64_t)(t0 + r) * a.pe_stride;
-        p[r] = src[lo];
-        q[r] = src[up];
-      }
-    }
-    find_rows();
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (row[r] < 0) continue;
-      if (a.rotate) {
-        float c, s;
-        cos_sin(a.table.turns[lane], pos[r], a.table.mscale, c, s);
-        const float x = bf16_to_f32(p[r]), y = bf16_to_f32(q[r]);
-        p[r] = f32_to_bf16_rn(x * c - y * s);
-        q[r] = f32_to_bf16_rn(x * s + y * c);
-      }
-      uint16_t* dst = reinterpret_cast<uint16_t*>(cache + row[r] * row_bytes + (F8 ? 528 : 1024));
-      dst[lo] = p[r];
-      dst[up] = q[r];
+    uint16_t* d = reinterpret_cast<uint16_t*>(dst + (F8 ? 528 : 1024));
+    if (half) {
+      d[lo] = p;
+      d[up] = q;
+    } else {
+      reinterpret_cast<uint32_t*>(d)[lane] = (uint32_t)p | (uint32_t)q << 16;
     }
   }
 }
@@ -288,17 +270,11 @@ int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t strea
   return half ? launch_t<uint16_t, true, false>(a, num_sms, stream) : launch_t<uint16_t, false, false>(a, num_sms, stream);
 }
 
-int launch_kv_append(const AppendArgs& a, bool fp8, int num_sms, cudaStream_t stream) {
+int launch_kv_append(const AppendArgs& a, bool fp8, cudaStream_t stream) {
   using namespace rope;
-  const int nt = a.d_rope > 0 ? NT_APPEND : 128;
-  if ((int64_t)a.T <= 8ll * num_sms) {   // a CTA per token fills the GPU's SMs at most about twice
-    if (fp8) append_kernel<true, 1><<<a.T, nt, 0, stream>>>(a);
-    else append_kernel<false, 1><<<a.T, nt, 0, stream>>>(a);
-  } else {
-    const unsigned grid = (unsigned)((a.T + (int64_t)ROWS_LONG - 1) / ROWS_LONG);
-    if (fp8) append_kernel<true, ROWS_LONG><<<grid, nt, 0, stream>>>(a);
-    else append_kernel<false, ROWS_LONG><<<grid, nt, 0, stream>>>(a);
-  }
+  const unsigned grid = (unsigned)(((int64_t)a.T + NT_APPEND / 32 - 1) / (NT_APPEND / 32));
+  if (fp8) append_kernel<true><<<grid, NT_APPEND, 0, stream>>>(a);
+  else append_kernel<false><<<grid, NT_APPEND, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
