@@ -780,7 +780,7 @@ def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: flo
         rows, ld = idx.shape
         if rows != B:
             raise ValueError("idx must have one row per request")
-        idx_ptr = idx.data_ptr()
+        idx_ptr = idx.data_ptr() or kv_lens.data_ptr()   # (an empty idx has no address, and means no keys)
         k = ld if k is None else int(k)
     elif k is not None:
         raise ValueError("k without idx")

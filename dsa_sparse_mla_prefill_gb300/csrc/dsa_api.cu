@@ -656,7 +656,8 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
                      const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
                      float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream) {
   if (B < 0 || N < 0 || max_blocks < 1 || block_size < 1) return DSA_ERR_INVALID_ARG;
-  if (!(scale > -INFINITY) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+  // (the kernel works in base 2: scale * log2(e) must be finite too)
+  if (!(std::fabs(scale) <= 2e38f)) return DSA_ERR_INVALID_ARG;
   if (H < 1 || H > 128 || !(d_qk == 576 || d_qk == 512) || d_v != 512) return DSA_ERR_UNSUPPORTED;
   if (cache_format != DSA_CACHE_BF16 && cache_format != DSA_CACHE_FP8) return DSA_ERR_UNSUPPORTED;
   if (cache_format == DSA_CACHE_BF16 && (ld_kv < d_qk || (ld_kv & 7) != 0)) return DSA_ERR_INVALID_ARG;

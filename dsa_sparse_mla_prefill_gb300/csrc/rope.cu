@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
   uint8_t* dst = static_cast<uint8_t*>(a.cache) + row * (F8 ? 528 + 2 * a.d_rope : 2ll * a.ld_kv);
   if constexpr (F8) {
     const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    float amax = 0.f;
+    float amax = max_ieee(abs_ieee(lo_f32(w[0])), abs_ieee(hi_f32(w[0])));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max_ieee(amax, max_ieee(abs_ieee(lo_f32(w[i])), abs_ieee(hi_f32(w[i]))));
+    for (int i = 1; i < 8; ++i) amax = max_ieee(amax, max_ieee(abs_ieee(lo_f32(w[i])), abs_ieee(hi_f32(w[i]))));
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float scale = e4m3_block_scale(amax);

@@ -493,7 +493,8 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
  * -1 nor in [0, kv_lens[b]), are treated as absent and counted.  Cache rows
  * that no position names are never read into a result, whatever they hold.
  * Two kernels are queued on `stream` (one when no request can hold more than
- * 128 keys).  scale must be finite.  The same inputs give the same bits.
+ * 128 keys).  |scale| must be at most 2e38.  The same inputs give the same
+ * bits.
  * DSA_ERR_UNSUPPORTED also when B requests of max_positions have 2^31 tiles of
  * 128 keys or more. */
 int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions);

@@ -169,7 +169,7 @@ WS = 64 << 20
     (dict(B=-1), INVALID), (dict(B=0, q=None, ws=None), OK), (dict(H=0), UNSUPPORTED), (dict(H=129), UNSUPPORTED),
     (dict(dqk=544), UNSUPPORTED), (dict(dv=256), UNSUPPORTED), (dict(fmt=7), UNSUPPORTED), (dict(ld_kv=568), INVALID),
     (dict(ld_kv=580), INVALID), (dict(mb=0), INVALID), (dict(bs=0), INVALID), (dict(N=-1), INVALID),
-    (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(k=9), INVALID), (dict(k=-1), INVALID),
+    (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=-3e38), INVALID), (dict(k=9), INVALID), (dict(k=-1), INVALID),
     (dict(q=None), INVALID), (dict(cache=None), INVALID), (dict(bt=None), INVALID), (dict(lens=None), INVALID),
     (dict(out=None), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID), (dict(ws=4096 + 128), INVALID),
     (dict(wsb=100000), INVALID), (dict(q=4104), INVALID), (dict(cache=4104), INVALID), (dict(out=4104), INVALID),

@@ -522,6 +522,119 @@ def test_decode_refusals():
             call(**bad)
 
 
+def test_decode_no_listed_positions():
+    """k = 0 and an idx without columns: no keys, whatever the lengths."""
+    d = Decode(22, [50, 3], 16)
+    for idx in (torch.zeros(2, 0, dtype=torch.int32, device="cuda"), torch.zeros(2, 5, dtype=torch.int32, device="cuda")):
+        out, lse = d.run(idx=idx, k=0)
+        assert bad_count() == 0 and (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_decode_position_listed_twice_counts_twice():
+    d = Decode(23, [40], 16, k=6)
+    d.idx[0, :6] = [7, 7, 3, -1, 7, 39]
+    d.check(d.run())
+
+
+def test_decode_shared_pages_and_many_requests():
+    """Requests with a common prefix in the same pages; thousands of short requests."""
+    d = Decode(24, [300] * 40, 32)
+    d.bt[:, :10] = d.bt[0, :10]
+    d.check(d.run())
+    rng = np.random.default_rng(25)
+    e = Decode(26, [160], 16)
+    lens = rng.integers(0, 3, 5000).astype(np.int32) * 30 + rng.integers(0, 2, 5000).astype(np.int32)
+    e.lens, e.bt = lens, np.repeat(e.bt, 5000, axis=0)
+    e.q = normal_bf16(rng, (5000, 16, 576))
+    e.check(e.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_offsets_past_32_bits(fmt):
+    """A cache of more than 4 GB whose pages lie at its ends: row offsets in bytes pass 2^32."""
+    d = Decode(27, [700, 90], 32, bs=64, fmt=fmt)
+    width = d.cache.shape[1] * d.cache.element_size()
+    N = (2 ** 32 // width // 64 + 40) * 64
+    big = torch.empty(N, d.cache.shape[1], dtype=d.cache.dtype, device="cuda")
+    pages = int(d.N) // 64
+    last = N // 64 - pages
+    big[last * 64:] = d.cache
+    assert last * 64 * width > 2 ** 32
+    values = d.values
+    d.cache = big
+    bt = d.bt.copy()
+    d.bt = np.where(bt >= 0, bt + last, -1).astype(np.int32)
+    got = d.run()
+    d.bt, d.N = bt, pages * 64
+    d.values = values
+    d.check(got)
+
+
+def test_rope_and_append_offsets_past_32_bits():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    fr = dsa.dsa_rope_freqs(64)
+    big = torch.empty(9, 2 ** 28 + 64, dtype=torch.bfloat16, device="cuda")           # 4.8 GB
+    x = big[:, :128].unflatten(1, (2, 64))
+    x.normal_()
+    keep = x.clone()
+    pos = np.arange(9, dtype=np.int32) * 1000
+    dsa.dsa_rope(x, i32(pos), fr, out=x)
+    check_rope(x, keep, pos, O.rope_frequencies(64, 10000.0), "interleaved")
+    N = 2 ** 32 // 1152 + 100
+    cache = big.flatten()[:N * 576].view(N, 576)
+    rng = np.random.default_rng(3)
+    c, pe = normal_bf16(rng, (2, 512)), normal_bf16(rng, (2, 64))
+    bt = np.array([[N - 1, 0]], dtype=np.int32)
+    dsa.dsa_kv_append(bf(c), bf(pe), i32([0, 1]), i32(bt), 1, cache, token_req=i32([0, 0]))
+    assert bad_count() == 0
+    assert np.array_equal(bits(cache[N - 1:]), np.concatenate([c[:1], pe[:1]], 1))
+    assert np.array_equal(bits(cache[:1]), np.concatenate([c[1:], pe[1:]], 1))
+
+
+def test_append_fp8_of_odd_values_is_the_quantize_kernels():
+    """NaN, infinities, subnormals, zeros: the same bits as quantizing the bf16 row."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    rng = np.random.default_rng(8)
+    c = rng.integers(0, 2 ** 16, (64, 512)).astype(np.uint16)          # any bf16 pattern
+    c[0, :128], c[0, 128:256], c[0, 256:384] = 0x7fc0, 0x7f80, 0x8000   # a block of NaN, of infinities, of -0
+    c[1, :128] = np.arange(128)                                          # subnormals
+    c[2, :128], c[2, 5] = 0x7fc0, 0x3f80                                 # one number among NaN
+    pe = normal_bf16(rng, (64, 64))
+    f8 = torch.zeros(64, 656, dtype=torch.uint8, device="cuda")
+    bt = i32(np.arange(64)[None])
+    dsa.dsa_kv_append(bf(c), bf(pe), i32(np.arange(64)), bt, 1, f8, token_req=i32(np.zeros(64)))
+    want = dsa.dsa_kv_fp8_quantize(bf(np.concatenate([c, pe], 1)), 64)
+    assert bad_count() == 0 and torch.equal(f8, want)
+
+
+def test_decode_two_graphs_at_once():
+    """Two captured calls with their own workspaces, replayed on two streams together, and an eager call
+    beside them."""
+    ds = [Decode(30, [2500, 70, 900], 32), Decode(31, [4000], 16), Decode(32, [10, 1300], 64)]
+    graphs, outs = [], []
+    for d in ds[:2]:
+        q, cache, bt, lens = bf(d.q), d.cache, i32(d.bt), i32(d.lens)
+        import dsa_sparse_mla_prefill_gb300 as dsa
+        dsa.dsa_paged_decode(q, cache, bt, lens, 16, d.scale)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(dsa.dsa_paged_decode(q, cache, bt, lens, 16, d.scale))
+        graphs.append((g, q, bt, lens))
+    s = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    eager = None
+    for _ in range(5):
+        for (g, *_), st in zip(graphs, s):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(s[2]):
+            eager = ds[2].run()
+    torch.cuda.synchronize()
+    for d, o in zip(ds, outs + [eager]):
+        d.check(o)
+
+
 # ---------------------------------------------------------------------------
 # the step: rotate the queries, append the new rows, attend
 # ---------------------------------------------------------------------------
