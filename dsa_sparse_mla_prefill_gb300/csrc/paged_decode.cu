@@ -429,13 +429,21 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       for (int it = 0; it < nt; ++it) {
         const int r = it % NI;
         if (enter) {
-          // (requests without keys have no tile)
-          while (true) {
-            if (it > 0) len = __ldg(a.kv_lens + b);
-            n = tiles_of(a, len);
-            if (n > 0) break;
-            ++b;
+          // the next request with a tile (one without keys has none; there may be
+          // thousands of them in a row, so 32 are looked at at once)
+          while (it > 0) {
+            len = b + lane < a.B ? __ldg(a.kv_lens + b + lane) : 0;
+            const uint32_t there = __ballot_sync(0xffffffffu, tiles_of(a, len) > 0);
+            const int skip = there ? __ffs(there) - 1 : 32;
+            b += skip;
+            len = __shfl_sync(0xffffffffu, len, skip & 31);
+            if (there) break;
+            if (b >= a.B) {   // (never with lengths that stay: a tile is left)
+              b = a.B - 1;
+              break;
+            }
           }
+          n = tiles_of(a, len);
           if (len > a.cap) {
             if (j == 0 && lane == 0) ++bad;
             len = a.cap;

@@ -549,6 +549,18 @@ def test_decode_shared_pages_and_many_requests():
     e.check(e.run())
 
 
+@pytest.mark.parametrize("gap", [31, 32, 33, 700])
+def test_decode_long_runs_of_empty_requests(gap):
+    """A padded batch: few requests have keys, the ones between them none."""
+    rng = np.random.default_rng(28 + gap)
+    d = Decode(28, [300], 16)
+    B = 5 * gap + 7
+    d.lens = np.where(np.arange(B) % gap == gap - 1, 290, 0).astype(np.int32)
+    d.bt = np.repeat(d.bt, B, axis=0)
+    d.q = normal_bf16(rng, (B, 16, 576))
+    d.check(d.run())
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_decode_offsets_past_32_bits(fmt):
     """A cache of more than 4 GB whose pages lie at its ends: row offsets in bytes pass 2^32."""
