@@ -150,7 +150,8 @@ __device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* err
   if (*abort_flag == 0) atomicAdd(err + ERR_TIMEOUT, 1u);
   *abort_flag = 1;
 }
-template <bool POLL>
+// CLUSTER: the phase is completed by the peer CTA too.
+template <bool POLL, bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
   const uint64_t t0 = globaltimer();
 #pragma unroll 1
@@ -163,7 +164,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
           "selp.u32 %0, 1, 0, p;\n\t}"
           : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     else
-      ok = mbar_try_wait_sleep(bar, parity);
+      ok = CLUSTER ? mbar_try_wait_cluster_sleep(bar, parity) : mbar_try_wait_sleep(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     if (*abort_flag) return false;
     if (globaltimer() - t0 > kWaitTimeoutNs) {
@@ -205,6 +206,26 @@ __device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* ma
       : "memory");
 }
 
+// The same into both CTAs of a pair, at the same shared-memory offset, the bytes
+// counted on each one's own barrier.
+__device__ __forceinline__ void gather4_pair(uint32_t dst, const CUtensorMap* map, int x, const int4& r, uint64_t* bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %9, %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
+      "l"(policy), "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %6, %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "h"((uint16_t)3)
+      : "memory");
+}
+
 // Tensor-core issue by one elected lane of a converged warp: the loops around
 // it are warp-uniform, so descriptors and loop state stay in uniform registers
 // (issued from inside a one-lane branch, every operand is first moved there,
@@ -234,6 +255,16 @@ __device__ __forceinline__ void commit_elected(uint32_t leader, uint64_t* bar) {
       "setp.ne.b32 e, %1, 0;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
       ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+
+// (arrives on the barrier of either CTA of a pair)
+__device__ __forceinline__ void commit_elected_pair(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader), "h"((uint16_t)3)
       : "memory");
 }
 
@@ -320,7 +351,7 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float* v) {
   }
 }
 
-template <int HB, int NC, bool F8>
+template <int HB, int NC, bool F8, bool PAIR>
 __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<HB, NC, F8>;
   constexpr int HT = C::HT;
@@ -362,6 +393,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       // rows filled, by eight converting warps
       if (i >= B_FULL + 8 && i < B_FULL + 16) n = F8 ? 8 : 2;
       if (F8 && i >= B_EMPTY && i < B_EMPTY + 8) n = 8;
+      // a slot of a pair is free when both CTAs have read it
+      if (PAIR && i >= B_EMPTY && i < B_EMPTY + 16) n = 2;
       mbar_init(&bars[i], n);
     }
     if (lane == 0) *abort_flag = 0;
@@ -372,7 +405,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // (the peer's barriers are there)
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_ptr;
   const int head0 = hb * HB;                                   // this CTA's first head
@@ -630,6 +664,9 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         const int empty = B_EMPTY + (ks ? 0 : 8) + mine_slot;
         const int col_step = ks ? 64 : 128;
         const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
+        // of a pair each CTA loads half of the rows, for both
+        const bool by_gather = !PAIR || (lane >> 4) == hb;
+        const bool by_box = PAIR ? lane < boxes && (2 * lane >= boxes) == (hb == 1) : lane < boxes;
         const uint64_t policy = ks ? evict_normal_policy() : evict_first_policy();
         int slot = 0;
         uint32_t used = 0;   // phases of the slot so far
@@ -649,21 +686,26 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             const bool mine_now = slot == mine_slot;
             if (++slot == nslots) slot = 0;
             if (!mine_now) continue;
-            if (!doze(empty, (used & 1) ^ 1)) { ok = false; break; }
+            if (!wait<false, PAIR>(bar(empty), (used & 1) ^ 1, abort_flag, err)) { ok = false; break; }
             if (lane == 0) {
               mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
               if (ks && st == 0) DSA_TRACE(a.tr, it, 1);
               if (ks && st == NC - 1) DSA_TRACE(a.tr, it, 2);
             }
-            if (!box)
-              gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
-            else if (lane < boxes)
-              load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+            if (!box) {
+              if constexpr (!PAIR) gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+              else if (by_gather) gather4_pair(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+            } else if (by_box) {
+              if constexpr (!PAIR) load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+              else load_2d_pair(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+            }
             ++used;
           }
         }
         // let the slot's last copies land before the CTA can exit
         if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
+        // and the peer's last arrival here
+        if (PAIR && lane == 0 && used > 0) mbar_wait_drain(&bars[empty], (used - 1) & 1, err);
         __syncwarp();
       }
       }
@@ -749,7 +791,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           if (leader && c == NC - 1) DSA_TRACE(a.tr, it, 4);
           mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)(slot * (C::CHUNK_BYTES >> 4)),
                          q_desc + (uint64_t)(c * (HB * 128 >> 4)), 2u, 2u, IDESC, c > 0 ? 1u : 0u);
-          commit_elected(leader, &bars[B_EMPTY + slot]);
+          if constexpr (PAIR) commit_elected_pair(leader, &bars[B_EMPTY + slot]);
+          else commit_elected(leader, &bars[B_EMPTY + slot]);
           if (++slot == C::NK) { slot = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -791,7 +834,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           // 16 keys (2048 bytes of V^T) per MMA; P^T one 64-key swizzle column per half
           mma_x4_elected(leader, d_o, v, p_desc, 128u, 2u, IDESC, acc);
           mma_x4_elected(leader, d_o, v + 512u, p_desc + (uint64_t)(HB * 128 >> 4), 128u, 2u, IDESC, 1u);
-          commit_elected(leader, &bars[B_EMPTY + 8 + slot]);
+          if constexpr (PAIR) commit_elected_pair(leader, &bars[B_EMPTY + 8 + slot]);
+          else commit_elected(leader, &bars[B_EMPTY + 8 + slot]);
           if (++slot == C::NV) { slot = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -1020,8 +1064,10 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     }
   }
 
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // (the peer's last arrivals and loads have come)
+  else __syncthreads();
   tc_fence_after();
   if (warp == 4) tmem_dealloc(tmem, C::TMEM_COLS);
 }
@@ -1141,34 +1187,40 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
 }
 
 template <typename... P, typename... A>
-static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const A&... args) {
+static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t stream,
+                        const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
 }
 
-template <int HB, int NC, bool F8>
+template <int HB, int NC, bool F8, bool PAIR = false>
 static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<HB, NC, F8>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
       return -1;
     attr_set[dev] = 1;
   }
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
-  return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES, stream, a);
+  return launch_after(decode_kernel<HB, NC, F8, PAIR>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES,
+                      PAIR ? 2 : 1, stream, a);
 }
 
 }  // namespace decode
@@ -1178,7 +1230,8 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   const int hb = decode_heads_per_cta(a.H, fp8);
   int r = -2;
   if (hb == 64) {
-    r = d_rope ? launch_t<64, 9, false>(a, stream) : launch_t<64, 8, false>(a, stream);
+    if (decode_pairs(a.H, fp8)) r = d_rope ? launch_t<64, 9, false, true>(a, stream) : launch_t<64, 8, false, true>(a, stream);
+    else r = d_rope ? launch_t<64, 9, false>(a, stream) : launch_t<64, 8, false>(a, stream);
   } else if (hb == 16) {
     if (fp8) r = d_rope ? launch_t<16, 9, true>(a, stream) : launch_t<16, 8, true>(a, stream);
     else r = d_rope ? launch_t<16, 9, false>(a, stream) : launch_t<16, 8, false>(a, stream);
@@ -1190,8 +1243,8 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
   const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
   const int pad = a.head_blocks * hb;
-  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, pad)
-                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, pad);
+  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, 1, stream, a, pad)
+                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, 1, stream, a, pad);
 }
 
 }  // namespace dsa
