@@ -5,9 +5,9 @@
 // over the positions j < kv_len[b], or over the token's own top-k positions;
 // position j lies in row table[b][j / block_size] * block_size + j % block_size.
 //
-// Bound: every row is read once for all heads of the request (1152 bytes, or
-// 656 in FP8, against 2 * 1088 * H flops), so up to 32 heads HBM is the bound;
-// at 128 heads the flops come within 15 % of it.
+// Bound: every row is read from HBM once for all heads of the request (1152
+// bytes, or 656 in FP8, against 2 * 1088 * H flops), so up to 32 heads HBM is the
+// bound; at 128 heads the flops come within 15 % of it.
 //
 // Split over the length: the keys of all requests, in tiles of 128, form one
 // line of W tiles, dealt to the CTA groups in equal contiguous ranges
@@ -17,31 +17,49 @@
 // requests and begins another: a request that lies whole in a range is stored
 // at once, the parts of one cut by a range border are stored as normalised fp32
 // outputs with their log-sum-exp and joined by a second small kernel, which is
-// launched so that its start overlaps the first one's end.  A group is one CTA
-// per 32 heads (16 when there are no more), all walking the same rows at the
-// same time, so the rows are read from HBM once and from L2 by the others.
+// launched so that its start overlaps the first one's end.
 //
-// One CTA, 24 warps:
-//   warps 0-7   softmax: thread = key (TMEM lane), warpgroup = half of the heads;
-//               online in base 2 with the lazy rescale (only when a head's
-//               running max grows by more than 2^8); P to shared memory in
+// A group is one CTA per 16 heads (H <= 16), 32 (H <= 32, and FP8 rows) or 64, all
+// walking the same rows at the same time.  Fewer, wider CTAs per group read fewer
+// copies of a row through L2: at 128 heads, 16 x 19456 positions take 193 us as 4
+// CTAs of 32 heads and 123 us as 2 of 64 (all pages in L2).  Over bf16 rows the two
+// CTAs of more than 64 heads are a cluster: each loads half of the rows, multicast
+// to both, which halves the row gathers (96 requests x 2048 listed positions, 128
+// heads: 134 us, 186 without; pages of 4 rows, 16 x 19456: 175 and 215; with boxes
+// the two forms are within 4 %).
+//
+// One CTA (24 warps; 28 of the 64-head form):
+//   softmax     8 warps (16): thread = key (TMEM lane), warpgroup = its share of
+//               the heads; online in base 2 with the lazy rescale (only when a
+//               head's running max grows by more than 2^8); P to shared memory in
 //               bf16; the epilogue (O^T lane = output column).
-//   warp 8      QK issuer: S^T = K q^T, keys on the M side (M = 128, N = heads)
-//   warps 9, 10, 20, 21  PV issuers: O^T += V^T P^T, one 128-column unit each
-//   warp 11     scheduler: walks the range, turns 128 positions per tile into
-//               rows (a ring of four tiles ahead)
-//   warps 12-19 TMA loads of the units: row gathers (4 rows x 128 bytes per
-//               instruction), or boxes of up to 128 rows where every key of the
-//               tile is there and the pages hold them in runs (page sizes that
-//               are multiples of 8 rows)
-//   warp 22     the same for the RoPE columns
-//   warp 23     q per request; the outputs of requests without keys
-// Every key row is gathered once: a tile of 128 keys is four 128-column units
-// (32 KB, in a ring of five) and one RoPE chunk; QK reads a unit K-major, P.V
-// reads the same bytes MN-major, and the unit goes back to the producers when
-// its P.V is done.  Rows that are masked (behind kv_len, -1, unmapped pages) are
-// gathered from outside the tensor map, which reads as zeros: whatever the
-// cache holds there, NaN included, never reaches the sums.
+//   W_QK        S^T = K q^T, keys on the M side (M = 128, N = heads)
+//   W_PV        O^T += V^T P^T, one 128-column unit after another
+//   W_Q         q per request; the outputs of requests without keys
+//   W_SCHED     walks the range, turns 128 positions per tile into rows (a ring of
+//               four tiles ahead)
+//   W_LOAD ...  TMA loads: row gathers (4 rows x 128 bytes per instruction), or
+//               boxes of up to 128 rows where every key of the tile is there and
+//               the pages hold them in runs (page sizes that are multiples of 8
+//               rows); for FP8 rows the last eight convert.
+//
+// bf16 rows are loaded twice, from HBM into a ring of 64-column K chunks (QK reads
+// them K-major) and from L2 into a ring of 128-column V units (P.V reads them
+// MN-major).  Loading them once, into units that QK and P.V share, needs a tile's
+// four units from the first QK to the last P.V: the next tile's loads wait for
+// this one's softmax, 7000-10000 cycles a tile against 5000 (all pages in L2).
+// FP8 rows are loaded once, into a ring of code slots, and converted into such
+// shared units, since converting costs more than loading (1130 cycles a unit): a
+// tile takes 8000 cycles, the conversions and the softmax one after another.
+// Rows that are masked (behind kv_len, -1, unmapped pages) are loaded from
+// outside the tensor map, which reads as zeros: whatever the cache holds there,
+// NaN included, never reaches the sums.
+//
+// Measured (128-key tiles per CTA of 32 heads): 2.5 us a tile with all pages in
+// L2, 3.3 from HBM (5.1 TB/s of 6.8); 64 ragged requests up to 16384 positions
+// 73 us against 43.6 for the bytes alone, one request of 131072 42 against 22.3:
+// the rest is the start (6 us), the last tile's way through the CTA and the join
+// (4-8 us).
 //
 // Rounding: P is rounded to bf16 for the tensor core.  The outputs are divided
 // by the sum of the rounded weights (so that the weights used add up to one);
@@ -542,10 +560,10 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     } else if (const int nt = poll(B_PLAN, 0) ? *plan : 0; warp >= C::W_LOAD) {
       if constexpr (F8) {
         // ----------------------------------------------------------------
-        // FP8 rows.  Warp 12 + s owns code slot s and loads 128-code blocks into
-        // it, warp 12 + NK the RoPE columns (bf16, byte 528 of the row) into
-        // their slot; lanes as for bf16 rows.
-        // Warps 16-23 convert: thread = row and half of the block, 64 codes into
+        // FP8 rows.  Warp W_LOAD + s owns code slot s and loads 128-code blocks
+        // into it, warp W_LOAD + NK the RoPE columns (bf16, byte 528 of the row)
+        // into their slot; lanes as for bf16 rows.
+        // The last eight warps convert: thread = row and half of the block, 64 codes into
         // the half's 64-column chunk of the unit, in the layout in which the bf16
         // rows would have landed, by the arithmetic of the dequantize kernel.
         // ----------------------------------------------------------------
@@ -646,7 +664,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       } else {
       // ------------------------------------------------------------------
       // row loads: a warp per 64-column chunk in flight, since a warp issues row
-      // gathers one after another (about 80 cycles each).  Warp 12 + s owns K
+      // gathers one after another (about 80 cycles each).  Warp W_LOAD + s owns K
       // slot s, the two warps after those a half of V slot 0, and so on: lane l
       // gathers rows 4l .. 4l+3, or where the keys lie in runs of box_rows rows
       // lane l loads box l of 128 / box_rows.  Each warp opens its chunk's share
