@@ -28,7 +28,7 @@
 // heads: 134 us, 186 without; pages of 4 rows, 16 x 19456: 175 and 215; with boxes
 // the two forms are within 4 %).
 //
-// One CTA (24 warps; 28 of the 64-head form):
+// One CTA (24 warps; 28 of the 64-head form, 32 of 16 heads over FP8 rows):
 //   softmax     8 warps (16): thread = key (TMEM lane), warpgroup = its share of
 //               the heads; online in base 2 with the lazy rescale (only when a
 //               head's running max grows by more than 2^8); P to shared memory in
@@ -41,7 +41,7 @@
 //   W_LOAD ...  TMA loads: row gathers (4 rows x 128 bytes per instruction), or
 //               boxes of up to 128 rows where every key of the tile is there and
 //               the pages hold them in runs (page sizes that are multiples of 8
-//               rows); for FP8 rows the last eight convert.
+//               rows); for FP8 rows the last eight (16) convert.
 //
 // bf16 rows are loaded twice, from HBM into a ring of 64-column K chunks (QK reads
 // them K-major) and from L2 into a ring of 128-column V units (P.V reads them
@@ -49,8 +49,12 @@
 // four units from the first QK to the last P.V: the next tile's loads wait for
 // this one's softmax, 7000-10000 cycles a tile against 5000 (all pages in L2).
 // FP8 rows are loaded once, into a ring of code slots, and converted into such
-// shared units, since converting costs more than loading (1130 cycles a unit): a
-// tile takes 8000 cycles, the conversions and the softmax one after another.
+// shared units, since converting costs more than loading: a tile takes 7500 cycles
+// at 16 heads, its four conversions (some 700 cycles apart), the softmax and the
+// first P.V one after another.  The conversion is a chain of latencies (two waits,
+// load, convert, store, fence), not of arithmetic (none at all: the same time), so
+// where registers allow (16 heads) two sets of eight warps take the units in turn:
+// 48 requests up to 16384 positions 68 us, 71 with one set.
 // Rows that are masked (behind kv_len, -1, unmapped pages) are loaded from
 // outside the tensor map, which reads as zeros: whatever the cache holds there,
 // NaN included, never reaches the sums.
@@ -83,24 +87,24 @@ struct Cfg {
   // warps: the softmax warpgroups, one each for QK, P.V, q and the schedule, then
   // the loaders (and converters)
   static constexpr int W_QK = 4 * SWG, W_PV = W_QK + 1, W_Q = W_QK + 2, W_SCHED = W_QK + 3, W_LOAD = W_QK + 4;
-  static constexpr int NWARPS = W_LOAD + (HB == 64 ? 8 : 12);
+  static constexpr int NCONV = !F8 ? 0 : (HB == 16 ? 16 : 8);   // converting warps, the last ones
+  static constexpr int NWARPS = W_LOAD + (HB == 64 ? 8 : (NCONV == 16 ? 20 : 12));
   static constexpr int NTHREADS = 32 * NWARPS;
-  // registers: at launch, of the softmax warps and of the others (converters of
-  // FP8 rows want room for several conversions at once)
-  static constexpr int REGS_LAUNCH = HB == 64 ? 72 : 80;
-  static constexpr int REGS_SOFTMAX = HB == 64 ? 96 : (F8 ? (HB == 16 ? 96 : 128) : 144);
-  static constexpr int REGS_REST = HB == 64 ? 40 : (F8 ? (HB == 16 ? 72 : 56) : 48);
+  // registers: at launch, of the softmax warps and of the others
+  static constexpr int REGS_LAUNCH = HB == 64 ? 72 : (NCONV == 16 ? 64 : 80);
+  static constexpr int REGS_SOFTMAX = HB == 64 ? 96 : (F8 ? (HB == 16 ? 88 : 128) : 144);
+  static constexpr int REGS_REST = HB == 64 ? 40 : (F8 ? 56 : 48);
   static_assert(128 * SWG * REGS_SOFTMAX + (NTHREADS - 128 * SWG) * REGS_REST <= NTHREADS * REGS_LAUNCH, "registers");
   // What shared memory leaves beside q and P.  bf16 rows: a ring of NK 64-column
-  // K chunks and one of NV 128-column V units.  FP8 rows: NK slots of codes (128
-  // rows x 128), NV units of converted columns that QK and P.V both read, and a
-  // slot for the RoPE columns.
-  static constexpr int NK = F8 ? (HB == 16 ? 3 : 2) : (HB == 16 ? 6 : (HB == 32 ? 5 : 4));
+  // K chunks and one of NV 128-column V units.  FP8 rows: a ring of NK slots for
+  // the RoPE columns and the four code blocks (128 rows x 128) of a tile, and NV
+  // units of converted columns that QK and P.V both read.
+  static constexpr int NK = F8 ? (HB == 16 ? 4 : 3) : (HB == 16 ? 6 : (HB == 32 ? 5 : 4));
   static constexpr int NV = F8 ? 4 : (HB == 64 ? 2 : 3);
-  static constexpr bool ROPE_SLOT = F8 && NC == 9;
   // warps that read the row ring: the loaders, and for FP8 rows the converters
-  static constexpr int NPROD = F8 ? NK + (ROPE_SLOT ? 1 : 0) + 8 : NK + 2 * NV;
+  static constexpr int NPROD = F8 ? NK + NCONV : NK + 2 * NV;
   static_assert(NPROD <= NWARPS - W_LOAD, "warps");
+  static_assert(!F8 || NV == 4, "a unit per code block");
   static constexpr uint32_t CHUNK_BYTES = BK * 128u;     // 128 keys x 64 columns
   static constexpr uint32_t UNIT_BYTES = 2u * CHUNK_BYTES;
   static constexpr uint32_t Q_BYTES = NC * HB * 128u;
@@ -108,8 +112,7 @@ struct Cfg {
   static constexpr uint32_t RED_FLOATS = 2u * SWG * 4u * HT;   // [parity][warpgroup][warp][head]
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + NK * CHUNK_BYTES;
-  static constexpr uint32_t OFF_R = OFF_V + NV * UNIT_BYTES;
-  static constexpr uint32_t OFF_Q = OFF_R + (ROPE_SLOT ? CHUNK_BYTES : 0u);
+  static constexpr uint32_t OFF_Q = OFF_V + NV * UNIT_BYTES;
   static constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
   static constexpr uint32_t OFF_ROWS = OFF_P + P_BYTES;
   static constexpr uint32_t OFF_META = OFF_ROWS + NI * BK * 4u;
@@ -141,10 +144,8 @@ enum {
   B_SMX = 60,        // [4] one per softmax warpgroup
   B_PLAN = 9,
   B_DRAIN = 24,      // [2] one per MMA issuer
-  B_FULL = 26,       // [16] K (or code) slots from 0, V units from 8
+  B_FULL = 26,       // [16] K slots (FP8: items of a tile) from 0, V units from 8
   B_EMPTY = 42,      // [16]
-  B_R_FULL = 11,     // RoPE columns (FP8 rows)
-  B_R_EMPTY = 58,
 };
 
 // flags of a tile
@@ -407,10 +408,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       if (i >= B_IDX_EMPTY && i < B_IDX_EMPTY + NI) n = 2 + C::SWG + C::NPROD + 1;
       if (i == B_S_EMPTY || i == B_S_EMPTY + 1 || i == B_O_EMPTY || i == B_O_EMPTY + 1 || i == B_P_FULL) n = 128 * C::SWG;
       if (i >= B_SMX && i < B_SMX + 4) n = 128;
-      // a V unit is two loading warps' work; codes are read, and units of FP8
-      // rows filled, by eight converting warps
+      // a V unit is two loading warps' work, one of FP8 rows eight converting warps'
       if (i >= B_FULL + 8 && i < B_FULL + 16) n = F8 ? 8 : 2;
-      if (F8 && i >= B_EMPTY && i < B_EMPTY + 8) n = 8;
       // a slot of a pair is free when both CTAs have read it
       if (PAIR && i >= B_EMPTY && i < B_EMPTY + 16) n = 2;
       mbar_init(&bars[i], n);
@@ -560,23 +559,26 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     } else if (const int nt = poll(B_PLAN, 0) ? *plan : 0; warp >= C::W_LOAD) {
       if constexpr (F8) {
         // ----------------------------------------------------------------
-        // FP8 rows.  Warp W_LOAD + s owns code slot s and loads 128-code blocks
-        // into it, warp W_LOAD + NK the RoPE columns (bf16, byte 528 of the row)
-        // into their slot; lanes as for bf16 rows.
-        // The last eight warps convert: thread = row and half of the block, 64 codes into
-        // the half's 64-column chunk of the unit, in the layout in which the bf16
-        // rows would have landed, by the arithmetic of the dequantize kernel.
+        // FP8 rows.  A tile is NC - 4 items: the RoPE columns (bf16, byte 528 of the
+        // row), then the four 128-code blocks; they go through the ring's NK slots in
+        // turn, warp W_LOAD + s loading every item of slot s, lanes as for bf16 rows.
+        // The barriers are by item (0 RoPE, 1 + m block m), a phase per tile, not by
+        // slot: a slot's phases would be now QK's, now the converters', and neither
+        // may pass over a phase that a parity tells apart.  QK gives an item's slot
+        // back: the RoPE columns when it has read them, a code block when the unit
+        // made of it is there.
+        // The converting warps, in sets of eight that take the units in turn: thread =
+        // row and half of the block, by the arithmetic of the dequantize kernel, into
+        // the unit as the bf16 rows would have landed.
         // ----------------------------------------------------------------
-        const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
-        if (warp < C::W_LOAD + C::NK + (C::ROPE_SLOT ? 1 : 0)) {
-          const bool rope = C::ROPE_SLOT && warp == C::W_LOAD + C::NK;
-          const int own = warp - C::W_LOAD, nslots = rope ? 1 : C::NK, stages = rope ? 1 : 4;
-          const uint32_t dst = sbase + (rope ? C::OFF_R : C::OFF_K + own * C::CHUNK_BYTES);
-          uint64_t* full = &bars[rope ? B_R_FULL : B_FULL + own];
-          const int empty = rope ? B_R_EMPTY : B_EMPTY + own;
+        constexpr int ITEMS = NC - 4;
+        if (warp < C::W_LOAD + C::NK) {
+          const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
+          const int own = warp - C::W_LOAD;
+          const uint32_t dst = sbase + C::OFF_K + own * C::CHUNK_BYTES;
           const uint64_t policy = evict_first_policy();
           int slot = 0;
-          uint32_t used = 0;
+          int had = -1, had_it = 0;   // the slot's item, its tile
           bool ok = true;
 #pragma unroll 1
           for (int it = 0; it < nt && ok; ++it) {
@@ -588,30 +590,34 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
 #pragma unroll 1
-            for (int st = 0; st < stages; ++st) {
-              const bool mine_now = rope || slot == own;
-              if (++slot == nslots) slot = 0;
+            for (int item = 5 - ITEMS; item < 5; ++item) {
+              const bool mine_now = slot == own;
+              if (++slot == C::NK) slot = 0;
               if (!mine_now) continue;
-              if (!doze(empty, (used & 1) ^ 1)) { ok = false; break; }
+              if (had >= 0 && !doze(B_EMPTY + had, had_it & 1)) { ok = false; break; }
+              had = item;
+              had_it = it;
+              uint64_t* full = &bars[B_FULL + item];
               if (lane == 0) {
                 mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
-                if (!rope && st == 0) DSA_TRACE(a.tr, it, 1);
-                if (!rope && st == 3) DSA_TRACE(a.tr, it, 2);
+                if (item == 1) DSA_TRACE(a.tr, it, 1);
+                if (item == 4) DSA_TRACE(a.tr, it, 2);
               }
-              const int col = rope ? 528 : 128 * st;
+              const int col = item == 0 ? 528 : 128 * (item - 1);
               if (!box)
                 gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
               else if (lane < boxes)
                 load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
-              ++used;
             }
           }
-          if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
+          if (lane == 0 && had >= 0) mbar_wait_drain(&bars[B_FULL + had], had_it & 1, err);
           __syncwarp();
-        } else if (warp >= C::NWARPS - 8) {
-          const int row = (warp & 3) * 32 + lane, hf = (warp - (C::NWARPS - 8)) >> 2;
+        } else if (warp >= C::NWARPS - C::NCONV) {
+          constexpr int SETS = C::NCONV / 8;
+          const int cw = warp - (C::NWARPS - C::NCONV), set = cw >> 3, hf = (cw >> 2) & 1;
+          const int row = (warp & 3) * 32 + lane;
           const uint32_t rsw = (uint32_t)(row & 7);   // 128B swizzle phase of this row
-          uint32_t cs = 0, cphase = 0, us = 0, uphase = 1;   // code slot and unit, their phases
+          int first = NC - 8;                         // slot of the tile's first code block
           // the four block scales of the row, loaded a tile ahead (zero for a masked row)
           auto scales = [&](int it) {
             const int r = it % NI;
@@ -630,17 +636,15 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           for (int it = 0; it < nt && ok; ++it) {
             float4 sc = next;
             next = scales(it + 1);
+            if (SETS == 2 && set == 1) sc = make_float4(sc.y, sc.z, sc.w, 0.f);
 #pragma unroll 1
-            for (int m = 0; m < 4; ++m) {
-              if (!poll(B_FULL + cs, cphase) || !poll(B_EMPTY + 8 + us, uphase)) { ok = false; break; }
-              const uint32_t src = sbase + C::OFF_K + cs * C::CHUNK_BYTES + row * 128;
-              const uint32_t dst = sbase + C::OFF_V + us * C::UNIT_BYTES + hf * C::CHUNK_BYTES + row * 128;
+            for (int m = set; m < 4; m += SETS) {
+              if (!poll(B_FULL + 1 + m, it & 1) || !poll(B_EMPTY + 8 + m, (it & 1) ^ 1)) { ok = false; break; }
+              const uint32_t src = sbase + C::OFF_K + (first + m) % C::NK * C::CHUNK_BYTES + row * 128;
+              const uint32_t dst = sbase + C::OFF_V + m * C::UNIT_BYTES + hf * C::CHUNK_BYTES + row * 128;
               uint4 w[4];
 #pragma unroll
               for (int pp = 0; pp < 4; ++pp) w[pp] = lds128(src + ((((uint32_t)(4 * hf + pp)) ^ rsw) << 4));
-              // every code this warp reads is in registers
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[B_EMPTY + cs]);
 #pragma unroll
               for (int pp = 0; pp < 4; ++pp) {
                 uint32_t v[8];
@@ -653,11 +657,10 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
               }
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[B_FULL + 8 + us]);
-              sc = make_float4(sc.y, sc.z, sc.w, 0.f);
-              if (++cs == C::NK) { cs = 0; cphase ^= 1; }
-              if (++us == C::NV) { us = 0; uphase ^= 1; }
+              if (lane == 0) mbar_arrive(&bars[B_FULL + 8 + m]);
+              sc = SETS == 2 ? make_float4(sc.z, sc.w, 0.f, 0.f) : make_float4(sc.y, sc.z, sc.w, 0.f);
             }
+            first = (first + ITEMS) % C::NK;
           }
           __syncwarp();
         }
@@ -765,6 +768,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       const uint64_t k_desc = sdesc_sw128(sbase + C::OFF_K, 16, 1024), q_desc = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       int nq = -1;
       uint32_t slot = 0, phase = 0;
+      uint32_t cs = 0;   // (FP8 rows: the RoPE columns' slot; slot and phase are the units')
       bool ok = true;
 #pragma unroll 1
       for (int it = 0; it < nt && ok; ++it) {
@@ -780,16 +784,18 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         if (!poll(B_S_EMPTY + sb, ((it >> 1) & 1) ^ 1)) break;
         if constexpr (F8) {
           if constexpr (NC == 9) {
-            if (!poll(B_R_FULL, it & 1)) break;
+            if (!poll(B_FULL, it & 1)) break;
             tc_fence_after();
-            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)((C::OFF_R - C::OFF_K) >> 4),
+            mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)(cs * (C::CHUNK_BYTES >> 4)),
                            q_desc + (uint64_t)(8 * (HB * 128) >> 4), 2u, 2u, IDESC, 0u);
-            commit_elected(leader, &bars[B_R_EMPTY]);
+            commit_elected(leader, &bars[B_EMPTY]);
+            cs = (cs + 5) % C::NK;
           }
           // the units that P.V reads too, which it gives back
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
             if (!poll(B_FULL + 8 + slot, phase)) { ok = false; break; }
+            if (leader) mbar_arrive(&bars[B_EMPTY + 1 + m]);   // (its codes are read)
             tc_fence_after();
             if (leader && m == 0) DSA_TRACE(a.tr, it, 3);
             if (leader && m == 3) DSA_TRACE(a.tr, it, 4);
