@@ -31,6 +31,7 @@ import subprocess
 import sys
 import threading
 import time
+import types
 
 import numpy as np
 
@@ -908,6 +909,20 @@ def run_profile_case(args):
             k, v = to_dev(x.k, dev), to_dev(x.v, dev)
             fn = lambda: dsa.dsa_masked_mha_prefill(q, k, v, km, w.scale, cu_seqlens_q=x.cu_seqlens_q,
                                                     cu_seqlens_kv=x.cu_seqlens_kv)
+    elif args.profile.startswith("decode"):
+        # one new token of 64 requests of 256 to 16384 positions (16 of 500 to 9001 for the CTA pairs), pages of 64
+        H, fp8, (B, lo, hi) = {"decode": (32, False, (64, 256, 16384)), "decode_fp8": (16, True, (48, 1024, 16384)),
+                               "decode_pair": (128, False, (16, 500, 9001))}[args.profile]
+        rng = np.random.default_rng(0)
+        lens = torch.from_numpy(rng.integers(lo, hi + 1, B).astype(np.int32)).to(dev)
+        pages = -(-hi // 64)
+        cache = torch.randn(B * pages * 64, 576, device=dev, dtype=torch.bfloat16)
+        if fp8:
+            cache = dsa.dsa_kv_fp8_quantize(cache, 64)
+        table = torch.from_numpy(rng.permutation(B * pages).astype(np.int32).reshape(B, pages)).to(dev)
+        q = torch.randn(B, H, 576, device=dev, dtype=torch.bfloat16)
+        w = types.SimpleNamespace(name=f"{args.profile}_{B}x{lo}-{hi}_h{H}", T=B)
+        fn = lambda: dsa.dsa_paged_decode(q, cache, table, lens, 64, 192 ** -0.5)
     else:
         raise ValueError(args.profile)
     ms = timed_steps(fn, args.steps, args.warmup, torch.cuda.current_stream(dev))
@@ -930,7 +945,8 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--e2e-chunk", type=int, default=1216, help="tokens per chunk of the host-buffer call (8 per SM)")
     ap.add_argument("--cpu-budget", type=float, default=12.0, help="seconds of oracle work per core")
-    ap.add_argument("--profile", choices=["sparse", "sparse_fp8", "union", "grouped", "masked"], default=None,
+    ap.add_argument("--profile", choices=["sparse", "sparse_fp8", "union", "grouped", "masked", "decode", "decode_fp8",
+                                            "decode_pair"], default=None,
                     help="run a small case of one kernel (for ncu) instead of the benchmark")
     ap.add_argument("--profile-tokens", type=int, default=2048)
     ap.add_argument("--profile-workload", default=None,

@@ -173,6 +173,7 @@ __device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* err
 template <bool POLL, bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
   const uint64_t t0 = globaltimer();
+  uint32_t turns = 0;
 #pragma unroll 1
   while (true) {
     uint32_t ok;
@@ -185,6 +186,8 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     else
       ok = CLUSTER ? mbar_try_wait_cluster_sleep(bar, parity) : mbar_try_wait_sleep(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
+    // (the flag and the clock on every sixteenth turn: a poll is already a shared-memory access)
+    if (POLL && (++turns & 15u)) continue;
     if (*abort_flag) return false;
     if (globaltimer() - t0 > kWaitTimeoutNs) {
       give_up(abort_flag, err);
