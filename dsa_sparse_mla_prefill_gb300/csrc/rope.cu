@@ -18,7 +18,8 @@
 // from two pieces) and walks over heads with four loads in flight; the heads of
 // a token are dealt to as many threads as it takes to fill the GPU, so that one
 // token's call is as wide as it can be and a long prompt computes each cos and
-// sin once per several heads.
+// sin once per several heads.  16384 tokens of 32 heads x 64 in bf16: 25.6 us, 5.2
+// TB/s; one token 2.2 us, the launch.
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
 
@@ -174,13 +175,15 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
 // columns turned) into row table[r][p / block_size] * block_size + p %
 // block_size of the cache, r being the token's request and p its position.
 // The FP8 row is the one the quantize kernel writes for the same bf16 row
-// (the same scale and conversion, e4m3_block_scale and e4m3_quantize2), the RoPE columns being rounded to bf16 first.
+// (the same scale and conversion, e4m3_block_scale and e4m3_quantize2), the RoPE
+// columns being rounded to bf16 first.
 //
 // Bound: HBM; a decode step's handful of tokens by the launch and two
 // dependent loads (position, then block id).  One warp per token: lane l holds
 // columns 16 l .. 16 l + 15 (eight lanes are a 128-column block of the
 // quantization) and pair l of the RoPE columns, all loaded before the row is
-// looked up.
+// looked up.  128 tokens 2.1 us; 16384 FP8 rows and reading them back as bf16
+// 15.8 us; a ragged chunk of 8000 tokens 4.5 us (8.1 with half a CTA per token).
 // --------------------------------------------------------------------------
 constexpr int NT_APPEND = 64;   // (2 tokens: 16384 of them 4 % faster than 4 or 8 per CTA)
 
