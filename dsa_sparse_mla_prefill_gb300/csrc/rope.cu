@@ -183,7 +183,7 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
 // columns 16 l .. 16 l + 15 (eight lanes are a 128-column block of the
 // quantization) and pair l of the RoPE columns, all loaded before the row is
 // looked up.  128 tokens 2.1 us; 16384 FP8 rows and reading them back as bf16
-// 15.8 us; a ragged chunk of 8000 tokens 4.5 us (8.1 with half a CTA per token).
+// 15.8 us; a ragged chunk of 8312 tokens 4.5 us (8.1 with half a CTA per token).
 // --------------------------------------------------------------------------
 constexpr int NT_APPEND = 64;   // (2 tokens: 16384 of them 4 % faster than 4 or 8 per CTA)
 

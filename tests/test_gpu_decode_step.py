@@ -366,6 +366,40 @@ def test_decode_long_context_is_split(fmt, H):
     d.check(d.run())
 
 
+@pytest.mark.parametrize("H,d_rope,bs,k", [(65, 64, 4, 0), (100, 0, 64, 0), (128, 64, 128, 0), (127, 64, 100, 0),
+                                           (80, 64, 16, 300), (128, 0, 64, 77)])
+def test_decode_head_pairs(H, d_rope, bs, k):
+    """More than 64 heads: two CTAs share every row; heads that fill neither, boxes and gathers mixed in a tile's run,
+    requests without keys, ranges without tiles."""
+    d = Decode(H, [700, 33, 0, 257, 1024, 5, 0, 128, 2500], H, bs=bs, d_rope=d_rope, k=k, ld_extra=8, spread=3.0)
+    d.check(d.run())
+    d.lens = np.array([3, 0, 0, 0, 0, 0, 0, 0, 0], np.int32)
+    if k:
+        d.idx[1:] = -1
+        d.idx[0, :k] = -1
+        d.idx[0, k - 1] = 2
+    d.check(d.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_calls_in_a_row_give_the_same_bits(fmt):
+    """Launches that overlap each other's ends, of different head counts and in one workspace."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    sets = [Decode(40 + i, [2000, 64, 0, 5000], H, bs=64, fmt=fmt) for i, H in enumerate((16, 128, 32))]
+    ws = torch.empty(max(dsa.dsa_paged_decode_workspace(4, d.H, d.bt.shape[1] * 64) for d in sets), dtype=torch.uint8,
+                     device="cuda")
+    args = [(bf(d.q), d.cache, i32(d.bt), i32(d.lens), 64, d.scale) for d in sets]
+    first = [d.run() for d in sets]
+    for d, got in zip(sets, first):
+        d.check(got)
+    outs = [[dsa.dsa_paged_decode(*a, workspace=ws) for a in args] for _ in range(20)]
+    torch.cuda.synchronize()
+    for row in outs:
+        for (o, l), (o0, l0) in zip(row, first):
+            assert torch.equal(o, o0) and torch.equal(l, l0)
+    assert bad_count() == 0
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_decode_many_short_requests(fmt):
     rng = np.random.default_rng(5)
