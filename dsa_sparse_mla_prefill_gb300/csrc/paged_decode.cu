@@ -210,15 +210,6 @@ __device__ __forceinline__ uint64_t evict_normal_policy() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-__device__ __forceinline__ void gather4_hint(uint32_t dst, const CUtensorMap* map, int x, const int4& r, uint64_t* bar,
-                                             uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
-      "l"(policy)
-      : "memory");
-}
 __device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
                                              uint64_t policy) {
   asm volatile(
@@ -230,15 +221,6 @@ __device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* ma
 
 // The same into both CTAs of a pair, at the same shared-memory offset, the bytes
 // counted on each one's own barrier.
-__device__ __forceinline__ void gather4_pair(uint32_t dst, const CUtensorMap* map, int x, const int4& r, uint64_t* bar,
-                                             uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %9, %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
-      "l"(policy), "h"((uint16_t)3)
-      : "memory");
-}
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
                                              uint64_t policy) {
   asm volatile(
@@ -280,6 +262,34 @@ __device__ __forceinline__ void commit_elected(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+// Row gathers n0 .. n1 - 1 of a tile's 32 (4 rows x 128 bytes each), issued by one
+// elected lane as the MMAs are (a lane per gather: 777 positions 13.9 against 13.4 us).
+template <bool PAIR>
+__device__ __forceinline__ void gather_rows(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, const int32_t* rows,
+                                            int n0, int n1, uint64_t* bar, uint64_t policy) {
+#pragma unroll 4
+  for (int n = n0; n < n1; ++n) {
+    const int4 r = *reinterpret_cast<const int4*>(rows + 4 * n);
+    if constexpr (!PAIR)
+      asm volatile(
+          "{\n\t.reg .pred e;\n\t"
+          "setp.ne.b32 e, %9, 0;\n\t"
+          "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
+          "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n\t}" ::"r"(dst + n * 512),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
+          "l"(policy), "r"(leader)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred e;\n\t"
+          "setp.ne.b32 e, %10, 0;\n\t"
+          "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
+          ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %9, %8;\n\t}" ::"r"(dst + n * 512),
+          "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
+          "l"(policy), "h"((uint16_t)3), "r"(leader)
+          : "memory");
+  }
+}
 // (arrives on the barrier of either CTA of a pair)
 __device__ __forceinline__ void commit_elected_pair(uint32_t leader, uint64_t* bar) {
   asm volatile(
@@ -564,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         // ----------------------------------------------------------------
         // FP8 rows.  A tile is NC - 4 items: the RoPE columns (bf16, byte 528 of the
         // row), then the four 128-code blocks; they go through the ring's NK slots in
-        // turn, warp W_LOAD + s loading every item of slot s, lanes as for bf16 rows.
+        // turn, warp W_LOAD + s loading every item of slot s.
         // The barriers are by item (0 RoPE, 1 + m block m), a phase per tile, not by
         // slot: a slot's phases would be now QK's, now the converters', and neither
         // may pass over a phase that a parity tells apart.  QK gives an item's slot
@@ -580,6 +590,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           const int own = warp - C::W_LOAD;
           const uint32_t dst = sbase + C::OFF_K + own * C::CHUNK_BYTES;
           const uint64_t policy = evict_first_policy();
+          const uint32_t leader = elect_one();
           int slot = 0;
           int had = -1, had_it = 0;   // the slot's item, its tile
           bool ok = true;
@@ -588,10 +599,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             const int r = it % NI;
             if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
             const bool box = (meta[r].y & F_BOX) != 0;
-            int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
-            if (box) x.x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+            const int x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];   // (a box's first row)
 #pragma unroll 1
             for (int item = 5 - ITEMS; item < 5; ++item) {
               const bool mine_now = slot == own;
@@ -601,17 +609,20 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
               had = item;
               had_it = it;
               uint64_t* full = &bars[B_FULL + item];
-              if (lane == 0) {
+              if (leader) {
                 mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
                 if (item == 1) DSA_TRACE(a.tr, it, 1);
                 if (item == 4) DSA_TRACE(a.tr, it, 2);
               }
               const int col = item == 0 ? 528 : 128 * (item - 1);
+              __syncwarp();
               if (!box)
-                gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+                gather_rows<false>(leader, dst, &a.tmap_kv, col, rows + r * BK, 0, BK / 4, full, policy);
               else if (lane < boxes)
-                load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+                load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
           }
           if (lane == 0 && had >= 0) mbar_wait_drain(&bars[B_FULL + had], had_it & 1, err);
           __syncwarp();
@@ -671,11 +682,13 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       // ------------------------------------------------------------------
       // row loads: a warp per 64-column chunk in flight, since a warp issues row
       // gathers one after another (about 80 cycles each).  Warp W_LOAD + s owns K
-      // slot s, the two warps after those a half of V slot 0, and so on: lane l
-      // gathers rows 4l .. 4l+3, or where the keys lie in runs of box_rows rows
-      // lane l loads box l of 128 / box_rows.  Each warp opens its chunk's share
-      // of every phase of its slot: none can fall behind it, which a wait on
-      // parity would not notice.
+      // slot s, the two warps after those a half of V slot 0, and so on: 32 gathers
+      // of four rows, or where the keys lie in runs of box_rows rows 128 / box_rows
+      // boxes, one a lane.  Gathers are the slower form: 6.2 us a tile of 32 heads
+      // with all rows in L2, 9 with rows all over HBM, boxes 2.5 and 3.3 (16-byte
+      // asynchronous copies instead of them: 7.9 and 10).  Each warp opens its
+      // chunk's share of every phase of its slot: none can fall behind it, which a
+      // wait on parity would not notice.
       // ------------------------------------------------------------------
       const bool ks = warp < C::W_LOAD + C::NK;
       const int vw = warp - C::W_LOAD - C::NK;
@@ -689,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         const int col_step = ks ? 64 : 128;
         const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
         // of a pair each CTA loads half of the rows, for both
-        const bool by_gather = !PAIR || (lane >> 4) == hb;
+        const uint32_t leader = elect_one();
         const bool by_box = PAIR ? lane < boxes && (2 * lane >= boxes) == (hb == 1) : lane < boxes;
         const uint64_t policy = ks ? evict_normal_policy() : evict_first_policy();
         int slot = 0;
@@ -700,10 +713,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           const int r = it % NI;
           if (!doze(B_IDX_FULL + r, (it / NI) & 1)) break;
           const bool box = (meta[r].y & F_BOX) != 0;
-          int4 x = *reinterpret_cast<const int4*>(rows + r * BK + 4 * lane);
-          if (box) x.x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
+          const int x = rows[r * BK + (lane & (boxes - 1)) * a.box_rows];   // (a box's first row)
           int col = hf * 64;
 #pragma unroll 1
           for (int st = 0; st < stages; ++st, col += col_step) {
@@ -711,20 +721,23 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             if (++slot == nslots) slot = 0;
             if (!mine_now) continue;
             if (!wait<false, PAIR>(bar(empty), (used & 1) ^ 1, abort_flag, err)) { ok = false; break; }
-            if (lane == 0) {
+            if (leader) {
               mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
               if (ks && st == 0) DSA_TRACE(a.tr, it, 1);
               if (ks && st == NC - 1) DSA_TRACE(a.tr, it, 2);
             }
+            __syncwarp();
             if (!box) {
-              if constexpr (!PAIR) gather4_hint(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
-              else if (by_gather) gather4_pair(dst + lane * 512, &a.tmap_kv, col, x, full, policy);
+              gather_rows<PAIR>(leader, dst, &a.tmap_kv, col, rows + r * BK, PAIR ? 16 * hb : 0, PAIR ? 16 * hb + 16 : 32, full,
+                                policy);
             } else if (by_box) {
-              if constexpr (!PAIR) load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
-              else load_2d_pair(dst + lane * a.box_rows * 128, &a.tmap_box, col, x.x, full, policy);
+              if constexpr (!PAIR) load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
+              else load_2d_pair(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
             }
             ++used;
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
         }
         // let the slot's last copies land before the CTA can exit
         if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
