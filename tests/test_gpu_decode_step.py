@@ -681,6 +681,31 @@ def test_decode_two_graphs_at_once():
         d.check(o)
 
 
+def test_decode_head_pairs_in_graphs_at_once():
+    """CTA pairs in two captured graphs on two streams, and a call over FP8 rows beside them."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    ds = [Decode(33, [2500, 70, 900], 128), Decode(34, [4000], 70, bs=64), Decode(35, [10, 1300], 16, fmt="fp8")]
+    held, s = [], [torch.cuda.Stream() for _ in range(3)]
+    for d in ds[:2]:
+        args = (bf(d.q), d.cache, i32(d.bt), i32(d.lens), d.bs, d.scale)
+        dsa.dsa_paged_decode(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = dsa.dsa_paged_decode(*args)
+        held.append((g, out, args))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (g, *_), st in zip(held, s):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(s[2]):
+            third = ds[2].run()
+    torch.cuda.synchronize()
+    for d, o in zip(ds, [held[0][1], held[1][1], third]):
+        d.check(o)
+
+
 # ---------------------------------------------------------------------------
 # the step: rotate the queries, append the new rows, attend
 # ---------------------------------------------------------------------------
