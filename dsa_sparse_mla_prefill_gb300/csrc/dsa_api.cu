@@ -684,7 +684,6 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   const int d_rope = d_qk - 512;
   a.rows_base = static_cast<const uint8_t*>(cache);
   a.row_bytes = fp8 ? 528 + 2 * d_rope : 2 * ld_kv;
-  a.row_used = fp8 ? a.row_bytes : 2 * d_qk;
   a.block_table = block_table;
   a.kv_lens = kv_lens;
   a.idx = idx;

@@ -100,8 +100,8 @@ struct DecodeArgs {
   CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box
   CUtensorMap tmap_box;       // cache rows, 64-column x box_rows box (unset when box_rows = 0)
   CUtensorMap tmap_q;         // q viewed [B*H, d_qk], 64-column x HB-row box
-  const uint8_t* rows_base;   // the cache rows as bytes, their pitch, and the bytes of each that are read
-  int row_bytes, row_used;
+  const uint8_t* rows_base;   // the cache rows as bytes, and their pitch
+  int row_bytes;
   int box_rows;               // rows that a page holds in one run: 8 .. 128, a power of two; 0 = gather rows
   const int32_t* block_table; // [B, max_blocks]
   const int32_t* kv_lens;     // [B]

@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       len = __shfl_sync(0xffffffffu, len, holder & 31);
       int bad = 0;
       const bool from_start = j == 0;   // the range's first request begins in it
+      int fetch = -1, fetch_next = -1;  // first rows of boxes to fetch
       bool enter = true;                // the next tile is the first of request b here
       int seg = 0;                    // requests begun
       for (int it = 0; it < nt; ++it) {
@@ -543,6 +544,21 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         }
         *reinterpret_cast<int4*>(rows + r * BK + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
         const bool box = __all_sync(0xffffffffu, (row[0] | row[1] | row[2] | row[3]) >= 0) && a.box_rows > 0;
+        // 64 heads: q leaves room for 128 KB of rows in flight, too little for HBM's
+        // latency, so the boxes of the tile two back, about a tile ahead of its loads,
+        // are fetched to L2, by each CTA of a pair its half (64 x 19456 at 64 heads
+        // 290 -> 265 us, 16 x 19456 at 128 142 -> 135; a tile earlier 274 and 129, but
+        // 16 x 500..9001 50.3 instead of 49).  Not with fewer heads (64 x 256..16384 at
+        // 32: 74 -> 79) nor for gathers (96 x 2048 listed at 64 heads: 109 -> 116).
+        if constexpr (HB == 64) {
+          if (fetch >= 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.rows_base + (int64_t)fetch * a.row_bytes),
+                         "r"(a.row_bytes * a.box_rows)
+                         : "memory");
+          fetch = fetch_next;
+          fetch_next = __shfl_sync(0xffffffffu, row[0], (lane * a.box_rows / 4) & 31);   // of box `lane`
+          if (!box || lane >= BK / a.box_rows || (PAIR && (lane & 1) != hb)) fetch_next = -1;
+        }
         const bool first = enter;
         const bool last = (it == nt - 1) || (j == n - 1);
         if (lane == 0) {
