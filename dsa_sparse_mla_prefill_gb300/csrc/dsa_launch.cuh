@@ -1,0 +1,35 @@
+// A launch whose start may overlap the end of the kernel before it on the stream.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace dsa {
+
+// Programmatic stream serialization: the grid may be put on the GPU once every CTA of
+// the kernel before has ended or called launch_dependents().  Such a kernel calls
+// wait_for_previous() before it touches global memory.  cluster: CTAs of a cluster.
+template <typename... P, typename... A>
+static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t stream,
+                        const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
+}
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace dsa

@@ -72,6 +72,7 @@
 
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "dsa_launch.cuh"
 
 namespace dsa {
 namespace decode {
@@ -444,12 +445,12 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
   const int64_t heads_padded = (int64_t)a.head_blocks * HB;
 
   // the joining kernel may be put on the GPU as soon as there is room
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
 
   if (warp >= C::W_QK) {
     regs_dec<C::REGS_REST>();
     // what earlier kernels wrote may be read from here on
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     if (warp == C::W_SCHED) {
       // ------------------------------------------------------------------
       // scheduler
@@ -927,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     float m_run[HT], l_exact[HT], l_used[HT];
 #pragma unroll
     for (int h = 0; h < HT; ++h) { m_run[h] = -FLT_MAX; l_exact[h] = 0.f; l_used[h] = 0.f; }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     const int nt = poll(B_PLAN, 0) ? *plan : 0;
 #pragma unroll 1
     for (int it = 0; it < nt; ++it) {
@@ -1152,8 +1153,8 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   __shared__ float4 acc[3][32];
   __shared__ float wgt[4][32 * LSE];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  launch_dependents();
+  wait_for_previous();
   const uint2 head = reinterpret_cast<const uint2*>(a.borders)[0];
   const int4 at = a.borders[1 + blockIdx.x];            // the end of range blockIdx.x
   const uint32_t total = head.x, ng = head.y, g = blockIdx.x;
@@ -1240,26 +1241,6 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
       a.lse[b * a.H + h] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     if (lg > 0) __syncthreads();
   }
-}
-
-template <typename... P, typename... A>
-static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t stream,
-                        const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
 }
 
 template <int HB, int NC, bool F8, bool PAIR = false>

@@ -18,10 +18,13 @@
 // from two pieces) and walks over heads with four loads in flight; the heads of
 // a token are dealt to as many threads as it takes to fill the GPU, so that one
 // token's call is as wide as it can be and a long prompt computes each cos and
-// sin once per several heads.  16384 tokens of 32 heads x 64 in bf16: 25.6 us, 5.2
-// TB/s; one token 2.2 us, the launch.
+// sin once per several heads.  16384 tokens of 32 heads x 64 in bf16: 25.4 us, 5.3
+// TB/s; one token 1.9 us, the launch.  Both kernels are launched to start while the
+// one before ends (2 to 20 % of back-to-back calls); they let the next one start only
+// when they end (earlier, its waiting CTAs cost a ragged append 5.8 against 4.3 us).
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "dsa_launch.cuh"
 
 namespace dsa {
 namespace rope {
@@ -85,6 +88,7 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
   const uint32_t item = g % items, rest = g / items;
   const uint32_t hg = rest % (uint32_t)a.head_groups, t = rest / (uint32_t)a.head_groups;
   if (t >= (uint32_t)a.T) return;
+  wait_for_previous();
   const int32_t pos = __ldg(a.positions + t);
   float c[PPT], s[PPT];
 #pragma unroll
@@ -166,8 +170,7 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
   a.head_groups = (a.H + each - 1) / each;
   const int64_t blocks = (per_group * a.head_groups + NT - 1) / NT;
   if (blocks * NT > 0xffffffffll) return -2;
-  rope_kernel<E, HALF, VEC><<<(unsigned)blocks, NT, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_after(rope_kernel<E, HALF, VEC>, dim3((unsigned)blocks), NT, 0, 1, stream, a);
 }
 
 // --------------------------------------------------------------------------
@@ -182,8 +185,8 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
 // dependent loads (position, then block id).  One warp per token: lane l holds
 // columns 16 l .. 16 l + 15 (eight lanes are a 128-column block of the
 // quantization) and pair l of the RoPE columns, all loaded before the row is
-// looked up.  128 tokens 2.1 us; 16384 FP8 rows and reading them back as bf16
-// 15.8 us; a ragged chunk of 8312 tokens 4.5 us (8.1 with half a CTA per token).
+// looked up.  128 tokens 1.9 us; 16384 FP8 rows and reading them back as bf16
+// 15.9 us; a ragged chunk of 8312 tokens 4.3 us (8.1 with half a CTA per token).
 // --------------------------------------------------------------------------
 constexpr int NT_APPEND = 64;   // (2 tokens: 16384 of them 4 % faster than 4 or 8 per CTA)
 
@@ -207,6 +210,7 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (NT_APPEND / 32) + (threadIdx.x >> 5);
   if (t >= a.T) return;
+  wait_for_previous();
   const uint4* src = reinterpret_cast<const uint4*>(a.c_kv + t * a.c_stride) + 2 * lane;
   const uint4 w0 = src[0], w1 = src[1];
   const bool half = a.table.layout == DSA_ROPE_HALF;
@@ -276,9 +280,8 @@ int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t strea
 int launch_kv_append(const AppendArgs& a, bool fp8, cudaStream_t stream) {
   using namespace rope;
   const unsigned grid = (unsigned)(((int64_t)a.T + NT_APPEND / 32 - 1) / (NT_APPEND / 32));
-  if (fp8) append_kernel<true><<<grid, NT_APPEND, 0, stream>>>(a);
-  else append_kernel<false><<<grid, NT_APPEND, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return fp8 ? launch_after(append_kernel<true>, dim3(grid), NT_APPEND, 0, 1, stream, a)
+             : launch_after(append_kernel<false>, dim3(grid), NT_APPEND, 0, 1, stream, a);
 }
 
 }  // namespace dsa
