@@ -26,7 +26,9 @@ static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t s
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return 0;
+  cudaGetLastError();   // (reported here, not by the next launch)
+  return -1;
 }
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

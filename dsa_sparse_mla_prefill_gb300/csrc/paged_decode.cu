@@ -39,7 +39,7 @@
 //   W_SCHED     walks the range, turns 128 positions per tile into rows (a ring of
 //               four tiles ahead)
 //   W_LOAD ...  TMA loads: row gathers (4 rows x 128 bytes per instruction), or
-//               boxes of up to 128 rows where every key of the tile is there and
+//               boxes of up to 128 rows (64 of a pair) where every key of the tile is there and
 //               the pages hold them in runs (page sizes that are multiples of 8
 //               rows); for FP8 rows the last eight (16) convert.
 //
@@ -53,8 +53,9 @@
 // at 16 heads, its four conversions (some 700 cycles apart), the softmax and the
 // first P.V one after another.  The conversion is a chain of latencies (two waits,
 // load, convert, store, fence), not of arithmetic (none at all: the same time), so
-// where registers allow (16 heads) two sets of eight warps take the units in turn:
-// 48 requests up to 16384 positions 68 us, 71 with one set.
+// where registers allow two sets of eight warps take the units in turn: 48 requests
+// up to 16384 positions at 16 heads 68 us, 71 with one set (at 32 heads, with 40
+// registers a thread, 16 x 19456 would take 96 us instead of 85).
 // Rows that are masked (behind kv_len, -1, unmapped pages) are loaded from
 // outside the tensor map, which reads as zeros: whatever the cache holds there,
 // NaN included, never reaches the sums.
