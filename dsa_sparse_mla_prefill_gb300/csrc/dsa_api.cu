@@ -717,9 +717,7 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   if (!mapped) return DSA_ERR_CUDA;
   // whole-context calls load runs of rows: the largest power of two in the page size, at most a tile
   const int run = block_size & -block_size;
-  // (half a tile for a CTA pair, which loads half each)
-  const int box = dsa::decode_pairs(H, fp8) ? 64 : 128;
-  a.box_rows = idx || none || run < 8 ? 0 : (run < box ? run : box);
+  a.box_rows = idx || none || run < 8 ? 0 : (run < 128 ? run : 128);
   if (a.box_rows &&
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))

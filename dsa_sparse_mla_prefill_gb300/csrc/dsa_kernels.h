@@ -212,8 +212,6 @@ inline int decode_heads_per_cta(int H, bool fp8) { return H <= 16 ? 16 : (H <= 3
 inline int decode_head_blocks(int H, bool fp8) {
   return (H + decode_heads_per_cta(H, fp8) - 1) / decode_heads_per_cta(H, fp8);
 }
-// More than 64 heads over bf16 rows: the two CTAs are a cluster and load every row once for both.
-inline bool decode_pairs(int H, bool fp8) { return decode_heads_per_cta(H, fp8) == 64 && decode_head_blocks(H, fp8) == 2; }
 constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
 // max_tiles: an upper bound of a request's key tiles (1: nothing is split).
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);

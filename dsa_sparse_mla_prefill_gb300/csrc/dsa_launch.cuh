@@ -8,24 +8,19 @@ namespace dsa {
 
 // Programmatic stream serialization: the grid may be put on the GPU once every CTA of
 // the kernel before has ended or called launch_dependents().  Such a kernel calls
-// wait_for_previous() before it touches global memory.  cluster: CTAs of a cluster.
+// wait_for_previous() before it touches global memory.
 template <typename... P, typename... A>
-static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t stream,
-                        const A&... args) {
+static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return 0;
   cudaGetLastError();   // (reported here, not by the next launch)
   return -1;

@@ -22,11 +22,8 @@
 // A group is one CTA per 16 heads (H <= 16), 32 (H <= 32, and FP8 rows) or 64, all
 // walking the same rows at the same time.  Fewer, wider CTAs per group read fewer
 // copies of a row through L2: at 128 heads, 16 x 19456 positions take 193 us as 4
-// CTAs of 32 heads and 123 us as 2 of 64 (all pages in L2).  Over bf16 rows the two
-// CTAs of more than 64 heads are a cluster: each loads half of the rows, multicast
-// to both, which halves the row gathers (96 requests x 2048 listed positions, 128
-// heads: 134 us, 186 without; pages of 4 rows, 16 x 19456: 175 and 215; with boxes
-// the two forms are within 4 %).
+// CTAs of 32 heads and 123 us as 2 of 64 (all pages in L2).  Each CTA loads what its
+// own MMAs read, into its own shared memory.
 //
 // One CTA (24 warps; 28 of the 64-head form, 32 of 16 heads over FP8 rows):
 //   softmax     8 warps (16): thread = key (TMEM lane), warpgroup = its share of
@@ -39,7 +36,7 @@
 //   W_SCHED     walks the range, turns 128 positions per tile into rows (a ring of
 //               four tiles ahead)
 //   W_LOAD ...  TMA loads: row gathers (4 rows x 128 bytes per instruction), or
-//               boxes of up to 128 rows (64 of a pair) where every key of the tile is there and
+//               boxes of up to 128 rows where every key of the tile is there and
 //               the pages hold them in runs (page sizes that are multiples of 8
 //               rows); for FP8 rows the last eight (16) convert.
 //
@@ -171,8 +168,7 @@ __device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* err
   if (*abort_flag == 0) atomicAdd(err + ERR_TIMEOUT, 1u);
   *abort_flag = 1;
 }
-// CLUSTER: the phase is completed by the peer CTA too.
-template <bool POLL, bool CLUSTER = false>
+template <bool POLL>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
   const uint64_t t0 = globaltimer();
   uint32_t turns = 0;
@@ -186,7 +182,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
           "selp.u32 %0, 1, 0, p;\n\t}"
           : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     else
-      ok = CLUSTER ? mbar_try_wait_cluster_sleep(bar, parity) : mbar_try_wait_sleep(bar, parity);
+      ok = mbar_try_wait_sleep(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     // (the flag and the clock on every sixteenth turn: a poll is already a shared-memory access)
     if (POLL && (++turns & 15u)) continue;
@@ -218,17 +214,6 @@ __device__ __forceinline__ void load_2d_hint(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
       "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
-// The same into both CTAs of a pair, at the same shared-memory offset, the bytes
-// counted on each one's own barrier.
-__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
-                                             uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %6, %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "h"((uint16_t)3)
       : "memory");
 }
 
@@ -264,42 +249,22 @@ __device__ __forceinline__ void commit_elected(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
-// Row gathers n0 .. n1 - 1 of a tile's 32 (4 rows x 128 bytes each), issued by one
+// A tile's 32 row gathers (4 rows x 128 bytes each), issued by one
 // elected lane as the MMAs are (a lane per gather: 777 positions 13.9 against 13.4 us).
-template <bool PAIR>
 __device__ __forceinline__ void gather_rows(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, const int32_t* rows,
-                                            int n0, int n1, uint64_t* bar, uint64_t policy) {
+                                            uint64_t* bar, uint64_t policy) {
 #pragma unroll 4
-  for (int n = n0; n < n1; ++n) {
+  for (int n = 0; n < BK / 4; ++n) {
     const int4 r = *reinterpret_cast<const int4*>(rows + 4 * n);
-    if constexpr (!PAIR)
-      asm volatile(
-          "{\n\t.reg .pred e;\n\t"
-          "setp.ne.b32 e, %9, 0;\n\t"
-          "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
-          "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n\t}" ::"r"(dst + n * 512),
-          "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
-          "l"(policy), "r"(leader)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred e;\n\t"
-          "setp.ne.b32 e, %10, 0;\n\t"
-          "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-          ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %9, %8;\n\t}" ::"r"(dst + n * 512),
-          "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
-          "l"(policy), "h"((uint16_t)3), "r"(leader)
-          : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %9, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n\t}" ::"r"(dst + n * 512),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar)),
+        "l"(policy), "r"(leader)
+        : "memory");
   }
-}
-// (arrives on the barrier of either CTA of a pair)
-__device__ __forceinline__ void commit_elected_pair(uint32_t leader, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
-      ::"r"(smem_u32(bar)), "r"(leader), "h"((uint16_t)3)
-      : "memory");
 }
 
 // The row of a page's at-th position, or -1 (counted).
@@ -385,7 +350,7 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float* v) {
   }
 }
 
-template <int HB, int NC, bool F8, bool PAIR>
+template <int HB, int NC, bool F8>
 __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<HB, NC, F8>;
   constexpr int HT = C::HT;
@@ -425,8 +390,6 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       if (i >= B_SMX && i < B_SMX + 4) n = 128;
       // a V unit is two loading warps' work, one of FP8 rows eight converting warps'
       if (i >= B_FULL + 8 && i < B_FULL + 16) n = F8 ? 8 : 2;
-      // a slot of a pair is free when both CTAs have read it
-      if (PAIR && i >= B_EMPTY && i < B_EMPTY + 16) n = 2;
       mbar_init(&bars[i], n);
     }
     if (lane == 0) *abort_flag = 0;
@@ -437,8 +400,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
     tmem_relinquish();
   }
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync();   // (the peer's barriers are there)
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_ptr;
   const int head0 = hb * HB;                                   // this CTA's first head
@@ -548,9 +510,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         const bool box = __all_sync(0xffffffffu, (row[0] | row[1] | row[2] | row[3]) >= 0) && a.box_rows > 0;
         // 64 heads: q leaves room for 128 KB of rows in flight, too little for HBM's
         // latency, so the boxes of the tile two back, about a tile ahead of its loads,
-        // are fetched to L2, by each CTA of a pair its half (64 x 19456 at 64 heads
-        // 290 -> 265 us, 16 x 19456 at 128 142 -> 135; a tile earlier 274 and 129, but
-        // 16 x 500..9001 50.3 instead of 49).  Not with fewer heads (64 x 256..16384 at
+        // are fetched to L2, by each of a group's two CTAs its half (64 x 19456 at 64
+        // heads 290 -> 265 us; 16 x 19456 at 128: 133).  Not with fewer heads (64 x 256..16384 at
         // 32: 74 -> 79) nor for gathers (96 x 2048 listed at 64 heads: 109 -> 116).
         if constexpr (HB == 64) {
           if (fetch >= 0)
@@ -559,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
                          : "memory");
           fetch = fetch_next;
           fetch_next = __shfl_sync(0xffffffffu, row[0], (lane * a.box_rows / 4) & 31);   // of box `lane`
-          if (!box || lane >= BK / a.box_rows || (PAIR && (lane & 1) != hb)) fetch_next = -1;
+          if (!box || lane >= BK / a.box_rows || (lane & (a.head_blocks - 1)) != hb) fetch_next = -1;   // (1 or 2 CTAs)
         }
         const bool first = enter;
         const bool last = (it == nt - 1) || (j == n - 1);
@@ -635,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
               const int col = item == 0 ? 528 : 128 * (item - 1);
               __syncwarp();
               if (!box)
-                gather_rows<false>(leader, dst, &a.tmap_kv, col, rows + r * BK, 0, BK / 4, full, policy);
+                gather_rows(leader, dst, &a.tmap_kv, col, rows + r * BK, full, policy);
               else if (lane < boxes)
                 load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
             }
@@ -719,9 +680,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         const int empty = B_EMPTY + (ks ? 0 : 8) + mine_slot;
         const int col_step = ks ? 64 : 128;
         const int boxes = a.box_rows > 0 ? BK / a.box_rows : 1;
-        // of a pair each CTA loads half of the rows, for both
         const uint32_t leader = elect_one();
-        const bool by_box = PAIR ? lane < boxes && (2 * lane >= boxes) == (hb == 1) : lane < boxes;
         const uint64_t policy = ks ? evict_normal_policy() : evict_first_policy();
         int slot = 0;
         uint32_t used = 0;   // phases of the slot so far
@@ -738,20 +697,17 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             const bool mine_now = slot == mine_slot;
             if (++slot == nslots) slot = 0;
             if (!mine_now) continue;
-            if (!wait<false, PAIR>(bar(empty), (used & 1) ^ 1, abort_flag, err)) { ok = false; break; }
+            if (!doze(empty, (used & 1) ^ 1)) { ok = false; break; }
             if (leader) {
               mbar_arrive_expect_tx(full, C::CHUNK_BYTES);
               if (ks && st == 0) DSA_TRACE(a.tr, it, 1);
               if (ks && st == NC - 1) DSA_TRACE(a.tr, it, 2);
             }
             __syncwarp();
-            if (!box) {
-              gather_rows<PAIR>(leader, dst, &a.tmap_kv, col, rows + r * BK, PAIR ? 16 * hb : 0, PAIR ? 16 * hb + 16 : 32, full,
-                                policy);
-            } else if (by_box) {
-              if constexpr (!PAIR) load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
-              else load_2d_pair(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
-            }
+            if (!box)
+              gather_rows(leader, dst, &a.tmap_kv, col, rows + r * BK, full, policy);
+            else if (lane < boxes)
+              load_2d_hint(dst + lane * a.box_rows * 128, &a.tmap_box, col, x, full, policy);
             ++used;
           }
           __syncwarp();
@@ -759,8 +715,6 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         }
         // let the slot's last copies land before the CTA can exit
         if (lane == 0 && used > 0) mbar_wait_drain(full, (used - 1) & 1, err);
-        // and the peer's last arrival here
-        if (PAIR && lane == 0 && used > 0) mbar_wait_drain(&bars[empty], (used - 1) & 1, err);
         __syncwarp();
       }
       }
@@ -849,8 +803,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           if (leader && c == NC - 1) DSA_TRACE(a.tr, it, 4);
           mma_x4_elected(leader, tmem + C::COL_S + sb * HB, k_desc + (uint64_t)(slot * (C::CHUNK_BYTES >> 4)),
                          q_desc + (uint64_t)(c * (HB * 128 >> 4)), 2u, 2u, IDESC, c > 0 ? 1u : 0u);
-          if constexpr (PAIR) commit_elected_pair(leader, &bars[B_EMPTY + slot]);
-          else commit_elected(leader, &bars[B_EMPTY + slot]);
+          commit_elected(leader, &bars[B_EMPTY + slot]);
           if (++slot == C::NK) { slot = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -892,8 +845,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           // 16 keys (2048 bytes of V^T) per MMA; P^T one 64-key swizzle column per half
           mma_x4_elected(leader, d_o, v, p_desc, 128u, 2u, IDESC, acc);
           mma_x4_elected(leader, d_o, v + 512u, p_desc + (uint64_t)(HB * 128 >> 4), 128u, 2u, IDESC, 1u);
-          if constexpr (PAIR) commit_elected_pair(leader, &bars[B_EMPTY + 8 + slot]);
-          else commit_elected(leader, &bars[B_EMPTY + 8 + slot]);
+          commit_elected(leader, &bars[B_EMPTY + 8 + slot]);
           if (++slot == C::NV) { slot = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -1124,8 +1076,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync();   // (the peer's last arrivals and loads have come)
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   if (warp == 4) tmem_dealloc(tmem, C::TMEM_COLS);
 }
@@ -1244,21 +1195,21 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   }
 }
 
-template <int HB, int NC, bool F8, bool PAIR = false>
+template <int HB, int NC, bool F8>
 static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<HB, NC, F8>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
       return -1;
     attr_set[dev] = 1;
   }
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
-  return launch_after(decode_kernel<HB, NC, F8, PAIR>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES,
-                      PAIR ? 2 : 1, stream, a);
+  return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES, stream,
+                      a);
 }
 
 }  // namespace decode
@@ -1268,8 +1219,7 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   const int hb = decode_heads_per_cta(a.H, fp8);
   int r = -2;
   if (hb == 64) {
-    if (decode_pairs(a.H, fp8)) r = d_rope ? launch_t<64, 9, false, true>(a, stream) : launch_t<64, 8, false, true>(a, stream);
-    else r = d_rope ? launch_t<64, 9, false>(a, stream) : launch_t<64, 8, false>(a, stream);
+    r = d_rope ? launch_t<64, 9, false>(a, stream) : launch_t<64, 8, false>(a, stream);
   } else if (hb == 16) {
     if (fp8) r = d_rope ? launch_t<16, 9, true>(a, stream) : launch_t<16, 8, true>(a, stream);
     else r = d_rope ? launch_t<16, 9, false>(a, stream) : launch_t<16, 8, false>(a, stream);
@@ -1281,8 +1231,8 @@ int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cuda
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
   const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
   const int pad = a.head_blocks * hb;
-  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, 1, stream, a, pad)
-                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, 1, stream, a, pad);
+  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, pad)
+                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, pad);
 }
 
 }  // namespace dsa

@@ -170,7 +170,7 @@ static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
   a.head_groups = (a.H + each - 1) / each;
   const int64_t blocks = (per_group * a.head_groups + NT - 1) / NT;
   if (blocks * NT > 0xffffffffll) return -2;
-  return launch_after(rope_kernel<E, HALF, VEC>, dim3((unsigned)blocks), NT, 0, 1, stream, a);
+  return launch_after(rope_kernel<E, HALF, VEC>, dim3((unsigned)blocks), NT, 0, stream, a);
 }
 
 // --------------------------------------------------------------------------
@@ -280,8 +280,8 @@ int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t strea
 int launch_kv_append(const AppendArgs& a, bool fp8, cudaStream_t stream) {
   using namespace rope;
   const unsigned grid = (unsigned)(((int64_t)a.T + NT_APPEND / 32 - 1) / (NT_APPEND / 32));
-  return fp8 ? launch_after(append_kernel<true>, dim3(grid), NT_APPEND, 0, 1, stream, a)
-             : launch_after(append_kernel<false>, dim3(grid), NT_APPEND, 0, 1, stream, a);
+  return fp8 ? launch_after(append_kernel<true>, dim3(grid), NT_APPEND, 0, stream, a)
+             : launch_after(append_kernel<false>, dim3(grid), NT_APPEND, 0, stream, a);
 }
 
 }  // namespace dsa
