@@ -274,3 +274,44 @@ extern "C" int dsa_selftest_mma_pair(const uint16_t* A, const uint16_t* B, float
   selftest_mma_pair_kernel<<<2, 128, smem, stream>>>(map, A, B, D, N, K, a_mn, b_mn, gather, status);
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
+
+// ---------------------------------------------------------------------------
+// Paged decode: the borders of the split, on the host, and the joining kernel over
+// borders that the caller writes.
+// ---------------------------------------------------------------------------
+#include "decode_join.cuh"
+
+// 1 and {request, first range, parts, whole start} in cut, or 0.
+extern "C" int dsa_selftest_border(unsigned total, unsigned ng, int request, int tiles, int so_far, unsigned g, int B,
+                                   int groups, int* cut) {
+  dsa::decode::Border c;
+  if (!dsa::decode::border_of(make_uint2(total, ng), make_int4(request, tiles, so_far, 0), g, B, groups, c)) return 0;
+  cut[0] = c.request;
+  cut[1] = c.first;
+  cut[2] = c.parts;
+  cut[3] = c.whole_start;
+  return 1;
+}
+extern "C" unsigned dsa_selftest_range_begin(unsigned g, unsigned total, unsigned ng) {
+  return dsa::decode::range_begin(g, total, ng);
+}
+
+// H <= 16 heads; borders int4 [1 + groups], part_o [2 groups][16][512], part_lse [2 groups][16].
+extern "C" int dsa_selftest_join(void* borders, float* part_o, float* part_lse, uint16_t* out, float* lse, int B, int H,
+                                 int groups, int ten, cudaStream_t stream) {
+  if (B < 1 || H < 1 || H > 16 || groups < 2 || groups > dsa::kDecodeMaxCtas) return 1;
+  dsa::DecodeArgs a = {};
+  a.borders = static_cast<int4*>(borders);
+  a.part_o = part_o;
+  a.part_lse = part_lse;
+  a.out = out;
+  a.lse = lse;
+  a.B = B;
+  a.H = H;
+  a.groups = groups;
+  a.head_blocks = 1;
+  const dim3 grid((unsigned)(groups - 1), dsa::decode::JOIN_Y);
+  if (ten) dsa::decode::join_kernel<10><<<grid, dsa::decode::NT_JOIN, 0, stream>>>(a, 16);
+  else dsa::decode::join_kernel<5><<<grid, dsa::decode::NT_JOIN, 0, stream>>>(a, 16);
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
