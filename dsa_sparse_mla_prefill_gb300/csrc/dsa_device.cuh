@@ -111,6 +111,41 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same with every turn of the loop decided by the whole warp's vote, so that no
+// lane leaves it while others still vote; a wait that runs out counts once per CTA.
+// Kept small: a launch runs its code cold, and every line of it that is not needed
+// costs several hundred cycles of instruction fetch.
+// POLL: a suspended try_wait wakes about 400 cycles after its phase completes; a poll
+// does not, but takes issue slots.
+inline __device__ __noinline__ void mbar_give_up(volatile int* abort_flag, unsigned int* err) {
+  if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) atomicAdd(err + ERR_TIMEOUT, 1u);
+}
+template <bool POLL>
+__device__ __forceinline__ bool mbar_wait_vote(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  const uint64_t t0 = globaltimer();
+  uint32_t turns = 0;
+#pragma unroll 1
+  while (true) {
+    uint32_t ok;
+    if constexpr (POLL)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+      ok = mbar_try_wait_sleep(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    // (the flag and the clock on every sixteenth turn: a poll is already a shared-memory access)
+    if (POLL && (++turns & 15u)) continue;
+    const bool raised = *abort_flag != 0, late = globaltimer() - t0 > kWaitTimeoutNs;
+    if (__any_sync(0xffffffffu, raised | late)) {
+      mbar_give_up(abort_flag, err);   // (one of the lanes, at most, finds the flag down)
+      return false;
+    }
+  }
+}
+
 // Bounded barrier among the `count` threads that share one mbarrier
 // (initialised with that count): arrive, then wait for the phase.  Unlike
 // bar.sync it cannot hang if a thread of the group has given up.

@@ -161,40 +161,6 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
   return ((uint32_t)(a.idx != nullptr ? a.k : min(len, a.cap)) + BK - 1) / BK;
 }
 
-// Bounded waits, kept small: a launch runs its code cold, and every line of it
-// that is not needed costs several hundred cycles of instruction fetch.
-// POLL: a suspended try_wait wakes about 400 cycles after its phase completes;
-// the waits on a tile's way through the CTA poll instead, the others sleep.
-__device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* err) {
-  if (*abort_flag == 0) atomicAdd(err + ERR_TIMEOUT, 1u);
-  *abort_flag = 1;
-}
-template <bool POLL>
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
-  const uint64_t t0 = globaltimer();
-  uint32_t turns = 0;
-#pragma unroll 1
-  while (true) {
-    uint32_t ok;
-    if constexpr (POLL)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    else
-      ok = mbar_try_wait_sleep(bar, parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    // (the flag and the clock on every sixteenth turn: a poll is already a shared-memory access)
-    if (POLL && (++turns & 15u)) continue;
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > kWaitTimeoutNs) {
-      give_up(abort_flag, err);
-      return false;
-    }
-  }
-}
-
 // TMA loads with an L2 hint.  The rows of a tile are read twice, for K and then
 // for V: the first read caches them as usual, the second marks them first to go.
 // (Marked on the first read, a sixth to a third of them were gone by the second,
@@ -361,8 +327,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
   unsigned int* err = a.err;
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * i; };
-  auto poll = [&](int i, uint32_t parity) { return wait<true>(bar(i), parity, abort_flag, err); };
-  auto doze = [&](int i, uint32_t parity) { return wait<false>(bar(i), parity, abort_flag, err); };
+  auto poll = [&](int i, uint32_t parity) { return mbar_wait_vote<true>(bar(i), parity, abort_flag, err); };
+  auto doze = [&](int i, uint32_t parity) { return mbar_wait_vote<false>(bar(i), parity, abort_flag, err); };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

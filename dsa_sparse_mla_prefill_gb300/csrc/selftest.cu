@@ -315,3 +315,38 @@ extern "C" int dsa_selftest_join(void* borders, float* part_o, float* part_lse, 
   else dsa::decode::join_kernel<5><<<grid, dsa::decode::NT_JOIN, 0, stream>>>(a, 16);
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
+
+// ---------------------------------------------------------------------------
+// The voted wait: three warps, whose lanes arrive one after another, wait on one
+// barrier, which a fourth warp completes after `delay_ns` (kind 0), leaves alone
+// (kind 1), or leaves alone while it raises the abort flag (kind 2).  got[96]: what each
+// lane was told; err: the counters of the library's device errors.
+// ---------------------------------------------------------------------------
+namespace {
+template <bool POLL>
+__global__ void __launch_bounds__(128, 1) selftest_wait_kernel(int kind, unsigned delay_ns, int* got, unsigned int* err) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == 3) {
+    __nanosleep(delay_ns);
+    if (lane == 0 && kind == 0) mbar_arrive(&bar);
+    if (lane == 0 && kind == 2) *(volatile int*)&abort_flag = 1;
+  } else {
+    for (int i = 0; i < lane; ++i) __nanosleep(100);
+    got[threadIdx.x] = mbar_wait_vote<POLL>(smem_u32(&bar), 0, &abort_flag, err) ? 1 : 0;
+  }
+}
+}  // namespace
+extern "C" int dsa_selftest_wait(int poll, int kind, unsigned delay_ns, int* got, unsigned int* err, cudaStream_t stream) {
+  if (delay_ns > 1000000u) return 1;   // (what a nanosleep takes)
+  if (poll) selftest_wait_kernel<true><<<1, 128, 0, stream>>>(kind, delay_ns, got, err);
+  else selftest_wait_kernel<false><<<1, 128, 0, stream>>>(kind, delay_ns, got, err);
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}

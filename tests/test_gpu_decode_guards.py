@@ -98,3 +98,22 @@ def test_join_over_borders_that_no_call_wrote(selftest, fill):
     j.borders[0] = 0x7f7f7f7f
     out, lse = j.run(selftest, 16, 1)
     assert (out == 5).all() and (lse == 5).all()
+
+
+@pytest.mark.parametrize("poll", [0, 1])
+@pytest.mark.parametrize("kind", ["completes", "runs out", "another gave up"])
+def test_voted_wait(selftest, poll, kind):
+    """Every lane of the waiting warps gets the same answer, and a wait that runs out is counted once for its CTA."""
+    import time
+    got = torch.full((96,), -1, dtype=torch.int32, device="cuda")
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    vp = ctypes.c_void_p
+    t0 = time.time()
+    rc = selftest.dsa_selftest_wait(poll, ["completes", "runs out", "another gave up"].index(kind), ctypes.c_uint(200000),
+                                    vp(got.data_ptr()), vp(err.data_ptr()), vp(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    torch.cuda.synchronize()
+    elapsed = time.time() - t0
+    assert got.tolist() == [int(kind == "completes")] * 96
+    assert err.tolist() == [0, int(kind == "runs out"), 0, 0]
+    assert (elapsed > 1.5) == (kind == "runs out") and elapsed < 60      # the wait limit is 2 s
