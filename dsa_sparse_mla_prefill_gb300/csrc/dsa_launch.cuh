@@ -8,7 +8,9 @@ namespace dsa {
 
 // Programmatic stream serialization: the grid may be put on the GPU once every CTA of
 // the kernel before has ended or called launch_dependents().  Such a kernel calls
-// wait_for_previous() before it touches global memory.
+// wait_for_previous() before it touches global memory, and reads it with plain loads:
+// the read-only path (__ldg) wants memory that nobody writes while the kernel is
+// there, and the compiler may move such a load above the wait.
 template <typename... P, typename... A>
 static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};

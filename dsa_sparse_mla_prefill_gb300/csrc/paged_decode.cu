@@ -236,7 +236,7 @@ __device__ __forceinline__ void gather_rows(uint32_t leader, uint32_t dst, const
 
 // The row of a page's at-th position, or -1 (counted).
 __device__ __forceinline__ int32_t row_at(const DecodeArgs& a, const int32_t* bt, uint32_t page, uint32_t at, int& bad) {
-  const int32_t blk = __ldg(bt + page);
+  const int32_t blk = bt[page];
   const int64_t x = (int64_t)blk * a.block_size + at;
   if (blk >= 0 && x < a.N) return (int32_t)x;
   ++bad;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       const int b_lo = min(a.B, lane * per), b_hi = min(a.B, b_lo + per);
       uint32_t mine = 0;
 #pragma unroll 4
-      for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(a, __ldg(a.kv_lens + i));
+      for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(a, a.kv_lens[i]);
       const uint32_t incl = warp_scan(mine), total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
       const uint32_t ng = total < (uint32_t)a.groups ? total : (uint32_t)a.groups;   // no range without a tile
       const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       if (holds) {
         uint32_t at = before;
         for (b = b_lo;; ++b) {
-          len = __ldg(a.kv_lens + b);
+          len = a.kv_lens[b];
           n = tiles_of(a, len);
           if (x0 < at + n) break;
           at += n;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
           // the next request with a tile (one without keys has none; there may be
           // thousands of them in a row, so 32 are looked at at once)
           while (it > 0) {
-            len = b + lane < a.B ? __ldg(a.kv_lens + b + lane) : 0;
+            len = b + lane < a.B ? a.kv_lens[b + lane] : 0;
             const uint32_t there = __ballot_sync(0xffffffffu, tiles_of(a, len) > 0);
             const int skip = there ? __ffs(there) - 1 : 32;
             b += skip;
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         } else {
           int32_t pos[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pos[e] = (e0 + e < a.k) ? __ldg(a.idx + (int64_t)b * a.ld + e0 + e) : -1;
+          for (int e = 0; e < 4; ++e) pos[e] = (e0 + e < a.k) ? a.idx[(int64_t)b * a.ld + e0 + e] : -1;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             row[e] = -1;
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (it < nt && doze(B_IDX_FULL + r, (it / NI) & 1)) {
               const int x = rows[r * BK + row];
-              if (x >= 0) s = __ldg(reinterpret_cast<const float4*>(a.rows_base + (int64_t)x * a.row_bytes + 512));
+              if (x >= 0) s = *reinterpret_cast<const float4*>(a.rows_base + (int64_t)x * a.row_bytes + 512);
               __syncwarp();
               if (lane == 0) mbar_arrive(&bars[B_IDX_EMPTY + r]);
             }
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       __syncwarp();
       // requests without keys: out = 0, lse = -inf (dealt over the groups)
       for (int b = range; b < a.B; b += a.groups) {
-        if (tiles_of(a, __ldg(a.kv_lens + b)) > 0) continue;
+        if (tiles_of(a, a.kv_lens[b]) > 0) continue;
         uint4* o = reinterpret_cast<uint4*>(a.out + ((int64_t)b * a.H + head0) * 512);
         for (int i = lane; i < heads * 64; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         for (int h = lane; h < heads; h += 32) a.lse[(int64_t)b * a.H + head0 + h] = -INFINITY;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
   const uint32_t hg = rest % (uint32_t)a.head_groups, t = rest / (uint32_t)a.head_groups;
   if (t >= (uint32_t)a.T) return;
   wait_for_previous();
-  const int32_t pos = __ldg(a.positions + t);
+  const int32_t pos = a.positions[t];
   float c[PPT], s[PPT];
 #pragma unroll
   for (int i = 0; i < PPT; ++i) {
@@ -193,12 +193,12 @@ constexpr int NT_APPEND = 64;   // (2 tokens: 16384 of them 4 % faster than 4 or
 // The physical row of token t, or -1 (a padding token, or a bad entry: *bad).
 __device__ __forceinline__ int64_t row_of(const AppendArgs& a, int t, int32_t& pos, bool& bad) {
   bad = false;
-  pos = __ldg(a.positions + t);
+  pos = a.positions[t];
   if (pos == -1) return -1;
-  const int r = a.token_req ? __ldg(a.token_req + t) : t;
+  const int r = a.token_req ? a.token_req[t] : t;
   bad = true;
   if (pos < 0 || r < 0 || r >= a.num_req || pos / a.block_size >= a.max_blocks) return -1;
-  const int32_t blk = __ldg(a.block_table + (int64_t)r * a.max_blocks + pos / a.block_size);
+  const int32_t blk = a.block_table[(int64_t)r * a.max_blocks + pos / a.block_size];
   const int64_t row = (int64_t)blk * a.block_size + pos % a.block_size;
   if (blk < 0 || row >= a.N) return -1;
   bad = false;
