@@ -169,6 +169,8 @@ def _host_i32(arr):
 def _stream(stream, device):
     if stream is None:
         torch = _torch or _load_torch()
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got one on {device}")
         return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if device.index is None else device.index))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
