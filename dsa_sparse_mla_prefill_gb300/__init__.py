@@ -609,13 +609,24 @@ def _queue(fn, where, args, dev, stream):
         raise DSAError(st, where)
 
 
-def _made_for(stream, tensors):
-    """Tensors made here on the current stream and used on another one: their memory must not be
-    handed out again before that stream is done."""
-    s = stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream))
-    if s.cuda_stream != _torch.cuda.current_stream(tensors[0].device).cuda_stream:
-        for t in tensors:
-            t.record_stream(s)
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one) to write.  Another stream's is made
+    as that stream's own memory: the current stream's may have been freed there while its queued
+    kernels still use it, and nothing orders the call behind them.  The current stream, which the
+    caller most likely reads the tensor on, is recorded as its user."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # a handle: 0 and 1 are names of the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
 
 
 def _int_tensor(t, name, ndim, dev):
@@ -669,9 +680,7 @@ def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, s
     if d != freqs.d_rope or positions.shape[0] != T:
         raise ValueError(f"x is {tuple(shape)}: it must have {freqs.d_rope} columns, and positions one entry per token")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-        if stream is not None:
-            _made_for(stream, (out,))
+        out = _empty(shape, dtype, x.device, stream)
     elif out.dtype is not dtype or out.shape != shape or out.get_device() != dev:
         raise ValueError("out must have x's shape, dtype and device")
     ys = out.stride()
@@ -787,28 +796,22 @@ def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: flo
     elif k is not None:
         raise ValueError("k without idx")
     device = q.device
-    made = []
     if out is None:
-        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=device)
-        made.append(out)
+        out = _empty((B, H, 512), torch.bfloat16, device, stream)
     elif out.dtype is not torch.bfloat16 or out.shape != (B, H, 512) or out.get_device() != dev or \
             not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 [B, H, 512] tensor on q's device")
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=device)
-        made.append(lse)
+        lse = _empty((B, H), torch.float32, device, stream)
     elif lse.dtype is not torch.float32 or lse.shape != (B, H) or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [B, H] tensor on q's device")
     if workspace is None:
         nbytes = dsa_paged_decode_workspace(B, H, max_blocks * block_size if idx is None else k)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        made.append(workspace)
+        workspace = _empty(nbytes, torch.uint8, device, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     else:
         nbytes = workspace.numel()
-    if stream is not None and made:
-        _made_for(stream, made)
     _queue(lib().dsa_paged_decode, "dsa_paged_decode",
            (q.data_ptr(), cache.data_ptr(), fmt, N, ld_kv, block_table.data_ptr(), max_blocks, block_size,
             kv_lens.data_ptr(), idx_ptr, k or 0, ld, B, H, d_qk, 512, float(scale), out.data_ptr(), lse.data_ptr(),

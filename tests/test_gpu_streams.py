@@ -1,0 +1,69 @@
+"""Calls on a stream that is not the current one: the tensors that the binding makes for them."""
+import numpy as np
+import pytest
+
+from gpu_util import bf, i32, need_gpu, torch
+from synth import normal_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def decode_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    rng = np.random.default_rng(1)
+    cache, q = bf(normal_bf16(rng, (4096, 576))), bf(normal_bf16(rng, (3, 32, 576)))
+    table, lens = i32(rng.permutation(64).reshape(1, 64).repeat(3, 0)), i32([4000, 77, 1500])
+    return lambda **kw: dsa.dsa_paged_decode(q, cache, table, lens, 64, 192 ** -0.5, **kw)
+
+
+def rope_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    x, pos = bf(normal_bf16(np.random.default_rng(2), (700, 16, 64))), i32(np.arange(700))
+    freqs = dsa.dsa_rope_freqs(64)
+    return lambda **kw: (dsa.dsa_rope(x, pos, freqs, **kw),)
+
+
+CALLS = {"decode": decode_call, "rope": rope_call}
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+@pytest.mark.parametrize("name", list(CALLS))
+def test_results_are_not_memory_that_the_current_stream_still_uses(name, as_handle):
+    """Blocks of the results' sizes, freed on the current stream behind a kernel that will yet write them: a call on
+    another stream, which waits for nothing, gets none of them, and neither does any harm to the other."""
+    call = CALLS[name]()
+    want = call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    spare = [torch.empty_like(t) for t in want for _ in range(2)] + \
+        [torch.empty(dsa.dsa_paged_decode_workspace(3, 32, 4096), dtype=torch.uint8, device="cuda")]
+    torch.cuda.synchronize()
+    blocks = {t.data_ptr() for t in spare}
+    torch.cuda._sleep(20_000_000)
+    for t in spare:
+        t.fill_(1)
+    del spare, t
+    got = call(stream=s.cuda_stream if as_handle else s)
+    assert not blocks & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_the_default_stream_by_its_handle(name):
+    """Handle 0 from inside another stream: the default stream, not the current one."""
+    call = CALLS[name]()
+    want = call()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(stream=0)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
