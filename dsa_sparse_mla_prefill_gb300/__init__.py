@@ -175,6 +175,26 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one) to write.  Another stream's is made
+    as that stream's own memory: the current stream's may have been freed there while its queued
+    kernels still use it, and nothing orders the call behind them.  The current stream, which the
+    caller most likely reads the tensor on, is recorded as its user."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # a handle: 0 and 1 are names of the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _need(t, dtype, name, ndim=None):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -213,9 +233,9 @@ def dsa_union_build(idx, k: int, G: int, N: int, cu_seqlens_q=None, union_pad: i
         union_pad = dsa_union_pad(G, k, union_block)
     ng = dsa_num_groups(cu_seqlens_q, T, G)
     if out is None:
-        u = torch.empty((ng, union_pad), dtype=torch.int32, device=idx.device)
-        ul = torch.empty((ng,), dtype=torch.int32, device=idx.device)
-        m = torch.empty((ng, union_pad), dtype=torch.uint8, device=idx.device)
+        u = _empty((ng, union_pad), torch.int32, idx.device, stream)
+        ul = _empty((ng,), torch.int32, idx.device, stream)
+        m = _empty((ng, union_pad), torch.uint8, idx.device, stream)
     else:
         u, ul, m = out
     arr, ptr = _host_i32(cu_seqlens_q)
@@ -238,9 +258,9 @@ def dsa_sparse_prefill(q, kv, idx, k: int, scale: float, d_v: int = 512, out=Non
     if idx.shape[0] != T:
         raise ValueError("idx rows must match q tokens")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, d_v), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     _check(lib().dsa_sparse_prefill(q.data_ptr(), kv.data_ptr(), N, ld_kv, idx.data_ptr(), T, H, d_qk, d_v, k,
                                     idx.shape[1], float(scale), out.data_ptr(), lse.data_ptr(),
                                     _stream(stream, q.device)), "dsa_sparse_prefill")
@@ -348,9 +368,9 @@ def dsa_grouped_prefill(q, kv, union_idx, union_len, mask, G: int, scale: float,
     T, H, d_qk = q.shape
     N, ld_kv = kv.shape
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, d_v), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     arr, ptr = _host_i32(cu_seqlens_q)
     nreq = 0 if arr is None else len(arr) - 1
     _check(lib().dsa_grouped_prefill(q.data_ptr(), kv.data_ptr(), N, ld_kv, union_idx.data_ptr(),
@@ -366,7 +386,7 @@ def dsa_topk_to_key_mask(idx, k: int, words: int, cu_seqlens_q=None, cu_seqlens_
     _need(idx, torch.int32, "idx", 2)
     T, ld = idx.shape
     if out is None:
-        out = torch.empty((T, words), dtype=torch.int32, device=idx.device)
+        out = _empty((T, words), torch.int32, idx.device, stream)
     aq, pq = _host_i32(cu_seqlens_q)
     ak, pk = _host_i32(cu_seqlens_kv)
     nreq = 0 if aq is None else len(aq) - 1
@@ -386,7 +406,7 @@ def dsa_local_to_global(idx_local, k: int, kv_lens, block_table, block_size: int
     _need(block_table, torch.int32, "block_table", 2)
     T, ld = idx_local.shape
     if out is None:
-        out = torch.empty_like(idx_local)
+        out = _empty(idx_local.shape, torch.int32, idx_local.device, stream)
     aq, pq = _host_i32(cu_seqlens_q)
     al, pl = _host_i32(kv_lens)
     nreq = 0 if aq is None else len(aq) - 1
@@ -410,9 +430,9 @@ def dsa_masked_mha_prefill(q, k, v, key_mask, scale: float, cu_seqlens_q=None, c
     T, H, d_qk = q.shape
     d_v = v.shape[2]
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, d_v), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     aq, pq = _host_i32(cu_seqlens_q)
     ak, pk = _host_i32(cu_seqlens_kv)
     nreq = 0 if aq is None else len(aq) - 1
@@ -446,9 +466,9 @@ def dsa_masked_mha_prefill_strided(q, k, v, key_mask, scale: float, k_pe=None, c
     if k.shape[2] + d_rope != d_qk:
         raise ValueError("k columns + k_pe columns must equal q's head dim")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, d_v), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     aq, pq = _host_i32(cu_seqlens_q)
     ak, pk = _host_i32(cu_seqlens_kv)
     nreq = 0 if aq is None else len(aq) - 1
@@ -473,7 +493,7 @@ def dsa_kv_fp8_quantize(kv, d_rope: int = 64, out=None, stream=None):
     _need(kv, torch.bfloat16, "kv", 2)
     N, ld = kv.shape
     if out is None:
-        out = torch.empty((N, dsa_kv_fp8_row_bytes(d_rope)), dtype=torch.uint8, device=kv.device)
+        out = _empty((N, dsa_kv_fp8_row_bytes(d_rope)), torch.uint8, kv.device, stream)
     _need(out, torch.uint8, "out", 2)
     _check(lib().dsa_kv_fp8_quantize(kv.data_ptr(), N, ld, int(d_rope), out.data_ptr(), _stream(stream, kv.device)),
            "dsa_kv_fp8_quantize")
@@ -488,7 +508,7 @@ def dsa_kv_fp8_dequantize(fp8, d_rope: int = 64, out=None, stream=None):
     if fp8.shape[1] != dsa_kv_fp8_row_bytes(d_rope):
         raise ValueError("fp8 rows must be dsa_kv_fp8_row_bytes(d_rope) bytes wide")
     if out is None:
-        out = torch.empty((N, 512 + d_rope), dtype=torch.bfloat16, device=fp8.device)
+        out = _empty((N, 512 + d_rope), torch.bfloat16, fp8.device, stream)
     _need(out, torch.bfloat16, "out", 2)
     _check(lib().dsa_kv_fp8_dequantize(fp8.data_ptr(), N, int(d_rope), out.data_ptr(), out.shape[1],
                                        _stream(stream, fp8.device)), "dsa_kv_fp8_dequantize")
@@ -568,9 +588,9 @@ def dsa_sparse_prefill_fp8(q, kv_fp8, idx, k: int, scale: float, d_rope: int = 6
     if idx.shape[0] != T:
         raise ValueError("idx rows must match q tokens")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, d_v), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     _check(lib().dsa_sparse_prefill_fp8(q.data_ptr(), kv_fp8.data_ptr(), N, int(d_rope), idx.data_ptr(), T, H, d_qk,
                                         d_v, k, idx.shape[1], float(scale), out.data_ptr(), lse.data_ptr(),
                                         _stream(stream, q.device)), "dsa_sparse_prefill_fp8")
@@ -607,26 +627,6 @@ def _queue(fn, where, args, dev, stream):
             st = fn(*args, _raw_stream(dev) if stream is None else stream)
     if st:
         raise DSAError(st, where)
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on `stream` (None: the current one) to write.  Another stream's is made
-    as that stream's own memory: the current stream's may have been freed there while its queued
-    kernels still use it, and nothing orders the call behind them.  The current stream, which the
-    caller most likely reads the tensor on, is recorded as its user."""
-    torch = _torch or _load_torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == here.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):   # a handle: 0 and 1 are names of the default stream
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(here)
-    return t
 
 
 def _int_tensor(t, name, ndim, dev):

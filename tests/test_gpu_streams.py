@@ -28,7 +28,86 @@ def rope_call():
     return lambda **kw: (dsa.dsa_rope(x, pos, freqs, **kw),)
 
 
-CALLS = {"decode": decode_call, "rope": rope_call}
+def prefill_inputs():
+    rng = np.random.default_rng(3)
+    q, kv = bf(normal_bf16(rng, (300, 16, 576))), bf(normal_bf16(rng, (2000, 576)))
+    return q, kv, i32(np.sort(rng.integers(0, 300, (300, 128)), axis=1) % (1 + np.arange(300))[:, None])
+
+
+def sparse_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    q, kv, idx = prefill_inputs()
+    return lambda **kw: dsa.dsa_sparse_prefill(q, kv, idx, 128, 0.07, **kw)
+
+
+def sparse_fp8_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    q, kv, idx = prefill_inputs()
+    rows = dsa.dsa_kv_fp8_quantize(kv, 64)
+    return lambda **kw: dsa.dsa_sparse_prefill_fp8(q, rows, idx, 128, 0.07, **kw)
+
+
+def union_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    idx = prefill_inputs()[2]
+
+    return lambda **kw: dsa.dsa_union_build(idx, 128, 8, 2000, **kw)
+
+
+def grouped_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    q, kv, idx = prefill_inputs()
+    u, n, m = dsa.dsa_union_build(idx, 128, 8, 2000)
+    return lambda **kw: dsa.dsa_grouped_prefill(q, kv, u, n, m, 8, 0.07, **kw)
+
+
+def key_mask_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    idx = prefill_inputs()[2]
+    return lambda **kw: (dsa.dsa_topk_to_key_mask(idx, 128, 64, **kw),)
+
+
+def convert_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    idx, table = prefill_inputs()[2], i32(np.arange(40)[None, ::-1].copy())
+    return lambda **kw: (dsa.dsa_local_to_global(idx, 128, [2000], table, 50, 2000, **kw),)
+
+
+def masked_inputs():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    rng = np.random.default_rng(4)
+    q, k, v = (bf(normal_bf16(rng, (300, 4, 256))) for _ in range(3))
+    return q, k, v, dsa.dsa_topk_to_key_mask(prefill_inputs()[2], 128, 12)
+
+
+def masked_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    a = masked_inputs()
+    return lambda **kw: dsa.dsa_masked_mha_prefill(*a, 0.06, **kw)
+
+
+def masked_strided_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    a = masked_inputs()
+    return lambda **kw: dsa.dsa_masked_mha_prefill_strided(*a, 0.06, **kw)
+
+
+def quantize_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    kv = prefill_inputs()[1]
+    return lambda **kw: (dsa.dsa_kv_fp8_quantize(kv, 64, **kw),)
+
+
+def dequantize_call():
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    rows = dsa.dsa_kv_fp8_quantize(prefill_inputs()[1], 64)
+    return lambda **kw: (dsa.dsa_kv_fp8_dequantize(rows, 64, **kw),)
+
+
+CALLS = {"decode": decode_call, "rope": rope_call, "sparse": sparse_call, "sparse_fp8": sparse_fp8_call,
+         "union": union_call, "grouped": grouped_call, "key_mask": key_mask_call, "convert": convert_call,
+         "masked": masked_call, "masked_strided": masked_strided_call, "quantize": quantize_call,
+         "dequantize": dequantize_call}
 
 
 @pytest.mark.parametrize("as_handle", [False, True])
