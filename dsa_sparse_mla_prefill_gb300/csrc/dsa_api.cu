@@ -718,6 +718,7 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   // whole-context calls load runs of rows: the largest power of two in the page size, at most a tile
   const int run = block_size & -block_size;
   a.box_rows = idx || none || run < 8 ? 0 : (run < 128 ? run : 128);
+  a.fetch_bytes = a.box_rows && !fp8 ? dsa::decode_fetch_bytes(a.box_rows, 2ll * ld_kv, 2 * d_qk) : 0;
   if (a.box_rows &&
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))

@@ -96,6 +96,15 @@ struct AppendArgs {
   dsa_rope_freqs table;
 };
 
+// Bytes that the 64-head decode form fetches to L2 of a run of `rows` cache rows: from the
+// first row to the end of what is read of the last, in one piece, what lies between the
+// rows included, so only where that is little (64 x 19456 at 64 heads, rows of 1152
+// bytes: a pitch of 1280 278 us, 288 unfetched; of 1408 295 and 289; of 2304 429 and
+// 289; row by row 312 at any of them).  0: nothing is fetched.
+inline int decode_fetch_bytes(int rows, int64_t row_bytes, int read_bytes) {
+  return 8 * (row_bytes - read_bytes) <= read_bytes ? (rows - 1) * (int)row_bytes + read_bytes : 0;
+}
+
 struct DecodeArgs {
   CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box
   CUtensorMap tmap_box;       // cache rows, 64-column x box_rows box (unset when box_rows = 0)
@@ -103,6 +112,7 @@ struct DecodeArgs {
   const uint8_t* rows_base;   // the cache rows as bytes, and their pitch
   int row_bytes;
   int box_rows;               // rows that a page holds in one run: 8 .. 128, a power of two; 0 = gather rows
+  int fetch_bytes;            // fetched to L2 of each run by the 64-head form (decode_fetch_bytes)
   const int32_t* block_table; // [B, max_blocks]
   const int32_t* kv_lens;     // [B]
   const int32_t* idx;         // [B, ld] positions, or null: every position < kv_len

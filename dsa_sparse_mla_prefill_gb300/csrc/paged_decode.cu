@@ -474,11 +474,12 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
         if constexpr (HB == 64) {
           if (fetch >= 0)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.rows_base + (int64_t)fetch * a.row_bytes),
-                         "r"(a.row_bytes * a.box_rows)
+                         "r"(a.fetch_bytes)
                          : "memory");
           fetch = fetch_next;
           fetch_next = __shfl_sync(0xffffffffu, row[0], (lane * a.box_rows / 4) & 31);   // of box `lane`
-          if (!box || lane >= BK / a.box_rows || (lane & (a.head_blocks - 1)) != hb) fetch_next = -1;   // (1 or 2 CTAs)
+          if (!box || a.fetch_bytes == 0 || lane >= BK / a.box_rows || (lane & (a.head_blocks - 1)) != hb)   // (1 or 2 CTAs)
+            fetch_next = -1;
         }
         const bool first = enter;
         const bool last = (it == nt - 1) || (j == n - 1);

@@ -350,3 +350,8 @@ extern "C" int dsa_selftest_wait(int poll, int kind, unsigned delay_ns, int* got
   else selftest_wait_kernel<false><<<1, 128, 0, stream>>>(kind, delay_ns, got, err);
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
+
+// Bytes that the paged decode kernel fetches to L2 of a run of rows.
+extern "C" int dsa_selftest_fetch(int rows, long long row_bytes, int read_bytes) {
+  return dsa::decode_fetch_bytes(rows, row_bytes, read_bytes);
+}

@@ -476,7 +476,9 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
  *
  * q            bf16 [B, H, d_qk], 16-byte aligned; 1 <= H <= 128.
  * cache        as for dsa_kv_append; d_qk = 576 or 512 (d_rope 64 or 0),
- *              d_v = 512.  May be NULL when N = 0.
+ *              d_v = 512.  Only the first d_qk columns of a bf16 row are read,
+ *              so the rows may be columns of a wider buffer.  May be NULL when
+ *              N = 0.
  * block_table  DEVICE int32 [B, max_blocks].
  * kv_lens      DEVICE int32 [B].  Zero or less: no keys.  A length past
  *              max_blocks * block_size is cut to it and counted once.

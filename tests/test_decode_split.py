@@ -70,3 +70,18 @@ def test_entries_that_no_call_wrote(lib):
         assert 0 <= request < B and 0 <= first <= g and parts >= 2 and first + parts - 1 > g and first + parts <= ng <= groups
     assert taken > 100
     assert border(lib, 5000, 152, 0, 0, 0, 3, 9, 152) is None                   # what a range leaves whose waits ran out
+
+
+@pytest.mark.parametrize("rows", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("d_qk", [512, 576])
+@pytest.mark.parametrize("extra", [0, 8, 64, 72, 128, 576, 4096, 2 ** 28, 2 ** 31 - 1024])
+def test_bytes_fetched_of_a_run(lib, rows, d_qk, extra):
+    """Up to the end of what is read of the run's last row and no further, so that the columns behind it need not be
+    memory; and not at all where more than an eighth would be fetched for nothing."""
+    pitch, read = 2 * (d_qk + extra), 2 * d_qk
+    size = lib.dsa_selftest_fetch(rows, ctypes.c_longlong(pitch), read)
+    if 2 * extra * 8 <= read:
+        assert size == (rows - 1) * pitch + read and size % 16 == 0
+        assert size <= rows * read * 9 / 8
+    else:
+        assert size == 0

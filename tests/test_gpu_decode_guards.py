@@ -117,3 +117,28 @@ def test_voted_wait(selftest, poll, kind):
     assert got.tolist() == [int(kind == "completes")] * 96
     assert err.tolist() == [0, int(kind == "runs out"), 0, 0]
     assert (elapsed > 1.5) == (kind == "runs out") and elapsed < 60      # the wait limit is 2 s
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("page", [8, 64, 128])
+def test_rows_that_are_columns_of_a_wider_buffer(selftest, H, page):
+    """The last columns of a buffer, which ends with the last row's: the same bits as from rows of their own."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    torch.manual_seed(5)
+    N, B, pages = 40 * 128, 3, 10 * 128 // page
+    wide = torch.full((N, 1152), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 576:].normal_()
+    table = torch.randperm(N // page, device="cuda")[:B * pages].to(torch.int32).reshape(B, pages).contiguous()
+    table[0, -1] = N // page - 1
+    lens = torch.tensor([pages * page, 700, 129], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, H, 576, dtype=torch.bfloat16, device="cuda")
+    want = dsa.dsa_paged_decode(q, wide[:, 576:].contiguous(), table, lens, page, 0.07)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = torch.empty(dsa.dsa_paged_decode_workspace(B, H, pages * page), dtype=torch.uint8, device="cuda")
+    rc = dsa.lib().dsa_paged_decode(q.data_ptr(), wide[:, 576:].data_ptr(), 0, N, 1152, table.data_ptr(), pages, page,
+                                    lens.data_ptr(), None, 0, 0, B, H, 576, 512, 0.07, out.data_ptr(), lse.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert dsa.dsa_last_device_error()[0] == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
