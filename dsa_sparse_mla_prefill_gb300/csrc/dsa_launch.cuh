@@ -28,6 +28,22 @@ static int launch_after(void (*kernel)(P...), dim3 grid, int threads, uint32_t s
   return -1;
 }
 
+// Lets a kernel have `smem` bytes of dynamic shared memory on the current device.  done:
+// the kernel's own, zeros at first, so that the devices it was asked for once are not
+// asked again.
+static inline int allow_smem(const void* kernel, uint32_t smem, int (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev < 64 && done[dev]) return 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
+      if (dev < 64) done[dev] = 1;
+      return 0;
+    }
+  }
+  cudaGetLastError();   // (reported here, not by the next launch)
+  return -1;
+}
+
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

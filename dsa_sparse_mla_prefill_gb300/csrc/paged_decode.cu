@@ -1043,15 +1043,8 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
 template <int HB, int NC, bool F8>
 static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<HB, NC, F8>;
-  static int attr_set[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(decode_kernel<HB, NC, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
-        cudaSuccess)
-      return -1;
-    attr_set[dev] = 1;
-  }
+  static int done[64] = {0};
+  if (allow_smem(reinterpret_cast<const void*>(decode_kernel<HB, NC, F8>), C::SMEM_BYTES, done) != 0) return -1;
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
   return launch_after(decode_kernel<HB, NC, F8>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES, stream,
                       a);

@@ -355,3 +355,10 @@ extern "C" int dsa_selftest_wait(int poll, int kind, unsigned delay_ns, int* got
 extern "C" int dsa_selftest_fetch(int rows, long long row_bytes, int read_bytes) {
   return dsa::decode_fetch_bytes(rows, row_bytes, read_bytes);
 }
+
+// What allow_smem says of `smem` bytes for one kernel, and 10 more if it leaves an error pending.
+extern "C" int dsa_selftest_allow_smem(unsigned smem) {
+  static int done[64] = {0};
+  const int r = dsa::allow_smem(reinterpret_cast<const void*>(selftest_wait_kernel<true>), smem, done);
+  return (r == 0 ? 0 : 1) + (cudaPeekAtLastError() == cudaSuccess ? 0 : 10);
+}

@@ -142,3 +142,12 @@ def test_rows_that_are_columns_of_a_wider_buffer(selftest, H, page):
     torch.cuda.synchronize()
     assert dsa.dsa_last_device_error()[0] == 0
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_refused_launch_attribute_is_not_left_for_the_next_launch(selftest):
+    """More shared memory than a CTA can have is refused, once: no error stays pending, and less is granted after."""
+    assert selftest.dsa_selftest_allow_smem(ctypes.c_uint(1 << 20)) == 1
+    assert selftest.dsa_selftest_allow_smem(ctypes.c_uint(100 << 10)) == 0
+    assert selftest.dsa_selftest_allow_smem(ctypes.c_uint(100 << 10)) == 0
+    torch.zeros(4, device="cuda").add_(1)
+    torch.cuda.synchronize()
