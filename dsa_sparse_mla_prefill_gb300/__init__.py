@@ -76,7 +76,7 @@ class FormEstimate(ctypes.Structure):
 
 
 class RopeFreqs(ctypes.Structure):
-    """Rotary frequencies (dsa_rope_freqs); read-only once made."""
+    """Rotary frequencies (dsa_rope_freqs)."""
     _fields_ = [("d_rope", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
                 ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
 
@@ -637,6 +637,14 @@ def _int_tensor(t, name, ndim, dev):
 
 
 @functools.lru_cache(maxsize=64)
+def _rope_table(d_rope, base, layout, scaling, factor, original_len, beta_fast, beta_slow, mscale) -> bytes:
+    f = RopeFreqs()
+    _check(lib().dsa_rope_freqs_init(ctypes.byref(f), int(d_rope), float(base), ROPE_LAYOUTS.index(layout),
+                                     ROPE_SCALINGS.index(scaling), float(factor), int(original_len), float(beta_fast),
+                                     float(beta_slow), float(mscale)), "dsa_rope_freqs_init")
+    return bytes(f)
+
+
 def dsa_rope_freqs(d_rope: int, base: float = 10000.0, layout: str = "interleaved", scaling: str = "none",
                    factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
                    mscale: float = 1.0) -> RopeFreqs:
@@ -644,16 +652,14 @@ def dsa_rope_freqs(d_rope: int, base: float = 10000.0, layout: str = "interleave
     "interleaved" (2i, 2i+1) or "half" (i, i + d_rope/2), frequencies base^(-2i/d_rope),
     ``scaling`` "none", "linear" (divided by factor) or "yarn" (fast pairs kept, slow ones
     divided, mixed between beta_fast and beta_slow turns over original_len positions); mscale
-    multiplies cos and sin.  The table depends on these numbers alone (and is kept by them)."""
+    multiplies cos and sin.  The table depends on these numbers alone (and is kept by them); every
+    call returns a copy of its own."""
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {ROPE_LAYOUTS}")
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
-    f = RopeFreqs()
-    _check(lib().dsa_rope_freqs_init(ctypes.byref(f), int(d_rope), float(base), ROPE_LAYOUTS.index(layout),
-                                     ROPE_SCALINGS.index(scaling), float(factor), int(original_len), float(beta_fast),
-                                     float(beta_slow), float(mscale)), "dsa_rope_freqs_init")
-    return f
+    return RopeFreqs.from_buffer_copy(_rope_table(d_rope, base, layout, scaling, factor, original_len, beta_fast,
+                                                  beta_slow, mscale))
 
 
 def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, stream=None):
