@@ -683,6 +683,8 @@ def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, s
     shape = x.shape
     T, H, d = shape
     xs = x.stride()
+    if T > 0x7fffffff or H > 0x7fffffff:   # (the library counts them in 32 bits)
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_rope")
     if d != freqs.d_rope or positions.shape[0] != T:
         raise ValueError(f"x is {tuple(shape)}: it must have {freqs.d_rope} columns, and positions one entry per token")
     if out is None:

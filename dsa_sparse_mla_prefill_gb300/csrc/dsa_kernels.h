@@ -82,6 +82,17 @@ struct RopeArgs {
   dsa_rope_freqs table;
 };
 
+// Threads that share a token's heads, per_group threads being one such share of all
+// tokens: as many heads per thread, in powers of two, as leave threads for half of
+// every SM's 2048 slots (16384 tokens of 32 heads, interleaved bf16: 8 heads each 25.7
+// us, 32 each 26.5, 11 each 27.3, 4 each 27.0, 2 each 36.6; 8191 of 16 heads, fp32
+// halves: 4 each 13.6 us, 2 each 15.3, the cos and sin being worked out per thread).
+inline int rope_head_groups(int64_t H, int64_t per_group, int num_sms) {
+  int64_t each = 1;
+  while (2 * each <= H && (H + 2 * each - 1) / (2 * each) * per_group >= 1024ll * num_sms) each *= 2;
+  return (int)((H + each - 1) / each);
+}
+
 struct AppendArgs {
   const uint16_t* c_kv;       // [T, 512] bf16, row stride c_stride
   const uint16_t* k_pe;       // [T, d_rope] bf16, row stride pe_stride

@@ -100,14 +100,15 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
   E* y = static_cast<E*>(a.y) + (int64_t)t * a.y_stride_t;
   const int lo = HALF ? item * PPT : 2 * item * PPT;   // first element of the thread's pairs
   const int up = HALF ? lo + a.d / 2 : lo + 1;         // the pairs' second elements (scalar and half)
-  const int step = a.head_groups;
-  for (int h0 = hg; h0 < a.H; h0 += UNROLL * step) {
+  // (unsigned: the last round of heads may look past 2^31)
+  const uint32_t step = (uint32_t)a.head_groups, H = (uint32_t)a.H;
+  for (uint32_t h0 = hg; h0 < H; h0 += UNROLL * step) {
     if constexpr (VEC) {
       uint4 w[UNROLL], u[UNROLL];
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) {
-        const int h = h0 + k * step;
-        if (h < a.H) {
+        const uint32_t h = h0 + k * step;
+        if (h < H) {
           const E* src = x + (int64_t)h * a.x_stride_h;
           w[k] = *reinterpret_cast<const uint4*>(src + lo);
           if constexpr (HALF) u[k] = *reinterpret_cast<const uint4*>(src + up);
@@ -115,8 +116,8 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
       }
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) {
-        const int h = h0 + k * step;
-        if (h < a.H) {
+        const uint32_t h = h0 + k * step;
+        if (h < H) {
           E* dst = y + (int64_t)h * a.y_stride_h;
           float p[P::V], q[P::V];
           P::unpack(w[k], p);
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
     } else {
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) {
-        const int h = h0 + k * step;
-        if (h < a.H) {
+        const uint32_t h = h0 + k * step;
+        if (h < H) {
           const E* src = x + (int64_t)h * a.x_stride_h;
           E* dst = y + (int64_t)h * a.y_stride_h;
           const float p = P::load(src + lo), q = P::load(src + up);
@@ -160,14 +161,7 @@ template <typename E, bool HALF, bool VEC>
 static int launch_t(RopeArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int PPT = pairs_per_thread<E, HALF, VEC>();
   const int64_t per_group = (int64_t)a.T * (a.d / (2 * PPT));   // threads of one head group
-  // as many heads per thread, in powers of two, as leave threads for half of
-  // every SM's 2048 slots (16384 tokens of 32 heads, interleaved bf16: 8 heads
-  // each 25.7 us, 32 each 26.5, 11 each 27.3, 4 each 27.0, 2 each 36.6; 8191 of
-  // 16 heads, fp32 halves: 4 each 13.6 us, 2 each 15.3, the cos and sin being
-  // worked out per thread)
-  int each = 1;
-  while (2 * each <= a.H && (a.H + 2 * each - 1) / (2 * each) * per_group >= 1024ll * num_sms) each *= 2;
-  a.head_groups = (a.H + each - 1) / each;
+  a.head_groups = rope_head_groups(a.H, per_group, num_sms);
   const int64_t blocks = (per_group * a.head_groups + NT - 1) / NT;
   if (blocks * NT > 0xffffffffll) return -2;
   return launch_after(rope_kernel<E, HALF, VEC>, dim3((unsigned)blocks), NT, 0, stream, a);

@@ -362,3 +362,7 @@ extern "C" int dsa_selftest_allow_smem(unsigned smem) {
   const int r = dsa::allow_smem(reinterpret_cast<const void*>(selftest_wait_kernel<true>), smem, done);
   return (r == 0 ? 0 : 1) + (cudaPeekAtLastError() == cudaSuccess ? 0 : 10);
 }
+
+extern "C" int dsa_selftest_rope_head_groups(int H, long long per_group, int num_sms) {
+  return dsa::rope_head_groups(H, per_group, num_sms);
+}
