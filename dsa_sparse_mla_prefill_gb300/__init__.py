@@ -667,7 +667,8 @@ def dsa_rope(x, positions, freqs: RopeFreqs, out=None, gradient: bool = False, s
     RoPE columns of a wider head are passed as that view), positions [T] int32.  ``out``: a tensor
     or view of the same shape and dtype, x itself for in place; a new contiguous one if None.
     gradient=True turns back: the gradient of the forward with respect to x, given the gradient
-    of its result.  Returns out."""
+    of its result.  Returns out.  (As with every call of the library, autograd does not see this one:
+    out is detached from an x that requires a gradient.)"""
     torch = _torch or _load_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a bf16 or fp32 tensor")

@@ -434,6 +434,8 @@ int dsa_rope_freqs_init(dsa_rope_freqs* freqs, int d_rope, double base, int layo
  * dtype      DSA_DTYPE_BF16 (the result rounded once) or DSA_DTYPE_F32.
  * positions  DEVICE int32 [T], any value (negative ones turn backwards).
  * freqs      HOST, copied into the launch.
+ * The arithmetic is float32 and takes subnormal values (below 2^-126) for
+ * zero, in x and in the results.
  * Pointers aligned to their element; any strides (16-byte aligned rows, heads
  * and pointers with d a multiple of 16 bytes' worth of elements run fastest).
  * DSA_ERR_UNSUPPORTED: more than 2^32 - 256 pairs of all tokens' heads. */
