@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
   E* y = static_cast<E*>(a.y) + (int64_t)t * a.y_stride_t;
   const int lo = HALF ? item * PPT : 2 * item * PPT;   // first element of the thread's pairs
   const int up = HALF ? lo + a.d / 2 : lo + 1;         // the pairs' second elements (scalar and half)
-  // (unsigned: the last round of heads may look past 2^31)
+  // (unsigned: a thread's last step looks past the heads, and may pass 2^31)
   const uint32_t step = (uint32_t)a.head_groups, H = (uint32_t)a.H;
   for (uint32_t h0 = hg; h0 < H; h0 += UNROLL * step) {
     if constexpr (VEC) {

@@ -146,3 +146,27 @@ def test_the_default_stream_by_its_handle(name):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["decode", "rope", "sparse"])
+def test_calls_on_a_side_stream_of_a_capture(name):
+    """A captured step that forks to another stream and joins again, replayed with other kernels in between."""
+    call = CALLS[name]()
+    want = call()
+    torch.cuda.synchronize()
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        s.wait_stream(here)
+        first = call(stream=s)
+        second = call(stream=s)
+        here.wait_stream(s)
+        third = call()
+    for _ in range(3):
+        for t in first + second + third:
+            t.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        for got in (first, second, third):
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)

@@ -19,7 +19,7 @@ def lib():
 @pytest.mark.parametrize("per_group", [1, 8, 128, 16384 * 16])
 def test_head_groups(lib, H, per_group):
     """Heads per thread are a power of two, the largest that leaves half of the SMs' threads; every head the kernel's
-    loop looks at (four rounds of a group's step behind the last one at most) is counted in 32 unsigned bits."""
+    loop looks at (four steps behind the last one at most) is counted in 32 unsigned bits."""
     groups = lib.dsa_selftest_rope_head_groups(H, ctypes.c_longlong(per_group), 152)
     each = 1
     while 2 * each <= H and -(-H // (2 * each)) * per_group >= 1024 * 152:
