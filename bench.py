@@ -910,7 +910,8 @@ def run_profile_case(args):
             fn = lambda: dsa.dsa_masked_mha_prefill(q, k, v, km, w.scale, cu_seqlens_q=x.cu_seqlens_q,
                                                     cu_seqlens_kv=x.cu_seqlens_kv)
     elif args.profile.startswith("decode"):
-        # one new token of 64 requests of 256 to 16384 positions (decode_pair: 16 of 500 to 9001, 128 heads as two CTAs of 64), pages of 64
+        # one new token of 64 requests of 256 to 16384 positions, pages of 64 (decode_pair: 16 of 500 to 9001, 128 heads as
+        # two CTAs of 64)
         H, fp8, (B, lo, hi) = {"decode": (32, False, (64, 256, 16384)), "decode_fp8": (16, True, (48, 1024, 16384)),
                                "decode_pair": (128, False, (16, 500, 9001))}[args.profile]
         rng = np.random.default_rng(0)
