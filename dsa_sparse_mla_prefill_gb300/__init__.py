@@ -23,6 +23,12 @@ The decode step over the same paged cache:
   dsa_rope                rotary positions and their gradient (frequencies from dsa_rope_freqs)
   dsa_kv_append           new tokens' latent rows into the cache, bf16 or FP8, RoPE columns rotated
   dsa_paged_decode        attention of one new token per request, whole context or its top-k positions
+
+Norms in front of the rotation, and the step that checks drafted tokens over that cache:
+  dsa_qk_norm_rope        RMS norms of queries' and keys' heads (or latent rows) with the rotation
+  dsa_qk_norm_rope_gradient  the gradients of their inputs and weights
+  dsa_tree_decode         attention of a tree of drafted tokens per request
+  dsa_kv_keep             the accepted path's rows take their places, in every layer's cache
 """
 from __future__ import annotations
 
@@ -116,6 +122,15 @@ _SIGNATURES = {
     "dsa_paged_decode_workspace": (_L, [_I, _I, _L]),
     "dsa_paged_decode": (_I, [_VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP,
                               _L, _VP]),
+    "dsa_qk_norm_rope": (_I, [_VP, _L, _L, _VP, _L, _L, _I, _VP, _L, _L, _VP, _L, _L, _I, _I, _VP, _VP, _I, _VP, _I, _I, _I,
+                              _F, ctypes.POINTER(RopeFreqs), _VP]),
+    "dsa_qk_norm_rope_gradient_workspace": (_L, [_I]),
+    "dsa_qk_norm_rope_gradient": (_I, [_VP, _L, _L, _VP, _L, _L, _VP, _I, _VP, _L, _L, _VP, _L, _L, _VP, _I, _I, _VP, _VP, _I,
+                                       _VP, _I, _I, _I, _F, ctypes.POINTER(RopeFreqs), _VP, _VP, _VP, _L, _VP]),
+    "dsa_tree_decode_workspace": (_L, [_I, _I, _I, _L]),
+    "dsa_tree_decode": (_I, [_VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP, _L,
+                             _VP]),
+    "dsa_kv_keep": (_I, [ctypes.POINTER(_VP), _I, _L, _I, _VP, _I, _I, _VP, _VP, _I, _VP, _I, _I, _VP, _VP]),
     "dsa_form_calibration_default": (_I, [ctypes.POINTER(FormCalibration)]),
     "dsa_choose_form": (_I, [ctypes.POINTER(FormQuery), ctypes.POINTER(FormCalibration),
                              ctypes.POINTER(FormEstimate)]),
@@ -826,3 +841,265 @@ def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: flo
             kv_lens.data_ptr(), idx_ptr, k or 0, ld, B, H, d_qk, 512, float(scale), out.data_ptr(), lse.data_ptr(),
             workspace.data_ptr(), nbytes), dev, stream)
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# norms in front of the rotation
+# ---------------------------------------------------------------------------
+def _norm_side(x, weight, name, d_norm, like):
+    """Checks of queries or keys and their weight; `like` = (dtype, device, T, d, weight dtype) of the other side."""
+    torch = _torch
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise TypeError(f"{name} must be a bf16 or fp32 tensor")
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1 and x.numel():
+        raise ValueError(f"{name} must be a 3-D CUDA tensor with unit stride in its last dimension")
+    T, H, d = x.shape
+    if T > 0x7fffffff or H > 0x7fffffff:   # (the library counts them in 32 bits)
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_qk_norm_rope")
+    if not isinstance(weight, torch.Tensor) or weight.dtype is not torch.bfloat16 and weight.dtype is not torch.float32:
+        raise TypeError(f"{name}'s weight must be a bf16 or fp32 tensor")
+    if d_norm is None:
+        d_norm = d
+    if not 1 <= d_norm <= d:
+        raise ValueError("d_norm must be between 1 and the columns of a head")
+    if weight.dim() != 1 or weight.shape[0] != d_norm or weight.get_device() != dev or not weight.is_contiguous():
+        raise ValueError(f"{name}'s weight must be a contiguous [d_norm] tensor on its device")
+    mine = (x.dtype, dev, T, d, weight.dtype)
+    if like is not None and mine != like:
+        raise ValueError("q and k must have the same tokens, columns, dtype and device, and weights of one dtype")
+    return mine, d_norm
+
+
+def _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm):
+    """Checks shared by the norm and its gradient; (device, dtype flag, weight dtype flag, T, d, d_norm, positions pointer)."""
+    torch = _torch or _load_torch()
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    if freqs is not None and not isinstance(freqs, RopeFreqs):
+        raise TypeError("freqs must come from dsa_rope_freqs")
+    like, n = None, d_norm
+    if q is not None:
+        like, n = _norm_side(q, q_weight, "q", d_norm, None)
+    if k is not None:
+        like, n = _norm_side(k, k_weight, "k", d_norm, like)
+    dtype, dev, T, d, w_dtype = like
+    if freqs is not None:
+        if freqs.d_rope > d:
+            raise ValueError("freqs have more columns than a head")
+        _int_tensor(positions, "positions", 1, dev)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+    f32 = torch.float32
+    return dev, int(dtype is f32), int(w_dtype is f32), T, d, n, None if freqs is None else positions.data_ptr()
+
+
+def _rows_like(t, x, name, dev):
+    """t, a tensor of x's shape and dtype with unit last stride."""
+    if not isinstance(t, _torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != dev:
+        raise ValueError(f"{name} must have the shape, dtype and device of what it belongs to")
+    if t.stride(2) != 1 and t.shape[2] != 1 and t.numel():
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return t
+
+
+def dsa_qk_norm_rope(q, k, q_weight, k_weight, positions, freqs: RopeFreqs = None, eps: float = 1e-6,
+                     d_norm: int | None = None, q_out=None, k_out=None, stream=None):
+    """RMS norms of the heads of queries q [T, Hq, d] and keys k [T, Hk, d] (bf16 or fp32, any strides
+    with unit last stride; one of them may be None) over their first ``d_norm`` columns (all of them if
+    None), times q_weight and k_weight [d_norm] (bf16 or fp32), with the last ``freqs.d_rope`` columns
+    turned by positions [T] int32 in the same pass (freqs None: nothing is turned, positions are not
+    read).  k = latent rows [T, 1, 576] with d_norm = 512 gives the cache's rows for dsa_kv_append.
+    q_out, k_out: tensors or views of the same shapes (q and k themselves for in place); new contiguous
+    ones if None.  Returns (q_out, k_out), None for a side that is not there.  Autograd does not see the
+    call: see dsa_qk_norm_rope_gradient."""
+    dev, f32, w_f32, T, d, n, pos = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
+    args = []
+    outs = []
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name} without its input")
+            args += [None, 0, 0, None, 0, 0, 0]
+        else:
+            out = _empty(x.shape, x.dtype, x.device, stream) if out is None else _rows_like(out, x, name, dev)
+            xs, ys = x.stride(), out.stride()
+            args += [x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], x.shape[1]]
+        outs.append(out)
+    _queue(lib().dsa_qk_norm_rope, "dsa_qk_norm_rope",
+           (*args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32, pos, T,
+            d, n, float(eps), freqs), dev, stream)
+    return tuple(outs)
+
+
+@functools.lru_cache(maxsize=64)
+def dsa_qk_norm_rope_gradient_workspace(d_norm: int) -> int:
+    """Device workspace bytes dsa_qk_norm_rope_gradient needs."""
+    n = int(lib().dsa_qk_norm_rope_gradient_workspace(d_norm))
+    if n < 0:
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_qk_norm_rope_gradient_workspace")
+    return n
+
+
+def dsa_qk_norm_rope_gradient(q_grad, k_grad, q, k, q_weight, k_weight, positions, freqs: RopeFreqs = None,
+                              eps: float = 1e-6, d_norm: int | None = None, workspace=None, stream=None):
+    """Gradients of dsa_qk_norm_rope: q, k and the weights, positions, freqs, eps and d_norm as in the
+    forward call, q_grad and k_grad [T, H, d] the gradients of its results (any strides with unit last
+    stride, expanded ones too).  Returns (gq, gk, gq_weight, gk_weight): gq and gk contiguous in q's
+    dtype, the weights' in fp32; None for a side that is not there.  workspace: a CUDA uint8 tensor of
+    dsa_qk_norm_rope_gradient_workspace(d_norm) bytes (calls sharing one must not overlap on the GPU);
+    one per call if None."""
+    dev, f32, w_f32, T, d, n, pos = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
+    torch = _torch
+    device = (k if q is None else q).device
+    args, outs, weights = [], [], []
+    for x, g, name in ((q, q_grad, "q_grad"), (k, k_grad, "k_grad")):
+        if x is None:
+            if g is not None:
+                raise ValueError(f"{name} without its input")
+            args += [None, 0, 0, None, 0, 0, None, 0]
+            outs.append(None)
+            weights.append(None)
+            continue
+        _rows_like(g, x, name, dev)
+        out = _empty(x.shape, x.dtype, device, stream)
+        gs, xs = g.stride(), x.stride()
+        args += [g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), x.shape[1]]
+        outs.append(out)
+        # (no rows: the library leaves the sums alone)
+        weights.append(_empty((n,), torch.float32, device, stream) if x.shape[1] else
+                       torch.zeros(n, dtype=torch.float32, device=device))
+    if workspace is None:
+        workspace = _empty((dsa_qk_norm_rope_gradient_workspace(n),), torch.uint8, device, stream)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _queue(lib().dsa_qk_norm_rope_gradient, "dsa_qk_norm_rope_gradient",
+           (*args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32, pos, T,
+            d, n, float(eps), freqs, *(None if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
+            workspace.numel()), dev, stream)
+    return (*outs, *weights)
+
+
+# ---------------------------------------------------------------------------
+# checking drafted tokens
+# ---------------------------------------------------------------------------
+TREE_MAX_TOKENS, TREE_MAX_ROWS, MAX_CACHES = 64, 2048, 128
+
+
+@functools.lru_cache(maxsize=1024)
+def dsa_tree_decode_workspace(B: int, n: int, H: int, max_positions: int) -> int:
+    """Device workspace bytes dsa_tree_decode needs for B requests of n drafted tokens and H heads;
+    max_positions: the block table's columns * block_size."""
+    b = int(lib().dsa_tree_decode_workspace(B, n, H, max_positions))
+    if b < 0:
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_tree_decode_workspace")
+    return b
+
+
+def dsa_tree_decode(q, cache, block_table, kv_lens, tree_mask, block_size: int, scale: float, num_draft=None,
+                    d_v: int = 512, out=None, lse=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens per request over a paged latent cache.  q [B, n, H, d_qk]
+    bf16 (d_qk = 576 or 512, n <= 64, H <= 128, n * H <= 2048); cache, block_table [B, max_blocks] and
+    kv_lens [B] as for dsa_paged_decode, kv_lens counting the drafted tokens, whose rows are the
+    request's last positions.  tree_mask [B, n] int64: bit j of entry i says whether drafted token i
+    sees drafted token j (itself included); every token sees the context.  num_draft [B] int32: drafted
+    tokens of each request (None: n); the tokens behind them are padding and get out = 0, lse = -inf.
+    workspace: a CUDA uint8 tensor of dsa_tree_decode_workspace(...) bytes (calls sharing one must not
+    overlap on the GPU); one per call if None.  Returns (out [B, n, H, 512] bf16, lse [B, n, H] fp32)."""
+    torch = _torch or _load_torch()
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.bfloat16:
+        raise TypeError("q must be a bf16 tensor")
+    dev = q.get_device()
+    if dev < 0 or q.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous 4-D CUDA tensor")
+    B, n, H, d_qk = q.shape
+    if d_qk != 576 and d_qk != 512 or d_v != 512:
+        raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_tree_decode")
+    _int_tensor(block_table, "block_table", 2, dev)
+    _int_tensor(kv_lens, "kv_lens", 1, dev)
+    if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype is not torch.int64:
+        raise TypeError("tree_mask must be an int64 tensor")
+    if tree_mask.shape != (B, n) or tree_mask.get_device() != dev or not tree_mask.is_contiguous():
+        raise ValueError("tree_mask must be a contiguous [B, n] tensor on q's device")
+    rows, max_blocks = block_table.shape
+    if rows != B or kv_lens.shape[0] != B:
+        raise ValueError("block_table and kv_lens must have one row per request")
+    draft_ptr = None
+    if num_draft is not None:
+        _int_tensor(num_draft, "num_draft", 1, dev)
+        if num_draft.shape[0] != B:
+            raise ValueError("num_draft must have one entry per request")
+        draft_ptr = num_draft.data_ptr()
+    fmt, N, ld_kv = _cache_of(cache, d_qk - 512, dev)
+    block_size = int(block_size)
+    device = q.device
+    if out is None:
+        out = _empty((B, n, H, 512), torch.bfloat16, device, stream)
+    elif out.dtype is not torch.bfloat16 or out.shape != (B, n, H, 512) or out.get_device() != dev or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 [B, n, H, 512] tensor on q's device")
+    if lse is None:
+        lse = _empty((B, n, H), torch.float32, device, stream)
+    elif lse.dtype is not torch.float32 or lse.shape != (B, n, H) or lse.get_device() != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, n, H] tensor on q's device")
+    if workspace is None:
+        nbytes = dsa_tree_decode_workspace(B, n, H, max(0, max_blocks * block_size))
+        workspace = _empty((nbytes,), torch.uint8, device, stream)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    else:
+        nbytes = workspace.numel()
+    _queue(lib().dsa_tree_decode, "dsa_tree_decode",
+           (q.data_ptr(), cache.data_ptr(), fmt, N, ld_kv, block_table.data_ptr(), max_blocks, block_size,
+            kv_lens.data_ptr(), tree_mask.data_ptr(), draft_ptr, B, n, H, d_qk, 512, float(scale), out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), nbytes), dev, stream)
+    return out, lse
+
+
+def dsa_kv_keep(caches, block_table, kv_lens, keep, block_size: int, n: int, num_draft=None, new_lens=None, stream=None):
+    """The accepted path's rows take their places: in every cache, the row of request b's drafted token
+    keep[b, i] moves to position context + i, where context = kv_lens[b] - drafted tokens (num_draft [B]
+    int32, or n for all).  caches: a cache tensor [N, columns] (bf16 or FP8 rows as uint8) or a sequence
+    of up to 128 of one shape and dtype, the layers'.  keep [B, m] int32: drafted tokens in ascending
+    order, -1 behind the last.  Returns the lengths behind the kept tokens, [B] int32 (``new_lens`` if
+    given, another tensor than kv_lens)."""
+    torch = _torch or _load_torch()
+    if isinstance(caches, torch.Tensor):
+        caches = (caches,)
+    if not len(caches):
+        raise ValueError("caches must hold a cache")
+    first = caches[0]
+    if not isinstance(first, torch.Tensor) or first.dtype is not torch.bfloat16 and first.dtype is not torch.uint8:
+        raise TypeError("caches must be bf16 rows or FP8 rows as uint8")
+    dev, shape, dtype = first.get_device(), first.shape, first.dtype
+    if dev < 0 or len(shape) != 2:
+        raise ValueError("caches must be 2-D CUDA tensors")
+    pointers = (_VP * len(caches))()
+    for i, c in enumerate(caches):
+        if not isinstance(c, torch.Tensor) or c.dtype is not dtype or c.shape != shape or c.get_device() != dev or \
+                not c.is_contiguous():
+            raise ValueError("caches must be contiguous tensors of one shape and dtype on one device")
+        pointers[i] = c.data_ptr()
+    _int_tensor(block_table, "block_table", 2, dev)
+    _int_tensor(kv_lens, "kv_lens", 1, dev)
+    _int_tensor(keep, "keep", 2, dev)
+    B = kv_lens.shape[0]
+    if block_table.shape[0] != B or keep.shape[0] != B:
+        raise ValueError("block_table, kv_lens and keep must have one row per request")
+    draft_ptr = None
+    if num_draft is not None:
+        _int_tensor(num_draft, "num_draft", 1, dev)
+        if num_draft.shape[0] != B:
+            raise ValueError("num_draft must have one entry per request")
+        draft_ptr = num_draft.data_ptr()
+    if new_lens is None:
+        new_lens = _empty((B,), torch.int32, kv_lens.device, stream)
+    else:
+        _int_tensor(new_lens, "new_lens", 1, dev)
+        if new_lens.shape[0] != B:
+            raise ValueError("new_lens must have one entry per request")
+    _queue(lib().dsa_kv_keep, "dsa_kv_keep",
+           (pointers, len(caches), shape[1] * first.element_size(), shape[0], block_table.data_ptr(), block_table.shape[1],
+            int(block_size), kv_lens.data_ptr(), draft_ptr, int(n), keep.data_ptr(), keep.shape[1], B,
+            new_lens.data_ptr()), dev, stream)
+    return new_lens

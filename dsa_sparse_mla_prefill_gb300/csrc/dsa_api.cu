@@ -48,6 +48,16 @@ bool dev_info(DevInfo** out) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether heads and tokens of a [T, H, d] result overlap: the closer-packed of the two
+// dimensions holds a row, the other all of its rows.
+bool rows_overlap(int64_t stride_t, int64_t stride_h, int T, int H, int d) {
+  const bool heads_inside = H == 1 || (T > 1 && stride_h <= stride_t) || T == 1;
+  const int64_t in_s = heads_inside ? stride_h : stride_t, in_n = heads_inside ? H : T;
+  const int64_t out_s = heads_inside ? stride_t : stride_h, out_n = heads_inside ? T : H;
+  if (in_n > 1 && in_s < d) return true;
+  return out_n > 1 && out_s < (in_n > 1 ? in_s * (in_n - 1) : 0) + d;
+}
+
 // Fills a request table from host offsets (NULL = one request of T tokens).
 // With G > 0, cu_g holds group offsets (G tokens of one request per group).
 int fill_req(dsa::ReqTable& rq, const int32_t* cu_q, const int32_t* cu_kv, int num_req, int T, int Nkv,
@@ -539,15 +549,7 @@ int dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* y, int
   const int es = dtype == DSA_DTYPE_F32 ? 4 : 2;
   const uintptr_t px = reinterpret_cast<uintptr_t>(x), py = reinterpret_cast<uintptr_t>(y);
   if (px % es || py % es) return DSA_ERR_INVALID_ARG;
-  // the result's heads and tokens must not overlap: the closer-packed of the
-  // two dimensions holds a row, the other all of its rows
-  {
-    const bool heads_inside = H == 1 || (T > 1 && y_stride_h <= y_stride_t) || T == 1;
-    const int64_t in_s = heads_inside ? y_stride_h : y_stride_t, in_n = heads_inside ? H : T;
-    const int64_t out_s = heads_inside ? y_stride_t : y_stride_h, out_n = heads_inside ? T : H;
-    if (in_n > 1 && in_s < d) return DSA_ERR_INVALID_ARG;
-    if (out_n > 1 && out_s < (in_n > 1 ? in_s * (in_n - 1) : 0) + d) return DSA_ERR_INVALID_ARG;
-  }
+  if (rows_overlap(y_stride_t, y_stride_h, T, H, d)) return DSA_ERR_INVALID_ARG;
   if (px == py && ((T > 1 && x_stride_t != y_stride_t) || (H > 1 && x_stride_h != y_stride_h)))
     return DSA_ERR_INVALID_ARG;
   DevInfo* dv;
@@ -574,6 +576,114 @@ int dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* y, int
                    (H == 1 || (x_stride_h % piece == 0 && y_stride_h % piece == 0));
   const int r = dsa::launch_rope(a, dtype == DSA_DTYPE_F32, vec, dv->num_sms, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
+}
+
+// Checks of one side of a norm call, and whether its rows allow 16-byte pieces.
+static int norm_side(dsa::NormSide& s, int T, int d, int es, bool gradient, bool* vec) {
+  const uintptr_t px = reinterpret_cast<uintptr_t>(s.x), py = reinterpret_cast<uintptr_t>(s.y);
+  const uintptr_t pg = reinterpret_cast<uintptr_t>(s.g);
+  if (!s.x || !s.y || (gradient && !s.g)) return DSA_ERR_INVALID_ARG;
+  if (s.x_stride_t < 0 || s.x_stride_h < 0 || s.g_stride_t < 0 || s.g_stride_h < 0) return DSA_ERR_INVALID_ARG;
+  if (px % es || py % es || pg % es) return DSA_ERR_INVALID_ARG;
+  if (rows_overlap(s.y_stride_t, s.y_stride_h, T, s.H, d)) return DSA_ERR_INVALID_ARG;
+  if (px == py && (gradient || (T > 1 && s.x_stride_t != s.y_stride_t) || (s.H > 1 && s.x_stride_h != s.y_stride_h)))
+    return DSA_ERR_INVALID_ARG;
+  if (gradient && pg == py) return DSA_ERR_INVALID_ARG;
+  const int64_t piece = 16 / es;
+  if (px % 16 || py % 16 || pg % 16) *vec = false;
+  if (T > 1 && (s.x_stride_t % piece || s.y_stride_t % piece || s.g_stride_t % piece)) *vec = false;
+  if (s.H > 1 && (s.x_stride_h % piece || s.y_stride_h % piece || s.g_stride_h % piece)) *vec = false;
+  return DSA_OK;
+}
+
+// The common part of the norm calls: a.side is filled (H = 0 where there is none).
+static int norm_call(dsa::NormArgs& a, int dtype, int weight_dtype, const dsa_rope_freqs* freqs, bool gradient,
+                     dsa_stream_t stream) {
+  const int T = a.T, d = a.d;
+  if (T < 0 || a.side[0].H < 0 || a.side[1].H < 0 || d < 1 || a.d_norm < 1 || a.d_norm > d) return DSA_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return DSA_ERR_INVALID_ARG;
+  if ((dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F32) ||
+      (weight_dtype != DSA_DTYPE_BF16 && weight_dtype != DSA_DTYPE_F32) || d > DSA_NORM_MAX_D)
+    return DSA_ERR_UNSUPPORTED;
+  if (freqs) {
+    if (freqs->d_rope < 2 || (freqs->d_rope & 1) || freqs->d_rope > 2 * DSA_ROPE_MAX_PAIRS || freqs->d_rope > d)
+      return DSA_ERR_INVALID_ARG;
+    if (freqs->layout != DSA_ROPE_INTERLEAVED && freqs->layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+    a.table = *freqs;
+    a.d_rope = freqs->d_rope;
+  }
+  if ((int64_t)T * ((int64_t)a.side[0].H + a.side[1].H) > 0xffffff00ll) return DSA_ERR_UNSUPPORTED;
+  if (a.side[0].H == 0 && a.side[1].H == 0) return DSA_OK;
+  if (!gradient && T == 0) return DSA_OK;
+  const int es = dtype == DSA_DTYPE_F32 ? 4 : 2, ws = weight_dtype == DSA_DTYPE_F32 ? 4 : 2;
+  const int64_t piece = 16 / es;
+  bool vec = d % piece == 0 && a.d_norm % piece == 0 && (d - a.d_rope) % piece == 0 && a.d_rope % (2 * piece) == 0;
+  for (dsa::NormSide& s : a.side) {
+    if (s.H == 0) continue;
+    if (!s.w || reinterpret_cast<uintptr_t>(s.w) % ws) return DSA_ERR_INVALID_ARG;
+    if (gradient && (!s.dw || !aligned4(s.dw))) return DSA_ERR_INVALID_ARG;
+    if (T == 0) continue;
+    const int r = norm_side(s, T, d, es, gradient, &vec);
+    if (r != DSA_OK) return r;
+  }
+  if (T > 0 && freqs && (!a.positions || !aligned4(a.positions))) return DSA_ERR_INVALID_ARG;
+  a.w_f32 = weight_dtype == DSA_DTYPE_F32;
+  DevInfo* dv;
+  if (!dev_info(&dv)) return DSA_ERR_CUDA;
+  const int r = dsa::launch_norm_rope(a, dtype == DSA_DTYPE_F32, vec, gradient, dv->num_sms, (cudaStream_t)stream);
+  return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
+}
+
+int dsa_qk_norm_rope(const void* q, int64_t q_stride_t, int64_t q_stride_h, void* q_out, int64_t q_out_stride_t,
+                     int64_t q_out_stride_h, int Hq, const void* k, int64_t k_stride_t, int64_t k_stride_h, void* k_out,
+                     int64_t k_out_stride_t, int64_t k_out_stride_h, int Hk, int dtype, const void* q_weight,
+                     const void* k_weight, int weight_dtype, const int32_t* positions, int T, int d, int d_norm,
+                     float eps, const dsa_rope_freqs* freqs, dsa_stream_t stream) {
+  dsa::NormArgs a;
+  memset(&a, 0, sizeof(a));
+  if (Hq)
+    a.side[0] = {q, nullptr, q_out, q_weight, nullptr, q_stride_t, q_stride_h, 0, 0, q_out_stride_t, q_out_stride_h, Hq, 0, 0};
+  if (Hk)
+    a.side[1] = {k, nullptr, k_out, k_weight, nullptr, k_stride_t, k_stride_h, 0, 0, k_out_stride_t, k_out_stride_h, Hk, 0, 0};
+  if (Hq > 0 && Hk > 0 && T > 0 && q_out && q_out == k_out) return DSA_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.T = T;
+  a.d = d;
+  a.d_norm = d_norm;
+  a.eps = eps;
+  return norm_call(a, dtype, weight_dtype, freqs, false, stream);
+}
+
+int64_t dsa_qk_norm_rope_gradient_workspace(int d_norm) {
+  return d_norm < 1 || d_norm > DSA_NORM_MAX_D ? -1 : (int64_t)dsa::kNormMaxCtas * d_norm * 4;
+}
+
+int dsa_qk_norm_rope_gradient(const void* q_grad, int64_t q_grad_stride_t, int64_t q_grad_stride_h, const void* q,
+                              int64_t q_stride_t, int64_t q_stride_h, void* gq, int Hq, const void* k_grad,
+                              int64_t k_grad_stride_t, int64_t k_grad_stride_h, const void* k, int64_t k_stride_t,
+                              int64_t k_stride_h, void* gk, int Hk, int dtype, const void* q_weight,
+                              const void* k_weight, int weight_dtype, const int32_t* positions, int T, int d, int d_norm,
+                              float eps, const dsa_rope_freqs* freqs, float* gq_weight, float* gk_weight,
+                              void* workspace, int64_t workspace_bytes, dsa_stream_t stream) {
+  dsa::NormArgs a;
+  memset(&a, 0, sizeof(a));
+  if (Hq)
+    a.side[0] = {q, q_grad, gq, q_weight, gq_weight, q_stride_t, q_stride_h, q_grad_stride_t, q_grad_stride_h,
+                 (int64_t)Hq * d, d, Hq, 0, 0};
+  if (Hk)
+    a.side[1] = {k, k_grad, gk, k_weight, gk_weight, k_stride_t, k_stride_h, k_grad_stride_t, k_grad_stride_h,
+                 (int64_t)Hk * d, d, Hk, 0, 0};
+  if (Hq > 0 && Hk > 0 && ((T > 0 && gq && gq == gk) || (gq_weight && gq_weight == gk_weight))) return DSA_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.T = T;
+  a.d = d;
+  a.d_norm = d_norm;
+  a.eps = eps;
+  if (d_norm >= 1 && d_norm <= DSA_NORM_MAX_D && (Hq > 0 || Hk > 0) &&
+      (!workspace || !aligned16(workspace) || workspace_bytes < dsa_qk_norm_rope_gradient_workspace(d_norm)))
+    return DSA_ERR_INVALID_ARG;
+  a.part = static_cast<float*>(workspace);
+  return norm_call(a, dtype, weight_dtype, freqs, true, stream);
 }
 
 int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, int64_t pe_stride, int T, int d_rope,
@@ -641,8 +751,7 @@ static int64_t decode_part_bytes(int H, bool fp8, int groups, int64_t* lse_at, i
   return *out_at + 2 * groups * hp * 512 * 4;
 }
 
-int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
-  if (B < 0 || H < 1 || H > 128 || max_positions < 0) return -1;
+static int64_t decode_workspace(int B, int H, int64_t max_positions) {
   int64_t l, o, most = 0;   // of either cache format
   for (int fp8 = 0; fp8 < 2; ++fp8) {
     const int64_t n = decode_part_bytes(H, fp8, decode_groups(B, H, fp8, decode_tiles(max_positions)), &l, &o);
@@ -650,15 +759,25 @@ int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
   }
   return most;
 }
+int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
+  return B < 0 || H < 1 || H > 128 || max_positions < 0 ? -1 : decode_workspace(B, H, max_positions);
+}
+int64_t dsa_tree_decode_workspace(int B, int n, int H, int64_t max_positions) {
+  if (B < 0 || n < 1 || n > DSA_TREE_MAX_TOKENS || H < 1 || H > 128 || n * H > DSA_TREE_MAX_ROWS || max_positions < 0) return -1;
+  return decode_workspace(B, n * H, max_positions);
+}
 
-int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
-                     const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
-                     const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
-                     float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream) {
+// The decode step's attention: one token per request (tree NULL, n = 1), or n drafted ones.
+// H: query rows of a request.
+static int decode_call(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                       const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                       const int32_t* idx, int k, int ld, const uint64_t* tree, const int32_t* num_draft, int n, int B,
+                       int H, int d_qk, int d_v, float scale, uint16_t* out, float* lse, void* workspace,
+                       int64_t workspace_bytes, dsa_stream_t stream) {
   if (B < 0 || N < 0 || max_blocks < 1 || block_size < 1) return DSA_ERR_INVALID_ARG;
   // (the kernel works in base 2: scale * log2(e) must be finite too)
   if (!(std::fabs(scale) <= 2e38f)) return DSA_ERR_INVALID_ARG;
-  if (H < 1 || H > 128 || !(d_qk == 576 || d_qk == 512) || d_v != 512) return DSA_ERR_UNSUPPORTED;
+  if (H < 1 || (!tree && H > 128) || !(d_qk == 576 || d_qk == 512) || d_v != 512) return DSA_ERR_UNSUPPORTED;
   if (cache_format != DSA_CACHE_BF16 && cache_format != DSA_CACHE_FP8) return DSA_ERR_UNSUPPORTED;
   if (cache_format == DSA_CACHE_BF16 && (ld_kv < d_qk || (ld_kv & 7) != 0)) return DSA_ERR_INVALID_ARG;
   if (idx && (k < 0 || ld < k)) return DSA_ERR_INVALID_ARG;
@@ -687,6 +806,10 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
   a.block_table = block_table;
   a.kv_lens = kv_lens;
   a.idx = idx;
+  a.tree_mask = tree;
+  a.num_draft = num_draft;
+  a.n = n;
+  a.heads = H / n;
   a.out = out;
   a.lse = lse;
   a.borders = static_cast<int4*>(workspace);
@@ -724,8 +847,72 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H, fp8))) return DSA_ERR_CUDA;
-  const int r = dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
+  const int r = tree ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
+                     : dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
+}
+
+int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                     const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                     const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
+                     float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream) {
+  return decode_call(q, cache, cache_format, N, ld_kv, block_table, max_blocks, block_size, kv_lens, idx, k, ld, nullptr,
+                     nullptr, 1, B, H, d_qk, d_v, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int dsa_tree_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                    const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                    const uint64_t* tree_mask, const int32_t* num_draft, int B, int n, int H, int d_qk, int d_v,
+                    float scale, uint16_t* out, float* lse, void* workspace, int64_t workspace_bytes,
+                    dsa_stream_t stream) {
+  if (n < 0 || H < 0) return DSA_ERR_INVALID_ARG;
+  if (n < 1 || n > DSA_TREE_MAX_TOKENS || H < 1 || H > 128 || n * H > DSA_TREE_MAX_ROWS) return DSA_ERR_UNSUPPORTED;
+  if (!tree_mask) {   // (an empty call may come without one)
+    if (B != 0) return DSA_ERR_INVALID_ARG;
+    static const uint64_t none = 0;
+    tree_mask = &none;
+  }
+  if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) || !aligned4(num_draft)) return DSA_ERR_INVALID_ARG;
+  return decode_call(q, cache, cache_format, N, ld_kv, block_table, max_blocks, block_size, kv_lens, nullptr, 0, 0,
+                     tree_mask, num_draft, n, B, n * H, d_qk, d_v, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int dsa_kv_keep(void* const* caches, int num_caches, int64_t row_bytes, int N, const int32_t* block_table,
+                int max_blocks, int block_size, const int32_t* kv_lens, const int32_t* num_draft, int n,
+                const int32_t* keep, int m, int B, int32_t* new_lens, dsa_stream_t stream) {
+  if (num_caches < 1 || row_bytes < 16 || (row_bytes & 15) != 0 || N < 0 || max_blocks < 1 || block_size < 1 || n < 0 ||
+      m < 0 || B < 0 || !caches)
+    return DSA_ERR_INVALID_ARG;
+  if (num_caches > DSA_MAX_CACHES || n > DSA_TREE_MAX_TOKENS || m > DSA_TREE_MAX_TOKENS || row_bytes > (1 << 24))
+    return DSA_ERR_UNSUPPORTED;
+  if (B == 0) return DSA_OK;
+  if (!block_table || !kv_lens || (!keep && m > 0) || !new_lens || new_lens == kv_lens) return DSA_ERR_INVALID_ARG;
+  if (!aligned4(block_table) || !aligned4(kv_lens) || !aligned4(num_draft) || !aligned4(keep) || !aligned4(new_lens))
+    return DSA_ERR_INVALID_ARG;
+  dsa::KeepArgs a;
+  memset(&a, 0, sizeof(a));
+  for (int i = 0; i < num_caches; ++i) {
+    if ((!caches[i] && N > 0) || !aligned16(caches[i])) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (N > 0 && caches[j] == caches[i]) return DSA_ERR_INVALID_ARG;
+    a.caches[i] = caches[i];
+  }
+  DevInfo* d;
+  if (!dev_info(&d)) return DSA_ERR_CUDA;
+  a.block_table = block_table;
+  a.kv_lens = kv_lens;
+  a.num_draft = num_draft;
+  a.keep = keep;
+  a.new_lens = new_lens;
+  a.err = d->err;
+  a.B = B;
+  a.m = m;
+  a.n = n;
+  a.N = N;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.row_pieces = (int)(row_bytes / 16);
+  return dsa::launch_kv_keep(a, num_caches, (cudaStream_t)stream) == 0 ? DSA_OK : DSA_ERR_CUDA;
 }
 
 int dsa_debug_wait_timeout(dsa_stream_t stream) {

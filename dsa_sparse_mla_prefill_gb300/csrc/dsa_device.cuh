@@ -862,6 +862,15 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rn(float x) {
 }
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(((uint32_t)b) << 16); }
 
+// cos and sin, times m, of position pos by a frequency in turns per position as a fraction of
+// 2^64: the product modulo a turn, as a signed number the angle in (-1/2, 1/2] turn.
+__device__ __forceinline__ void rope_cos_sin(uint64_t turns, int32_t pos, float m, float& c, float& s) {
+  const int64_t t = (int64_t)(turns * (uint64_t)(int64_t)pos);
+  sincospif(__ll2float_rn(t) * 1.0842021724855044e-19f /* 2^-63: half turns */, &s, &c);
+  c *= m;
+  s *= m;
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

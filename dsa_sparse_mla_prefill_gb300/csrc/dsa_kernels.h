@@ -93,6 +93,29 @@ inline int rope_head_groups(int64_t H, int64_t per_group, int num_sms) {
   return (int)((H + each - 1) / each);
 }
 
+// Head norms with rotation (norm_rope.cu): one of queries and keys.
+struct NormSide {
+  const void* x;              // [T, H, d] by strides (elements), unit last stride
+  const void* g;              // gradient: the result's gradient, likewise
+  void* y;                    // the result, or x's gradient
+  const void* w;              // [d_norm] weights
+  float* dw;                  // gradient: [d_norm]
+  int64_t x_stride_t, x_stride_h, g_stride_t, g_stride_h, y_stride_t, y_stride_h;
+  int H;
+  int groups;                 // groups of lanes that share a token's heads (set by the launch)
+  int ctas;                   // gradient: CTAs that work for this side (set by the launch)
+};
+struct NormArgs {
+  NormSide side[2];           // queries, keys (H = 0: none)
+  const int32_t* positions;   // [T] (unused without RoPE columns)
+  float* part;                // gradient: [ctas][d_norm] partial sums of dw
+  int T, d, d_norm, d_rope;
+  int w_f32;                  // weights are float32, not bf16
+  float eps;
+  dsa_rope_freqs table;
+};
+constexpr int kNormMaxCtas = 304;   // of a gradient call; also what its workspace is sized for
+
 struct AppendArgs {
   const uint16_t* c_kv;       // [T, 512] bf16, row stride c_stride
   const uint16_t* k_pe;       // [T, d_rope] bf16, row stride pe_stride
@@ -133,6 +156,11 @@ struct DecodeArgs {
   float* part_o;              // [2 groups][heads padded][512] normalised partial outputs
   float* part_lse;            // [2 groups][heads padded] their log-sum-exp, base 2
   unsigned int* err;
+  // tree form: [B, n] mask words, [B] drafted tokens or null (n of every request); H is then
+  // the query rows of a request, n * heads
+  const uint64_t* tree_mask;
+  const int32_t* num_draft;
+  int n, heads;
   int B, H, N, k, ld, max_blocks, block_size;
   int cap;                    // positions that the block table has room for
   int groups;                 // CTA groups (each of head_blocks CTAs)
@@ -225,6 +253,7 @@ int launch_masked_mha(const MaskedArgs& a, int num_sms, cudaStream_t stream);
 int launch_wait_timeout(unsigned int* err, cudaStream_t stream);
 int launch_kv_fp8(const Fp8KvArgs& a, bool quantize, int num_sms, cudaStream_t stream);
 int launch_rope(RopeArgs& a, bool f32, bool vec, int num_sms, cudaStream_t stream);
+int launch_norm_rope(NormArgs& a, bool f32, bool vec, bool gradient, int num_sms, cudaStream_t stream);
 int launch_kv_append(const AppendArgs& a, bool fp8, cudaStream_t stream);
 
 // Heads per CTA of the decode kernel and the CTAs its heads take.  (FP8 rows: the
@@ -236,6 +265,21 @@ inline int decode_head_blocks(int H, bool fp8) {
 constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
 // max_tiles: an upper bound of a request's key tiles (1: nothing is split).
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
+int launch_tree_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
+
+// Rows that move in the caches of one or more layers (kv_keep.cu).
+struct KeepArgs {
+  void* caches[DSA_MAX_CACHES];
+  const int32_t* block_table;   // [B, max_blocks]
+  const int32_t* kv_lens;       // [B]
+  const int32_t* num_draft;     // [B] or null: n of every request
+  const int32_t* keep;          // [B, m], ascending, -1 ends
+  int32_t* new_lens;            // [B]
+  unsigned int* err;
+  int B, m, n, N, max_blocks, block_size;
+  int row_pieces;               // 16-byte pieces of a row
+};
+int launch_kv_keep(const KeepArgs& a, int num_caches, cudaStream_t stream);
 
 // dsa_sparse_prefill with the streamed-call fields of SparseArgs (ready, done,
 // done_blk; all null / 0 for an ordinary call).  Same checks and DSA_* status

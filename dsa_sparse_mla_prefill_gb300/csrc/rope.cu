@@ -32,13 +32,6 @@ namespace rope {
 constexpr int NT = 256;
 constexpr int UNROLL = 4;   // heads in flight per thread
 
-__device__ __forceinline__ void cos_sin(uint64_t turns, int32_t pos, float m, float& c, float& s) {
-  const int64_t t = (int64_t)(turns * (uint64_t)(int64_t)pos);
-  sincospif(__ll2float_rn(t) * 1.0842021724855044e-19f /* 2^-63: half turns */, &s, &c);
-  c *= m;
-  s *= m;
-}
-
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -93,7 +86,7 @@ __global__ void __launch_bounds__(NT) rope_kernel(const __grid_constant__ RopeAr
   float c[PPT], s[PPT];
 #pragma unroll
   for (int i = 0; i < PPT; ++i) {
-    cos_sin(a.table.turns[item * PPT + i], pos, a.table.mscale, c[i], s[i]);
+    rope_cos_sin(a.table.turns[item * PPT + i], pos, a.table.mscale, c[i], s[i]);
     if (a.gradient) s[i] = -s[i];
   }
   const E* x = static_cast<const E*>(a.x) + (int64_t)t * a.x_stride_t;
@@ -242,7 +235,7 @@ __global__ void __launch_bounds__(NT_APPEND) append_kernel(const __grid_constant
   if (pe) {
     if (a.rotate) {
       float c, s;
-      cos_sin(a.table.turns[lane], pos, a.table.mscale, c, s);
+      rope_cos_sin(a.table.turns[lane], pos, a.table.mscale, c, s);
       const float x = bf16_to_f32(p), y = bf16_to_f32(q);
       p = f32_to_bf16_rn(x * c - y * s);
       q = f32_to_bf16_rn(x * s + y * c);

@@ -1,0 +1,15 @@
+// Attention of a tree of drafted tokens per request over the paged latent cache.
+//
+//     out[b,i,h,:] = softmax_j(scale q[b,i,h,:] . c_j) . c_j[0:512],   lse likewise,
+// over the positions j of request b in front of its drafted tokens, and of those the ones
+// that token i's mask word names.  A request's n tokens x H heads are the query rows of the
+// paged decode kernel; only the tiles that hold drafted tokens look at the mask.
+#include "paged_decode.cuh"
+
+namespace dsa {
+
+int launch_tree_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream) {
+  return decode::launch_decode<true>(a, fp8, d_rope, max_tiles, stream);
+}
+
+}  // namespace dsa

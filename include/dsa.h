@@ -444,6 +444,65 @@ int dsa_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, void* y, int
              int dtype, const int32_t* positions, int T, int H, const dsa_rope_freqs* freqs, int gradient,
              dsa_stream_t stream);
 
+/* RMS norms of the heads of queries and keys, with the rotation of their RoPE
+ * columns in the same pass.  A row is one head of one token, d columns:
+ *     r = 1 / sqrt(sum_{c < d_norm} x_c^2 / d_norm + eps)
+ *     n_c = x_c r w_c (c < d_norm), x_c (d_norm <= c < d)
+ *     y = n with its last freqs->d_rope columns turned as dsa_rope turns them.
+ * d_norm = d is a norm of whole heads; d = 576 with d_norm = 512 and one head is
+ * a token's latent row on its way into the cache (dsa_kv_append, freqs NULL).
+ *
+ * q, q_out     [T, Hq, d] by strides in elements (unit last stride), as dsa_rope's
+ *              x and y: q_out may be q (same strides), otherwise it must not
+ *              overlap an input; its heads and tokens must not overlap each other;
+ *              q may be broadcast (stride 0).
+ * k, k_out     [T, Hk, d] likewise.  Hq or Hk may be 0: that side's pointers are
+ *              then ignored.  The two results must not overlap.
+ * dtype        of q, k and results: DSA_DTYPE_BF16 (rounded once) or DSA_DTYPE_F32.
+ * q_weight, k_weight  [d_norm] of weight_dtype (bf16 or fp32).
+ * positions    DEVICE int32 [T], any value; ignored (may be NULL) without freqs.
+ * freqs        HOST, copied into the launch, or NULL: nothing is turned.
+ * The arithmetic is float32, with subnormal values taken for zero; a row's sum of
+ * squares has to stay finite there.
+ * DSA_ERR_INVALID_ARG also: d < 1, d_norm outside [1, d], freqs->d_rope > d, eps
+ * negative or not finite.  DSA_ERR_UNSUPPORTED: d > 1024, another dtype, more
+ * than 2^32 - 256 rows.
+ * Any strides and alignments of whole elements; 16-byte aligned rows, heads and
+ * pointers with d, d_norm and d - d_rope multiples of 16 bytes' worth of elements
+ * and d_rope of 32 bytes' run fastest. */
+#define DSA_NORM_MAX_D 1024
+int dsa_qk_norm_rope(const void* q, int64_t q_stride_t, int64_t q_stride_h, void* q_out, int64_t q_out_stride_t,
+                     int64_t q_out_stride_h, int Hq, const void* k, int64_t k_stride_t, int64_t k_stride_h, void* k_out,
+                     int64_t k_out_stride_t, int64_t k_out_stride_h, int Hk, int dtype, const void* q_weight,
+                     const void* k_weight, int weight_dtype, const int32_t* positions, int T, int d, int d_norm,
+                     float eps, const dsa_rope_freqs* freqs, dsa_stream_t stream);
+
+/* The gradients of dsa_qk_norm_rope: of its inputs and weights, given those of its
+ * results.  With g = q_grad, its last d_rope columns turned back:
+ *     gq_c = r (g_c w_c - q_c r^2 / d_norm * sum_{e < d_norm} g_e w_e q_e)  (c < d_norm),  g_c (else)
+ *     gq_weight_c = sum over all tokens and heads of g_c q_c r,
+ * and the same for k.
+ *
+ * q, k         the inputs of the forward call (not its results).
+ * q_grad, k_grad  [T, H, d] gradients of the results; may be broadcast.
+ * gq, gk       [T, H, d] contiguous (out) of dtype; must not overlap an input.
+ * gq_weight, gk_weight  fp32 [d_norm] (out), summed in float32 in an order that
+ *              depends on sizes and the GPU alone: the same inputs give the same
+ *              bits.  T = 0 gives zeros.
+ * workspace    DEVICE scratch, 16-byte aligned, of at least
+ *              dsa_qk_norm_rope_gradient_workspace(d_norm) bytes; nothing in it has
+ *              to survive between calls or start at zero; calls that share it
+ *              must not overlap on the GPU.
+ * Everything else, and the errors, as dsa_qk_norm_rope. */
+int64_t dsa_qk_norm_rope_gradient_workspace(int d_norm);
+int dsa_qk_norm_rope_gradient(const void* q_grad, int64_t q_grad_stride_t, int64_t q_grad_stride_h, const void* q,
+                              int64_t q_stride_t, int64_t q_stride_h, void* gq, int Hq, const void* k_grad,
+                              int64_t k_grad_stride_t, int64_t k_grad_stride_h, const void* k, int64_t k_stride_t,
+                              int64_t k_stride_h, void* gk, int Hk, int dtype, const void* q_weight,
+                              const void* k_weight, int weight_dtype, const int32_t* positions, int T, int d, int d_norm,
+                              float eps, const dsa_rope_freqs* freqs, float* gq_weight, float* gk_weight,
+                              void* workspace, int64_t workspace_bytes, dsa_stream_t stream);
+
 /* New tokens' latent rows into a paged cache.  Token t of request r at
  * position p is written to row block_table[r][p / block_size] * block_size +
  * p % block_size: columns 0..511 from c_kv, then d_rope columns from k_pe
@@ -506,6 +565,67 @@ int dsa_paged_decode(const uint16_t* q, const void* cache, int cache_format, int
                      const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
                      const int32_t* idx, int k, int ld, int B, int H, int d_qk, int d_v, float scale, uint16_t* out,
                      float* lse, void* workspace, int64_t workspace_bytes, dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Checking drafted tokens (speculative decoding) over the paged latent cache (no
+ * counterpart on the pages): several new tokens per request, a tree by their
+ * ancestors, attend in one call; the accepted path's rows then take their places.
+ * Like the decode step, positions, lengths and tables are read on the device.
+ * ---------------------------------------------------------------------- */
+
+/* Attention of a tree of drafted tokens per request.  Request b's n_b drafted
+ * tokens are its last positions: token j's row lies at position ctx_b + j,
+ * ctx_b = kv_lens[b] - n_b (appended there before the call; their rotary positions
+ * are the caller's, by depth).  Token i sees every position below ctx_b, and of
+ * the drafted tokens j those with bit j of tree_mask[b,i] set:
+ *     out[b,i,h,:] = softmax_j(scale * q[b,i,h,:] . c_j) . c_j[0:512],  lse likewise.
+ *
+ * q            bf16 [B, n, H, d_qk], 16-byte aligned; 1 <= n <= DSA_TREE_MAX_TOKENS,
+ *              1 <= H <= 128, n * H <= DSA_TREE_MAX_ROWS.
+ * tree_mask    DEVICE uint64 [B, n], 8-byte aligned; a token that is to see itself
+ *              has its own bit set.  Bits from n_b on are ignored.
+ * num_draft    DEVICE int32 [B], or NULL: n_b = n.  Values are cut to [0, n].
+ * out, lse     bf16 [B, n, H, 512] (16-byte aligned), fp32 [B, n, H].  Padding
+ *              tokens (i >= n_b) and tokens without a visible key get out = 0 and
+ *              lse = -inf.
+ * cache, block_table, kv_lens, scale, counted errors and everything else as for
+ * dsa_paged_decode without idx.  Drafted rows that no token of the request sees
+ * are never read into a result, whatever they hold; one that some of its tokens see
+ * has to be finite, or the tokens that do not see it may get NaN as well.
+ * workspace    as dsa_paged_decode's, of at least dsa_tree_decode_workspace(B, n, H,
+ *              max_blocks * block_size) bytes. */
+#define DSA_TREE_MAX_TOKENS 64
+#define DSA_TREE_MAX_ROWS 2048
+int64_t dsa_tree_decode_workspace(int B, int n, int H, int64_t max_positions);
+int dsa_tree_decode(const uint16_t* q, const void* cache, int cache_format, int N, int ld_kv,
+                    const int32_t* block_table, int max_blocks, int block_size, const int32_t* kv_lens,
+                    const uint64_t* tree_mask, const int32_t* num_draft, int B, int n, int H, int d_qk, int d_v,
+                    float scale, uint16_t* out, float* lse, void* workspace, int64_t workspace_bytes,
+                    dsa_stream_t stream);
+
+/* The accepted path takes its places: in every cache, the row of request b's drafted
+ * token keep[b,i] moves to position ctx_b + i, and new_lens[b] = ctx_b + the number
+ * of tokens kept.  Rows move whole (row_bytes); rows behind the kept ones, and
+ * those of other positions, stay as they are.
+ *
+ * caches       HOST array of num_caches (1 .. DSA_MAX_CACHES) DEVICE pointers, copied into
+ *              the launch: the cache of each layer, [N] packed rows of row_bytes bytes
+ *              (a multiple of 16), any format, 16-byte aligned, all different.
+ * kv_lens      DEVICE int32 [B], drafted tokens included; zero or less: a padding
+ *              request, left alone (new_lens[b] = kv_lens[b]).
+ * num_draft    DEVICE int32 [B] or NULL, as for dsa_tree_decode; n <= DSA_TREE_MAX_TOKENS.
+ * keep         DEVICE int32 [B, m], m <= DSA_TREE_MAX_TOKENS: drafted tokens of the path
+ *              in ascending order, the first -1 ends it.  Any other entry that is not
+ *              in [0, n_b) or not above the one before it ends the path as well
+ *              and is counted (counts[0] of dsa_last_device_error).
+ * new_lens     DEVICE int32 [B] (out), another array than kv_lens.
+ * A request with n_b outside [0, n] or above its length is left alone and counted. A
+ * row whose block id or row is out of range does not move and is counted.
+ * Requests must not share the pages of their drafted positions. */
+#define DSA_MAX_CACHES 128
+int dsa_kv_keep(void* const* caches, int num_caches, int64_t row_bytes, int N, const int32_t* block_table,
+                int max_blocks, int block_size, const int32_t* kv_lens, const int32_t* num_draft, int n,
+                const int32_t* keep, int m, int B, int32_t* new_lens, dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Form choice (host only, no GPU call).  "[Perf][GLM-5.3-Flash] ...", commit

@@ -509,6 +509,114 @@ def paged_decode(q_bits, cache, block_table, kv_lens, block_size: int, scale: fl
 
 
 # ----------------------------------------------------------------------------
+# norms in front of the rotation; checking drafted tokens
+# ----------------------------------------------------------------------------
+def norm_rope(x, w, positions, freqs, layout, eps: float, d_norm: int, mscale: float = 1.0) -> np.ndarray:
+    """x [T, H, d] (float64): the first d_norm columns over their root mean
+    square (eps added to the mean) times w, then the last 2 len(freqs) columns
+    turned by positions (freqs None: none)."""
+    y = np.array(x, dtype=np.float64)
+    y[..., :d_norm] *= np.asarray(w) / np.sqrt((y[..., :d_norm] ** 2).mean(-1, keepdims=True) + eps)
+    if freqs is not None:
+        r = y.shape[-1] - 2 * len(freqs)
+        y[..., r:] = rope(y[..., r:], positions, freqs, layout, mscale)
+    return y
+
+
+def norm_rope_gradient(g, x, w, positions, freqs, layout, eps: float, d_norm: int, mscale: float = 1.0):
+    """Gradients of sum(g * norm_rope(x, w)) by x and by w, from the chain rule
+    through the unit row u = x / rms: d u_c / d x_e = (delta_ce - u_c u_e /
+    d_norm) / rms."""
+    g, x = np.array(g, dtype=np.float64), np.asarray(x, dtype=np.float64)
+    if freqs is not None:
+        r = x.shape[-1] - 2 * len(freqs)
+        g[..., r:] = rope(g[..., r:], positions, freqs, layout, mscale, gradient=True)
+    rms = np.sqrt((x[..., :d_norm] ** 2).mean(-1, keepdims=True) + eps)
+    u, gu = x[..., :d_norm] / rms, g[..., :d_norm] * np.asarray(w)
+    gw = (g[..., :d_norm] * u).sum(axis=(0, 1))
+    g[..., :d_norm] = (gu - u * (gu * u).mean(-1, keepdims=True)) / rms
+    return g, gw
+
+
+def tree_decode(q_bits, cache, block_table, kv_lens, tree_mask, block_size: int, scale: float, num_draft=None):
+    """Attention of n drafted tokens per request (q [B, n, H, d_qk]) over the
+    latent rows (cache, float64 [N, d_qk]): the request's last num_draft[b]
+    positions (n if None) are its drafted tokens, token i sees every position
+    before them and drafted token j where bit j of tree_mask[b][i] is set;
+    tokens from num_draft[b] on see nothing.  Absent and counted as in
+    paged_decode, drafted positions that no token sees being passed over.
+    Returns what paged_decode returns, with [B, n, H] for its [B, H]."""
+    q = bf16_to_f64(q_bits)
+    B, n, H, _ = q.shape
+    bt = np.asarray(block_table, dtype=np.int64)
+    res = dict(out=np.zeros((B, n, H, 512)), lse=np.full((B, n, H), -np.inf), spread=np.zeros((B, n, H, 512)),
+               mass=np.zeros((B, n, H)), bad=0)
+    for b in range(B):
+        length = int(kv_lens[b])
+        drafted = n if num_draft is None else min(max(int(num_draft[b]), 0), n)
+        context = length - drafted
+        if length > bt.shape[1] * block_size:
+            length = bt.shape[1] * block_size
+            res["bad"] += 1
+        seen = [{j for j in range(drafted) if int(tree_mask[b][i]) >> j & 1} for i in range(drafted)]
+        any_of = set().union(*seen) if seen else set()
+        row = {}
+        for p in range(max(length, 0)):
+            if p >= context and p - context not in any_of:
+                continue
+            blk = bt[b, p // block_size]
+            r = blk * block_size + p % block_size
+            if blk < 0 or r >= len(cache):
+                res["bad"] += 1
+                continue
+            row[p] = int(r)
+        for i in range(drafted):
+            rows = [r for p, r in row.items() if p < context or p - context in seen[i]]
+            if not rows:
+                continue
+            c = cache[np.array(rows)]
+            res["out"][b, i], res["lse"][b, i] = attend(q[b, i], c, c[:, :512], scale)
+            w = np.exp(scale * (q[b, i] @ c.T) - res["lse"][b, i][:, None])
+            res["spread"][b, i] = w @ np.abs(c[:, :512])
+            res["mass"][b, i] = (abs(scale) * (np.abs(q[b, i]) @ np.abs(c).T)).max(axis=1)
+    return res
+
+
+def kv_keep(block_table, kv_lens, keep, block_size: int, N: int, n: int, num_draft=None):
+    """(moves, new lengths, bad): rows (source, destination) in the order of the
+    path, all read before any is written."""
+    bt = np.asarray(block_table, dtype=np.int64)
+    moves, lens, bad = [], [], 0
+    for b in range(len(kv_lens)):
+        length = int(kv_lens[b])
+        drafted = n if num_draft is None else int(num_draft[b])
+        if length <= 0 or not 0 <= drafted <= min(n, length):
+            bad += length > 0
+            lens.append(length)
+            continue
+        context, kept = length - drafted, 0
+        for e in (int(x) for x in keep[b]):
+            if e == -1:
+                break
+            if not (0 <= e < drafted and (kept == 0 or e > int(keep[b][kept - 1]))):
+                bad += 1
+                break
+            if e != kept:
+                rows = []
+                for p in (context + e, context + kept):
+                    blk = bt[b, p // block_size] if p // block_size < bt.shape[1] else -1
+                    r = int(blk) * block_size + p % block_size
+                    rows.append(r if blk >= 0 and r < N else -1)
+                if min(rows) < 0:
+                    bad += 1
+                else:
+                    moves.append(tuple(rows))
+            kept += 1
+        lens.append(context + kept)
+    return moves, np.array(lens, dtype=np.int32), bad
+
+
+# ----------------------------------------------------------------------------
 # comparison used by the parity tests
 # ----------------------------------------------------------------------------
 
