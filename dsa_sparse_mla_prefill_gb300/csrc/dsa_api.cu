@@ -642,9 +642,9 @@ int dsa_qk_norm_rope(const void* q, int64_t q_stride_t, int64_t q_stride_h, void
   dsa::NormArgs a;
   memset(&a, 0, sizeof(a));
   if (Hq)
-    a.side[0] = {q, nullptr, q_out, q_weight, nullptr, q_stride_t, q_stride_h, 0, 0, q_out_stride_t, q_out_stride_h, Hq, 0, 0};
+    a.side[0] = {q, nullptr, q_out, q_weight, nullptr, q_stride_t, q_stride_h, 0, 0, q_out_stride_t, q_out_stride_h, Hq, 0};
   if (Hk)
-    a.side[1] = {k, nullptr, k_out, k_weight, nullptr, k_stride_t, k_stride_h, 0, 0, k_out_stride_t, k_out_stride_h, Hk, 0, 0};
+    a.side[1] = {k, nullptr, k_out, k_weight, nullptr, k_stride_t, k_stride_h, 0, 0, k_out_stride_t, k_out_stride_h, Hk, 0};
   if (Hq > 0 && Hk > 0 && T > 0 && q_out && q_out == k_out) return DSA_ERR_INVALID_ARG;
   a.positions = positions;
   a.T = T;
@@ -669,10 +669,10 @@ int dsa_qk_norm_rope_gradient(const void* q_grad, int64_t q_grad_stride_t, int64
   memset(&a, 0, sizeof(a));
   if (Hq)
     a.side[0] = {q, q_grad, gq, q_weight, gq_weight, q_stride_t, q_stride_h, q_grad_stride_t, q_grad_stride_h,
-                 (int64_t)Hq * d, d, Hq, 0, 0};
+                 (int64_t)Hq * d, d, Hq, 0};
   if (Hk)
     a.side[1] = {k, k_grad, gk, k_weight, gk_weight, k_stride_t, k_stride_h, k_grad_stride_t, k_grad_stride_h,
-                 (int64_t)Hk * d, d, Hk, 0, 0};
+                 (int64_t)Hk * d, d, Hk, 0};
   if (Hq > 0 && Hk > 0 && ((T > 0 && gq && gq == gk) || (gq_weight && gq_weight == gk_weight))) return DSA_ERR_INVALID_ARG;
   a.positions = positions;
   a.T = T;

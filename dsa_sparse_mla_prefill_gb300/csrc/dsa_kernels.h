@@ -102,8 +102,7 @@ struct NormSide {
   float* dw;                  // gradient: [d_norm]
   int64_t x_stride_t, x_stride_h, g_stride_t, g_stride_h, y_stride_t, y_stride_h;
   int H;
-  int groups;                 // groups of lanes that share a token's heads (set by the launch)
-  int ctas;                   // gradient: CTAs that work for this side (set by the launch)
+  int ctas;                   // CTAs that work for this side (set by the launch)
 };
 struct NormArgs {
   NormSide side[2];           // queries, keys (H = 0: none)
