@@ -732,39 +732,42 @@ int dsa_kv_append(const uint16_t* c_kv, int64_t c_stride, const uint16_t* k_pe, 
                                                                                                         : DSA_ERR_CUDA;
 }
 
-// Key tiles of a request that may attend to `positions`, and the CTA groups of
-// a call: no more than tiles, one CTA per SM.
-static int64_t decode_tiles(int64_t positions) {
-  return ((positions < INT32_MAX ? positions : INT32_MAX) + 127) / 128;
+// Key tiles of a request that may attend to `positions`, and the CTA groups of a call (the
+// blocks of all query rows): no more than tiles, one CTA per SM.
+static int64_t decode_tiles(const dsa::DecodeForm& f, int64_t positions) {
+  return ((positions < INT32_MAX ? positions : INT32_MAX) + f.keys - 1) / f.keys;
 }
-static int decode_groups(int B, int H, bool fp8, int64_t max_tiles) {
-  const int64_t tiles = B * max_tiles, most = dsa::kDecodeMaxCtas / dsa::decode_head_blocks(H, fp8);
-  return (int)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
+static int decode_blocks(const dsa::DecodeForm& f, int H) { return (H + f.rows - 1) / f.rows; }
+static int decode_groups(const dsa::DecodeForm& f, int B, int H, int64_t max_tiles, int num_sms) {
+  const int64_t tiles = B * max_tiles, most = num_sms / (decode_blocks(f, H) * f.ctas);
+  return (int)(tiles < 1 || most < 1 ? 1 : (tiles < most ? tiles : most));
 }
 
 // workspace: where the ranges end, then two partial results per CTA group
 // (log-sum-exp, then outputs)
-static int64_t decode_part_bytes(int H, bool fp8, int groups, int64_t* lse_at, int64_t* out_at) {
-  const int64_t hp = (int64_t)dsa::decode_head_blocks(H, fp8) * dsa::decode_heads_per_cta(H, fp8);
+static int64_t decode_part_bytes(const dsa::DecodeForm& f, int H, int groups, int64_t* lse_at, int64_t* out_at) {
+  const int64_t hp = (int64_t)decode_blocks(f, H) * f.rows;
   *lse_at = (16 * (1 + groups) + 255) / 256 * 256;
   *out_at = *lse_at + (2 * groups * hp * 4 + 255) / 256 * 256;
   return *out_at + 2 * groups * hp * 512 * 4;
 }
 
-static int64_t decode_workspace(int B, int H, int64_t max_positions) {
+static int64_t decode_workspace(int B, int H, int64_t max_positions, bool tree) {
   int64_t l, o, most = 0;   // of either cache format
   for (int fp8 = 0; fp8 < 2; ++fp8) {
-    const int64_t n = decode_part_bytes(H, fp8, decode_groups(B, H, fp8, decode_tiles(max_positions)), &l, &o);
+    const dsa::DecodeForm f = dsa::decode_form(H, fp8, tree);
+    const int groups = decode_groups(f, B, H, decode_tiles(f, max_positions), dsa::kDecodeMaxCtas);
+    const int64_t n = decode_part_bytes(f, H, groups, &l, &o);
     most = n > most ? n : most;
   }
   return most;
 }
 int64_t dsa_paged_decode_workspace(int B, int H, int64_t max_positions) {
-  return B < 0 || H < 1 || H > 128 || max_positions < 0 ? -1 : decode_workspace(B, H, max_positions);
+  return B < 0 || H < 1 || H > 128 || max_positions < 0 ? -1 : decode_workspace(B, H, max_positions, false);
 }
 int64_t dsa_tree_decode_workspace(int B, int n, int H, int64_t max_positions) {
   if (B < 0 || n < 1 || n > DSA_TREE_MAX_TOKENS || H < 1 || H > 128 || n * H > DSA_TREE_MAX_ROWS || max_positions < 0) return -1;
-  return decode_workspace(B, n * H, max_positions);
+  return decode_workspace(B, n * H, max_positions, true);
 }
 
 // The decode step's attention: one token per request (tree NULL, n = 1), or n drafted ones.
@@ -783,18 +786,19 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   if (idx && (k < 0 || ld < k)) return DSA_ERR_INVALID_ARG;
   if ((int64_t)B * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   // key tiles of a request at most, and of all (counted in 32 bits)
-  const int64_t max_tiles = decode_tiles(idx ? k : (int64_t)max_blocks * block_size);
+  const bool fp8 = cache_format == DSA_CACHE_FP8;
+  const dsa::DecodeForm form = dsa::decode_form(H, fp8, tree != nullptr);
+  const int64_t max_tiles = decode_tiles(form, idx ? k : (int64_t)max_blocks * block_size);
   if (B * max_tiles > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (B == 0) return DSA_OK;
   if (!q || (!cache && N > 0) || !block_table || !kv_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||
       !aligned16(out) || !aligned4(lse))
     return DSA_ERR_INVALID_ARG;
-  const bool fp8 = cache_format == DSA_CACHE_FP8;
-  const int groups = decode_groups(B, H, fp8, max_tiles);
+  const int groups = decode_groups(form, B, H, max_tiles, dsa::kDecodeMaxCtas);
   int64_t lse_at, out_at;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < decode_part_bytes(H, fp8, groups, &lse_at, &out_at))
+      workspace_bytes < decode_part_bytes(form, H, groups, &lse_at, &out_at))
     return DSA_ERR_INVALID_ARG;
   DevInfo* d;
   if (!dev_info(&d)) return DSA_ERR_CUDA;
@@ -826,10 +830,10 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   a.cap = (int)((int64_t)max_blocks * block_size < INT32_MAX ? (int64_t)max_blocks * block_size : INT32_MAX);
   a.scale = scale;
   a.tr = g_trace;
-  a.head_blocks = dsa::decode_head_blocks(H, fp8);
+  a.head_blocks = decode_blocks(form, H);
   // (a GPU with fewer SMs than the workspace is sized for runs fewer ranges)
-  const int most = d->num_sms / a.head_blocks;
-  a.groups = groups < most ? groups : (most > 0 ? most : 1);
+  const int most = decode_groups(form, B, H, max_tiles, d->num_sms);
+  a.groups = groups < most ? groups : most;
   // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
   const bool none = N == 0;
   const bool mapped = fp8 ? dsa::make_row_gather_map_u8(&a.tmap_kv, none ? (const void*)q : cache,
@@ -840,15 +844,17 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   if (!mapped) return DSA_ERR_CUDA;
   // whole-context calls load runs of rows: the largest power of two in the page size, at most a tile
   const int run = block_size & -block_size;
-  a.box_rows = idx || none || run < 8 ? 0 : (run < 128 ? run : 128);
+  const int most_rows = form.ctas == 2 ? 64 : 128;   // (of a pair's half slot)
+  a.box_rows = idx || none || run < 8 ? 0 : (run < most_rows ? run : most_rows);
   a.fetch_bytes = a.box_rows && !fp8 ? dsa::decode_fetch_bytes(a.box_rows, 2ll * ld_kv, 2 * d_qk) : 0;
   if (a.box_rows &&
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;
-  if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, dsa::decode_heads_per_cta(H, fp8))) return DSA_ERR_CUDA;
-  const int r = tree ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
-                     : dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
+  if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, form.rows / form.ctas)) return DSA_ERR_CUDA;
+  const int r = form.ctas == 2 ? dsa::launch_tree_pair(a, d_rope, (int)max_tiles, (cudaStream_t)stream)
+                : tree         ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
+                               : dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);
 }
 

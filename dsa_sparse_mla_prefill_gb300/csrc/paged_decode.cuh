@@ -1092,6 +1092,14 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
                       a);
 }
 
+// The join of what range borders cut; padded: rows of a part.
+static inline int launch_join(const DecodeArgs& a, int padded, int max_tiles, cudaStream_t stream) {
+  if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
+  const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
+  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, padded)
+                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, padded);
+}
+
 template <bool TREE>
 static int launch_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream) {
   const int hb = decode_heads_per_cta(a.H, fp8);
@@ -1106,11 +1114,7 @@ static int launch_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cud
     else r = d_rope ? launch_t<32, 9, false, TREE>(a, stream) : launch_t<32, 8, false, TREE>(a, stream);
   }
   if (r != 0) return r;
-  if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
-  const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
-  const int pad = a.head_blocks * hb;
-  return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, pad)
-                             : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, pad);
+  return launch_join(a, a.head_blocks * hb, max_tiles, stream);
 }
 
 }  // namespace decode

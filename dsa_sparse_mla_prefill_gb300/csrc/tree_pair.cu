@@ -1,0 +1,713 @@
+// Attention of a tree of drafted tokens over bf16 latent rows, for more than 64 query rows per
+// request (tokens x heads): CTA pairs with the query rows on the tensor cores' M side.
+//
+// Bound: at 128 rows and more a key row's flops (2 * 1088 each query row) take longer than its
+// 1152 bytes take from HBM, so the tensor cores are the roof, and what feeds them.
+//
+// A pair (2-CTA cluster, cta_group::2) holds a block of 128 query rows of one request, 64 in
+// each CTA, and walks the keys in tiles of 256:
+//   S = Q K^T     M = 128, N = 256: CTA r supplies its 64 rows of Q (resident) and 128 keys'
+//                 rows of the tile; it gets S of its own 64 query rows, TMEM lanes 0-63 with
+//                 the even CTA's keys, lanes 64-127 with the odd one's.
+//   softmax       thread = (query row, 64 of the tile's keys): row maxima stay in the CTA
+//                 (four threads a row, one exchange through shared memory), P goes to shared
+//                 memory as the A operand of the same CTA's rows.
+//   O += P V      M = 128, N = 256 for output columns 256 m + ..: CTA r supplies columns 256 m +
+//                 128 r .. +127 of all 256 keys.  O takes 2 x 128 TMEM columns, S twice 128.
+// With the query rows as M, nothing of P or the maxima crosses the pair, and each CTA's MMAs
+// read 4.2 KB of shared memory per 64 query rows x key (with the keys as M, as the decode kernel has it,
+// 64 rows to a CTA: 5.8) and load 1.1 KB (2.2).
+//
+// All loads go through one ring of 16 KB slots in the order in which the one MMA warp uses
+// them: the tile's nine 64-column chunks of 128 keys, then eight V slots (64 keys x 128
+// columns) of the tile before, so that a tile's softmax runs beside the next tile's QK.  A
+// request's first tile comes after the last P.V of the one before, whose Q it replaces.
+//
+// Split over the length, join and the rows of absent keys as in paged_decode.cuh; a range of
+// tiles is walked by the pairs of all row blocks at the same time.
+#include <cfloat>
+
+#include "paged_decode.cuh"
+
+namespace dsa {
+namespace treepair {
+
+using decode::border_of;
+using decode::drafted_of;
+using decode::elect_one;
+using decode::evict_first_policy;
+using decode::evict_normal_policy;
+using decode::range_begin;
+using decode::row_at;
+using decode::warp_scan;
+
+constexpr int TK = 256;              // keys of a tile
+constexpr int ROWS = 64;             // query rows of a CTA
+constexpr int NI = 4;                // tiles of rows ahead
+constexpr int NSLOT = 7;
+constexpr float kTau = 8.0f;         // lazy-rescale threshold (log2 units)
+constexpr uint16_t kBoth = 3;
+constexpr int W_MMA = 8, W_SCHED = 9, W_Q = 10, W_LOAD = 11;
+constexpr int NTHREADS = 640;        // 20 warps (two without work), launched at 96 registers
+constexpr int REGS_SOFTMAX = 168, REGS_REST = 48;
+static_assert(256 * REGS_SOFTMAX + (NTHREADS - 256) * REGS_REST <= NTHREADS * 96, "registers");
+
+constexpr uint32_t SLOT_BYTES = 16384u, HALF_BYTES = 8192u;
+constexpr uint32_t Q_CHUNK = ROWS * 128u;
+constexpr uint32_t P_COLUMN = ROWS * 128u;         // 64 rows x 64 keys
+constexpr uint32_t OFF_RING = 0;
+constexpr uint32_t OFF_Q = OFF_RING + NSLOT * SLOT_BYTES;
+constexpr uint32_t OFF_P = OFF_Q + 9 * Q_CHUNK;
+constexpr uint32_t OFF_ROWS = OFF_P + 4 * P_COLUMN;
+constexpr uint32_t OFF_META = OFF_ROWS + NI * TK * 4u;
+constexpr uint32_t OFF_VALID = OFF_META + NI * 16u;
+constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums
+constexpr uint32_t OFF_BAR = OFF_RED + 3u * 4u * ROWS * 4u;
+constexpr int NBAR = 48;
+constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
+constexpr uint32_t SMEM_BYTES = OFF_MISC + 64u + 1024u;
+static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
+constexpr uint32_t COL_O = 0, COL_S = 256;
+
+enum {
+  B_FULL = 0,       // [NSLOT] even CTA: armed for both CTAs' bytes
+  B_EMPTY = 8,      // [NSLOT] one commit
+  B_QF = 16,        // even CTA
+  B_QE = 17,
+  B_SF = 18,        // [2] one commit
+  B_SE = 20,        // [2] even CTA: 16 softmax warps of the pair
+  B_PF = 22,        // even CTA: 16 warps
+  B_PE = 23,        // one commit: the tile's P.V is done
+  B_OF = 24,
+  B_OE = 25,        // even CTA: 16 warps
+  B_IDXF = 26,      // [NI]
+  B_IDXE = 30,      // [NI] the loaders, Q, MMA and softmax warps
+  B_GRP = 34,       // [2] the four warps of 32 query rows
+  B_PLAN = 36,
+  B_DRAIN = 37,
+};
+constexpr int F_FIRST = 1, F_LAST = 2, F_PART = 4, F_SLOT1 = 8, F_BOX = 16, F_FULL = 32;
+
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
+  return len <= 0 ? 0 : (int)(((uint32_t)min(len, a.cap) + TK - 1) / TK);
+}
+
+// As mbar_wait_vote, for barriers that the other CTA of the pair arrives on too.
+template <bool POLL>
+__device__ __forceinline__ bool wait_vote(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  const uint64_t t0 = globaltimer();
+  uint32_t turns = 0;
+#pragma unroll 1
+  while (true) {
+    uint32_t ok;
+    if constexpr (POLL)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+      ok = mbar_try_wait_cluster_sleep(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (POLL && (++turns & 15u)) continue;
+    const bool raised = *abort_flag != 0, late = globaltimer() - t0 > kWaitTimeoutNs;
+    if (__any_sync(0xffffffffu, raised | late)) {
+      mbar_give_up(abort_flag, err);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void mma_pair_x4_elected(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t da,
+                                                    uint32_t db, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %11, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %5, %6, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %7, %8, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %9, %10, %3, 1;\n\t}"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "l"(a + da), "l"(b + db), "l"(a + 2ull * da),
+      "l"(b + 2ull * db), "l"(a + 3ull * da), "l"(b + 3ull * db), "r"(leader)
+      : "memory");
+}
+// (a completion signal to the barriers of both CTAs; no data moves)
+__device__ __forceinline__ void commit_pair_elected(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
+      ::"r"(bar), "r"(leader), "h"(kBoth)
+      : "memory");
+}
+
+// TMA loads into this CTA that complete on a barrier of the even one.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void gather_half(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, const int32_t* rows,
+                                            uint32_t bar, uint64_t policy) {
+#pragma unroll 4
+  for (int n = 0; n < 16; ++n) {
+    const int4 r = *reinterpret_cast<const int4*>(rows + 4 * n);
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %9, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n\t}" ::"r"(dst + n * 512),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar), "l"(policy),
+        "r"(leader)
+        : "memory");
+  }
+}
+
+template <int NC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pair_kernel(const __grid_constant__ DecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);   // (the same offset in both CTAs)
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile uint32_t* tmem_base_ptr = misc;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* plan = reinterpret_cast<volatile int*>(misc + 2);
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + OFF_ROWS);
+  int4* meta = reinterpret_cast<int4*>(smem + OFF_META);
+  uint64_t* valid = reinterpret_cast<uint64_t*>(smem + OFF_VALID);
+  unsigned int* err = a.err;
+  const uint32_t bar0 = sbase + OFF_BAR;
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto poll = [&](int i, uint32_t parity) { return wait_vote<true>(bar(i), parity, abort_flag, err); };
+  auto doze = [&](int i, uint32_t parity) { return wait_vote<false>(bar(i), parity, abort_flag, err); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int pair = (int)blockIdx.x >> 1;
+  const int range = pair / a.head_blocks, rb = pair - range * a.head_blocks;
+  const int row0 = 2 * ROWS * rb + ROWS * rank;   // this CTA's first query row of a request
+
+  if (warp == 0) {
+    for (int i = lane; i < NBAR; i += 32) {
+      uint32_t n = 1;
+      if (i == B_SE || i == B_SE + 1 || i == B_PF || i == B_OE) n = 16;
+      if (i >= B_IDXE && i < B_IDXE + NI) n = NSLOT + 2 + 8;
+      if (i == B_GRP || i == B_GRP + 1) n = 4;
+      mbar_init(&bars[i], n);
+    }
+    if (lane == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc_pair(const_cast<uint32_t*>(tmem_base_ptr), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before a copy, commit or arrival reaches them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_ptr;
+  launch_dependents();
+
+  if (warp >= W_MMA) {
+    regs_dec<REGS_REST>();
+    wait_for_previous();
+    if (warp == W_SCHED) {
+      // ----------------------------------------------------------------
+      // scheduler: as the decode kernel's, in each CTA for itself
+      // ----------------------------------------------------------------
+      const bool counts = rank == 0 && rb == 0;
+      const int per = (a.B + 31) / 32;
+      const int b_lo = min(a.B, lane * per), b_hi = min(a.B, b_lo + per);
+      uint32_t mine = 0;
+#pragma unroll 4
+      for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(a, a.kv_lens[i]);
+      const uint32_t incl = warp_scan(mine), total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+      const uint32_t ng = total < (uint32_t)a.groups ? total : (uint32_t)a.groups;
+      const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
+      const int nt = (uint32_t)range < ng ? (int)(range_begin(range + 1, total, ng) - x0) : 0;
+      if (lane == 0) {
+        *plan = nt;
+        mbar_arrive(&bars[B_PLAN]);
+        if (range == 0 && counts) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
+        if (counts) a.borders[1 + range] = make_int4(0, 0, 0, 0);
+      }
+      int b = 0, j = 0, len = 0, n = 0;
+      const bool holds = nt > 0 && before <= x0 && x0 < before + mine;
+      if (holds) {
+        uint32_t at = before;
+        for (b = b_lo;; ++b) {
+          len = a.kv_lens[b];
+          n = tiles_of(a, len);
+          if (x0 < at + n) break;
+          at += n;
+        }
+        j = (int)(x0 - at);
+      }
+      const int holder = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+      b = __shfl_sync(0xffffffffu, b, holder & 31);
+      j = __shfl_sync(0xffffffffu, j, holder & 31);
+      len = __shfl_sync(0xffffffffu, len, holder & 31);
+      int bad = 0, seg = 0, drafted = 0, context = 0;
+      uint64_t seen = 0;
+      const bool from_start = j == 0;
+      bool enter = true;
+      for (int it = 0; it < nt; ++it) {
+        const int r = it % NI;
+        if (enter) {
+          while (it > 0) {
+            len = b + lane < a.B ? a.kv_lens[b + lane] : 0;
+            const uint32_t there = __ballot_sync(0xffffffffu, tiles_of(a, len) > 0);
+            const int skip = there ? __ffs(there) - 1 : 32;
+            b += skip;
+            len = __shfl_sync(0xffffffffu, len, skip & 31);
+            if (there) break;
+            if (b >= a.B) {   // (never with lengths that stay: a tile is left)
+              b = a.B - 1;
+              break;
+            }
+          }
+          n = tiles_of(a, len);
+          drafted = drafted_of(a, b);
+          context = len - drafted;
+          uint64_t any = 0;
+          for (int i = lane; i < drafted; i += 32) any |= a.tree_mask[(int64_t)b * a.n + i];
+          seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
+          if (len > a.cap) {
+            if (j == 0 && lane == 0) ++bad;
+            len = a.cap;
+          }
+        }
+        if (!doze(B_IDXE + r, ((it / NI) & 1) ^ 1)) break;
+        const int32_t* bt = a.block_table + (int64_t)b * a.max_blocks;
+        int32_t row[8];
+        const uint32_t e0 = (uint32_t)j * TK + 8 * lane;
+        uint32_t page = e0 / (uint32_t)a.block_size, at = e0 - page * (uint32_t)a.block_size, there8 = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          bool there = e0 + e < (uint32_t)len;
+          const int bit = (int)(e0 + e) - context;
+          if (there && bit >= 0) there = seen >> bit & 1;   // (bit < drafted, for the position is below len)
+          row[e] = -1;
+          if (there) row[e] = row_at(a, bt, page, at, bad);
+          there8 |= row[e] >= 0 ? 1u << e : 0u;
+          if (++at == (uint32_t)a.block_size) { at = 0; ++page; }
+        }
+        *reinterpret_cast<int4*>(rows + r * TK + 8 * lane) = make_int4(row[0], row[1], row[2], row[3]);
+        *reinterpret_cast<int4*>(rows + r * TK + 8 * lane + 4) = make_int4(row[4], row[5], row[6], row[7]);
+        reinterpret_cast<uint8_t*>(valid + 4 * r)[lane] = (uint8_t)there8;
+        const bool all = __all_sync(0xffffffffu, there8 == 0xffu);
+        const bool first = enter, last = (it == nt - 1) || (j == n - 1);
+        if (lane == 0) {
+          int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (all && a.box_rows > 0 ? F_BOX : 0);
+          if (all && (j + 1) * TK <= context) flags |= F_FULL;
+          if (last) {
+            const bool whole = (seg > 0 || from_start) && j == n - 1;
+            if (!whole) flags |= F_PART | (seg > 0 ? F_SLOT1 : 0);
+          }
+          meta[r] = make_int4(b, flags, j * TK - context, drafted);
+          if (it == nt - 1 && counts) a.borders[1 + range] = make_int4(b, n, j + 1, 0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IDXF + r]);
+        enter = (j == n - 1);
+        if (enter) {
+          ++b;
+          j = 0;
+          ++seg;
+        } else {
+          ++j;
+        }
+      }
+      bad = __reduce_add_sync(0xffffffffu, bad);
+      if (lane == 0 && bad && counts) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
+    } else if (const int nt = doze(B_PLAN, 0) ? *plan : 0; warp >= W_LOAD && warp < W_LOAD + NSLOT) {
+      // ----------------------------------------------------------------
+      // loads, a warp per ring slot.  A slot is two halves of 64 rows x 64 columns: of K the
+      // two halves of this CTA's 128 keys, of V (64 keys) its two 64-column groups.
+      // ----------------------------------------------------------------
+      const int own = warp - W_LOAD;
+      const uint32_t dst = sbase + OFF_RING + own * SLOT_BYTES;
+      const uint32_t full0 = map_peer(bar(B_FULL + own), 0);
+      const uint32_t leader = elect_one();
+      const int per_half = a.box_rows > 0 ? ROWS / a.box_rows : 1;   // boxes
+      const int h = lane / per_half, at = (lane - h * per_half) * a.box_rows;   // of a lane with a box
+      const uint64_t k_policy = evict_normal_policy(), v_policy = a.head_blocks == 1 ? evict_first_policy() : k_policy;
+      int slot = 0;
+      uint32_t used = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it <= nt && ok; ++it) {
+        bool first = true;
+        if (it < nt) {
+          if (!doze(B_IDXF + it % NI, (it / NI) & 1)) { ok = false; break; }
+          first = (meta[it % NI].y & F_FIRST) != 0;
+        }
+        // the V of the tile before comes behind this tile's K, or in front of a request's first
+#pragma unroll 1
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+          const bool is_k = ph == (first ? 1 : 0);
+          const int tile = is_k ? it : it - 1;
+          if (tile < 0 || tile >= nt) continue;
+          const int r = tile % NI, stages = is_k ? NC : 8;
+          const bool box = (meta[r].y & F_BOX) != 0;
+          const int32_t* tile_rows = rows + r * TK;
+#pragma unroll 1
+          for (int st = 0; st < stages; ++st) {
+            const bool mine_now = slot == own;
+            if (++slot == NSLOT) slot = 0;
+            if (!mine_now) continue;
+            if (!doze(B_EMPTY + own, (used & 1) ^ 1)) { ok = false; break; }
+            if (rank == 0 && leader) mbar_arrive_expect_tx(&bars[B_FULL + own], 2u * SLOT_BYTES);
+            __syncwarp();
+            ++used;
+            // first row and column of half 0, and how half 1 differs
+            const int ra = is_k ? 128 * rank : 64 * (st & 3), rstep = is_k ? 64 : 0;
+            const int ca = is_k ? 64 * st : 256 * (st >> 2) + 128 * rank, cstep = is_k ? 0 : 64;
+            const uint64_t policy = is_k ? k_policy : v_policy;
+            if (box) {
+              if (h < 2)
+                load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
+            } else {
+              gather_half(leader, dst, &a.tmap_kv, ca, tile_rows + ra, full0, policy);
+              gather_half(leader, dst + HALF_BYTES, &a.tmap_kv, ca + cstep, tile_rows + ra + rstep, full0, policy);
+            }
+          }
+          __syncwarp();
+          if (!is_k && lane == 0) mbar_arrive(&bars[B_IDXE + r]);   // (the tile's last use of its rows)
+        }
+      }
+      if (!ok) {
+        // a wait ran out: let loads in flight land before this CTA can leave
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 20000ull) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == W_Q) {
+      // ----------------------------------------------------------------
+      // Q of every request of the range; then the requests without keys
+      // ----------------------------------------------------------------
+      const uint32_t full0 = map_peer(bar(B_QF), 0);
+      int nq = 0;
+      for (int it = 0; it < nt; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDXF + r, (it / NI) & 1)) break;
+        const int4 mt = meta[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
+        if (!(mt.y & F_FIRST)) continue;
+        if (!doze(B_QE, (nq & 1) ^ 1)) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars[B_QF], 2u * NC * Q_CHUNK);
+        __syncwarp();
+        if (lane < NC) tma_load_2d_pair(sbase + OFF_Q + lane * Q_CHUNK, &a.tmap_q, lane * 64, mt.x * a.H + row0, full0);
+        ++nq;
+      }
+      const int mine = min(a.H - row0, ROWS);
+      for (int b = range; b < a.B; b += a.groups) {
+        if (tiles_of(a, a.kv_lens[b]) > 0) continue;
+        uint4* o = reinterpret_cast<uint4*>(a.out + ((int64_t)b * a.H + row0) * 512);
+        for (int i = lane; i < mine * 64; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        for (int i = lane; i < mine; i += 32) a.lse[(int64_t)b * a.H + row0 + i] = -INFINITY;
+      }
+    } else if (warp == W_MMA) {
+      // ----------------------------------------------------------------
+      // MMA issuer (even CTA), in the ring's order
+      // ----------------------------------------------------------------
+      constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 256, false, false), IDESC_PV = idesc_bf16_f32(128, 256, false, true);
+      const uint32_t leader = elect_one();
+      const uint64_t k_desc = sdesc_sw128(sbase + OFF_RING, 16, 1024), v_desc = sdesc_sw128(sbase + OFF_RING, HALF_BYTES, 1024);
+      const uint64_t q_desc = sdesc_sw128(sbase + OFF_Q, 16, 1024), p_desc = sdesc_sw128(sbase + OFF_P, 16, 1024);
+      uint32_t slot = 0, phase = 0;
+      int nq = -1;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it <= nt && ok; ++it) {
+        bool first = true;
+        if (it < nt) {
+          if (!doze(B_IDXF + it % NI, (it / NI) & 1)) break;
+          first = (__shfl_sync(0xffffffffu, meta[it % NI].y, 0) & F_FIRST) != 0;
+        }
+#pragma unroll 1
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+          const bool is_k = ph == (first ? 1 : 0);
+          const int tile = is_k ? it : it - 1;
+          if (tile < 0 || tile >= nt) continue;
+          const int r = tile % NI;
+          const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
+          if (rank != 0) {
+            if (!is_k && leader) mbar_arrive(&bars[B_IDXE + r]);
+            continue;
+          }
+          const int sb = tile & 1;
+          if (is_k) {
+            if (flags & F_FIRST) {
+              ++nq;
+              if (!poll(B_QF, nq & 1)) { ok = false; break; }
+            }
+            if (!poll(B_SE + sb, ((tile >> 1) & 1) ^ 1)) { ok = false; break; }
+            if (leader) DSA_TRACE(a.tr, tile, 3);
+          } else {
+            if (leader) mbar_arrive(&bars[B_IDXE + r]);
+            if (!poll(B_PF, tile & 1)) { ok = false; break; }
+            if ((flags & F_FIRST) && !poll(B_OE, (nq & 1) ^ 1)) { ok = false; break; }
+            if (leader) DSA_TRACE(a.tr, tile, 0);
+          }
+          const int stages = is_k ? NC : 8;
+#pragma unroll 1
+          for (int st = 0; st < stages; ++st) {
+            if (!poll(B_FULL + slot, phase)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t at = (uint64_t)(slot * (SLOT_BYTES >> 4));
+            if (is_k)
+              mma_pair_x4_elected(leader, tmem + COL_S + sb * 128, q_desc + (uint64_t)(st * (Q_CHUNK >> 4)), k_desc + at, 2u, 2u,
+                                  IDESC_QK, st > 0 ? 1u : 0u);
+            else
+              mma_pair_x4_elected(leader, tmem + COL_O + (st >> 2) * 128, p_desc + (uint64_t)((st & 3) * (P_COLUMN >> 4)),
+                                  v_desc + at, 2u, 128u, IDESC_PV, (flags & F_FIRST) && (st & 3) == 0 ? 0u : 1u);
+            commit_pair_elected(leader, bar(B_EMPTY + slot));
+            if (++slot == NSLOT) { slot = 0; phase ^= 1; }
+          }
+          if (!ok) break;
+          if (is_k) {
+            if (leader) DSA_TRACE(a.tr, tile, 4);
+            commit_pair_elected(leader, bar(B_SF + sb));
+            if (flags & F_LAST) commit_pair_elected(leader, bar(B_QE));
+          } else {
+            if (leader) DSA_TRACE(a.tr, tile, 7);
+            commit_pair_elected(leader, bar(B_PE));
+            if (flags & F_LAST) commit_pair_elected(leader, bar(B_OF));
+          }
+        }
+      }
+      if (rank == 0) {   // every MMA issued above has completed
+        commit_pair_elected(leader, bar(B_DRAIN));
+        if (leader) mbar_wait_drain(&bars[B_DRAIN], 0, err);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_inc<REGS_SOFTMAX>();
+    // --------------------------------------------------------------------
+    // softmax and epilogue: warps w, w + 2 (the odd CTA's keys), w + 4 (the second 64 keys
+    // of a half) and w + 6 have query rows 32 w .. 32 w + 31, w = 0, 1
+    // --------------------------------------------------------------------
+    const int wg = warp >> 2, half = (warp >> 1) & 1, rg = warp & 1;
+    const int row = 32 * rg + lane;                       // of this CTA
+    const int part = 2 * half + wg;                       // 64 keys of the tile: 64 part ..
+    const int q_row = row0 + row;                         // of the request
+    const int token = q_row / a.heads;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t p_row = sbase + OFF_P + part * P_COLUMN + row * 128;
+    const uint32_t sw = (uint32_t)(row & 7);
+    float* red = reinterpret_cast<float*>(smem + OFF_RED);
+    float* sums = red + 2 * 4 * ROWS;
+    const uint32_t se0 = map_peer(bar(B_SE), 0), pf0 = map_peer(bar(B_PF), 0), oe0 = map_peer(bar(B_OE), 0);
+    auto arrive0 = [&](uint32_t at) {   // the warp's arrival on a barrier of the even CTA
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(at);
+    };
+    uint32_t grp_phase = 0;
+    auto group = [&]() {   // the four warps of these rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_GRP + rg]);
+      const bool ok = poll(B_GRP + rg, grp_phase);
+      grp_phase ^= 1u;
+      return ok;
+    };
+    float m_run = -FLT_MAX, l_run = 0.f;   // (the lowest finite value, so that no difference of two is NaN)
+    uint64_t word = 0;
+    int seg = -1;
+    wait_for_previous();
+    const int nt = poll(B_PLAN, 0) ? *plan : 0;
+#pragma unroll 1
+    for (int it = 0; it < nt; ++it) {
+      const int r = it % NI, sb = it & 1;
+      if (!doze(B_IDXF + r, (it / NI) & 1)) break;
+      const int4 mt = meta[r];
+      if (mt.y & F_FIRST) {
+        ++seg;
+        m_run = -FLT_MAX;
+        l_run = 0.f;
+        word = token < mt.w ? a.tree_mask[(int64_t)mt.x * a.n + token] : 0ull;
+      }
+      uint64_t vis = ~0ull;
+      if (!(mt.y & F_FULL)) {
+        const int first = mt.z + 64 * part;   // drafted token of this thread's first key
+        vis = first >= 64 ? 0ull : first >= 0 ? word >> first : first <= -64 ? ~0ull : (word << -first) | (~0ull >> (64 + first));
+        vis &= valid[4 * r + part];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
+      if (!poll(B_SF + sb, (it >> 1) & 1)) break;
+      if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 5);
+      tc_fence_after();
+      float t[64];
+      tmem_ld_cols<64>(t_lane + COL_S + sb * 128 + wg * 64, t);
+      tmem_ld_wait();
+      tc_fence_before();
+      arrive0(se0 + 8u * sb);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) mul2(t[i], t[i + 1], t[i], t[i + 1], scale_log2, scale_log2);
+      if (!(mt.y & F_FULL)) {
+        const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          t[i] = lo >> i & 1 ? t[i] : -INFINITY;
+          t[32 + i] = hi >> i & 1 ? t[32 + i] : -INFINITY;
+        }
+      }
+      float mx[4] = {t[0], t[1], t[2], t[3]};
+#pragma unroll
+      for (int i = 4; i < 64; i += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], t[i + k]);
+      }
+      float* redb = red + sb * (4 * ROWS);
+      redb[part * ROWS + row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (!group()) break;
+      const float top = fmaxf(fmaxf(redb[row], redb[ROWS + row]), fmaxf(redb[2 * ROWS + row], redb[3 * ROWS + row]));
+      // lazy rescale: the reference moves only where a score is above it by more than kTau
+      float alpha = 1.f;
+      if (top > m_run + kTau) {
+        alpha = exp2f(m_run - top);
+        m_run = top;
+        l_run *= alpha;
+      }
+      const float neg = -m_run;
+      float s0 = 0.f, s1 = 0.f;
+      uint32_t pk[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        float x, y;
+        add2(x, y, t[i], t[i + 1], neg, neg);
+        x = exp2f(x);
+        y = exp2f(y);
+        add2(s0, s1, s0, s1, x, y);
+        pk[i / 2] = pack_bf16x2(x, y);
+      }
+      l_run += s0 + s1;
+      // the previous P.V must be done before P is overwritten and O rescaled
+      if (!poll(B_PE, sb ^ 1)) break;
+      tc_fence_after();
+      if (!(mt.y & F_FIRST) && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          float o[16];
+          const uint32_t ta = t_lane + COL_O + wg * 128 + c;
+          tmem_ld16(ta, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] *= alpha;
+          tmem_st16(ta, o);
+        }
+        tmem_st_wait();
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        sts128(p_row + ((((uint32_t)c) ^ sw) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive0(pf0);
+      if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
+      if (!(mt.y & F_LAST)) continue;
+
+      // ---- epilogue of the request's part in this range
+      sums[part * ROWS + row] = l_run;
+      if (!group()) break;
+      const bool live = token < mt.w;   // (a padding token's row is zeros)
+      const float l = live ? (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]) : 0.f;
+      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      const bool is_part = (mt.y & F_PART) != 0, there = q_row < a.H;
+      const int64_t slot_row = (int64_t)(2 * range + ((mt.y & F_SLOT1) ? 1 : 0)) * (2 * ROWS * a.head_blocks) + q_row;
+      if (part == 0 && there) {
+        const float l2 = l != 0.f ? m_run + log2f(l) : -INFINITY;
+        if (is_part)
+          a.part_lse[slot_row] = l2;
+        else
+          a.lse[(int64_t)mt.x * a.H + q_row] = l2 * 0.6931471805599453f;
+      }
+      if (!poll(B_OF, seg & 1)) break;
+      tc_fence_after();
+      // output columns 256 wg + 128 half .. +127 of this row
+      const int col = 256 * wg + 128 * half;
+      uint4* out = reinterpret_cast<uint4*>(a.out + ((int64_t)mt.x * a.H + q_row) * 512 + col);
+      float4* po = reinterpret_cast<float4*>(a.part_o + slot_row * 512 + col);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float o[32];
+        tmem_ld_cols<32>(t_lane + COL_O + wg * 128 + c, o);
+        tmem_ld_wait();
+        if (c == 96) {
+          tc_fence_before();
+          arrive0(oe0);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = inv != 0.f ? o[i] * inv : 0.f;
+        if (there) {
+          if (is_part) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) po[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[c / 8 + i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves or frees tensor memory while the pair may still use it
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int NC>
+static int launch_t(DecodeArgs& a, cudaStream_t stream) {
+  static int done[64] = {0}, clusters[64] = {0};
+  if (allow_smem(reinterpret_cast<const void*>(tree_pair_kernel<NC>), SMEM_BYTES, done) != 0) return -1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  // pairs that the GPU holds at a time: a range more would run behind all others
+  int most = dev < 64 ? clusters[dev] : 0;
+  if (most == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kDecodeMaxCtas);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&most, tree_pair_kernel<NC>, &cfg) != cudaSuccess || most < 1) {
+      cudaGetLastError();
+      most = kDecodeMaxCtas / 2;
+    }
+    if (dev < 64) clusters[dev] = most;
+  }
+  most = most / a.head_blocks;
+  if (a.groups > most) a.groups = most > 0 ? most : 1;
+  return launch_after(tree_pair_kernel<NC>, dim3((unsigned)(2 * a.groups * a.head_blocks)), NTHREADS, SMEM_BYTES, stream, a);
+}
+
+}  // namespace treepair
+
+int launch_tree_pair(DecodeArgs& a, int d_rope, int max_tiles, cudaStream_t stream) {
+  const int r = d_rope ? treepair::launch_t<9>(a, stream) : treepair::launch_t<8>(a, stream);
+  if (r != 0) return r;
+  return decode::launch_join(a, 2 * treepair::ROWS * a.head_blocks, max_tiles, stream);
+}
+
+}  // namespace dsa
