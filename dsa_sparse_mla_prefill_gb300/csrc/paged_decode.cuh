@@ -1093,8 +1093,14 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
 }
 
 // The join of what range borders cut; padded: rows of a part.
-static inline int launch_join(const DecodeArgs& a, int padded, int max_tiles, cudaStream_t stream) {
+static inline int launch_join(const DecodeArgs& a, int padded, int max_tiles, bool tree, cudaStream_t stream) {
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
+  if (tree) {
+    // two pieces a warp where a request is cut once, about one where it is cut as often as the batch's mean
+    const int64_t mean = 2ll * a.H * a.B / a.groups, most = a.H / 2;
+    const int64_t y = mean < most ? mean : most;
+    return launch_after(tree_join_kernel<8>, dim3((unsigned)(a.groups - 1), (unsigned)(y < 4 ? 4 : y)), NT_JOIN, 0, stream, a, padded);
+  }
   const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
   return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, padded)
                              : launch_after(join_kernel<5>, grid, NT_JOIN, 0, stream, a, padded);
@@ -1114,7 +1120,7 @@ static int launch_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cud
     else r = d_rope ? launch_t<32, 9, false, TREE>(a, stream) : launch_t<32, 8, false, TREE>(a, stream);
   }
   if (r != 0) return r;
-  return launch_join(a, a.head_blocks * hb, max_tiles, stream);
+  return launch_join(a, a.head_blocks * hb, max_tiles, TREE, stream);
 }
 
 }  // namespace decode

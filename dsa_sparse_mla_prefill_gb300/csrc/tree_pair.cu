@@ -18,10 +18,9 @@
 // read 4.2 KB of shared memory per 64 query rows x key (with the keys as M, as the decode kernel has it,
 // 64 rows to a CTA: 5.8) and load 1.1 KB (2.2).
 //
-// All loads go through one ring of 16 KB slots in the order in which the one MMA warp uses
-// them: the tile's nine 64-column chunks of 128 keys, then eight V slots (64 keys x 128
-// columns) of the tile before, so that a tile's softmax runs beside the next tile's QK.  A
-// request's first tile comes after the last P.V of the one before, whose Q it replaces.
+// Loads go through two rings of 16 KB slots, a tile's nine 64-column chunks of 128 keys and its
+// eight V slots (64 keys x 128 columns), each with a loading warp per slot and an issuing
+// warp of its own, so that a tile's softmax and P.V run beside the next tile's QK.
 //
 // Split over the length, join and the rows of absent keys as in paged_decode.cuh; a range of
 // tiles is walked by the pairs of all row blocks at the same time.
@@ -44,11 +43,12 @@ using decode::warp_scan;
 constexpr int TK = 256;              // keys of a tile
 constexpr int ROWS = 64;             // query rows of a CTA
 constexpr int NI = 4;                // tiles of rows ahead
-constexpr int NSLOT = 7;
+constexpr int NK = 3, NV = 2;        // ring slots
+constexpr int NSLOT = NK + NV;
 constexpr float kTau = 8.0f;         // lazy-rescale threshold (log2 units)
 constexpr uint16_t kBoth = 3;
-constexpr int W_MMA = 8, W_SCHED = 9, W_Q = 10, W_LOAD = 11;
-constexpr int NTHREADS = 640;        // 20 warps (two without work), launched at 96 registers
+constexpr int W_QK = 8, W_SCHED = 9, W_Q = 10, W_LOAD = 11, W_PV = 18;
+constexpr int NTHREADS = 640;        // 20 warps (the last without work), launched at 96 registers
 constexpr int REGS_SOFTMAX = 168, REGS_REST = 48;
 static_assert(256 * REGS_SOFTMAX + (NTHREADS - 256) * REGS_REST <= NTHREADS * 96, "registers");
 
@@ -58,7 +58,8 @@ constexpr uint32_t P_COLUMN = ROWS * 128u;         // 64 rows x 64 keys
 constexpr uint32_t OFF_RING = 0;
 constexpr uint32_t OFF_Q = OFF_RING + NSLOT * SLOT_BYTES;
 constexpr uint32_t OFF_P = OFF_Q + 9 * Q_CHUNK;
-constexpr uint32_t OFF_ROWS = OFF_P + 4 * P_COLUMN;
+constexpr uint32_t P_BYTES = 4 * P_COLUMN;
+constexpr uint32_t OFF_ROWS = OFF_P + 2 * P_BYTES;
 constexpr uint32_t OFF_META = OFF_ROWS + NI * TK * 4u;
 constexpr uint32_t OFF_VALID = OFF_META + NI * 16u;
 constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums
@@ -70,21 +71,22 @@ static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
 constexpr uint32_t COL_O = 0, COL_S = 256;
 
 enum {
-  B_FULL = 0,       // [NSLOT] even CTA: armed for both CTAs' bytes
-  B_EMPTY = 8,      // [NSLOT] one commit
+  B_FULL = 0,       // [NK K slots, then NV V slots] even CTA: armed for both CTAs' bytes
+  B_EMPTY = 8,      // one commit
   B_QF = 16,        // even CTA
   B_QE = 17,
   B_SF = 18,        // [2] one commit
   B_SE = 20,        // [2] even CTA: 16 softmax warps of the pair
-  B_PF = 22,        // even CTA: 16 warps
-  B_PE = 23,        // one commit: the tile's P.V is done
-  B_OF = 24,
-  B_OE = 25,        // even CTA: 16 warps
-  B_IDXF = 26,      // [NI]
-  B_IDXE = 30,      // [NI] the loaders, Q, MMA and softmax warps
-  B_GRP = 34,       // [2] the four warps of 32 query rows
-  B_PLAN = 36,
-  B_DRAIN = 37,
+  B_PF = 22,        // [2] this CTA's 8 softmax warps: its rows of P are stored
+  B_PR = 24,        // [2] even CTA: the odd one's are (relayed)
+  B_PE = 26,        // [2] one commit: the P.V that reads this P is done
+  B_OF = 28,
+  B_OE = 29,        // even CTA: 16 warps of the pair
+  B_IDXF = 30,      // [NI]
+  B_IDXE = 34,      // [NI] the loaders, Q, softmax and (even CTA) issuing warps
+  B_GRP = 38,       // [2] the four warps of 32 query rows
+  B_PLAN = 40,
+  B_DRAIN = 41,     // [2] one per issuer
 };
 constexpr int F_FIRST = 1, F_LAST = 2, F_PART = 4, F_SLOT1 = 8, F_BOX = 16, F_FULL = 32;
 
@@ -95,7 +97,7 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
 // As mbar_wait_vote, for barriers that the other CTA of the pair arrives on too.
 template <bool POLL>
 __device__ __forceinline__ bool wait_vote(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = 0;   // (the clock is first read on the sixteenth turn)
   uint32_t turns = 0;
 #pragma unroll 1
   while (true) {
@@ -103,14 +105,16 @@ __device__ __forceinline__ bool wait_vote(uint32_t bar, uint32_t parity, volatil
     if constexpr (POLL)
       asm volatile(
           "{\n\t.reg .pred p;\n\t"
-          "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
           "selp.u32 %0, 1, 0, p;\n\t}"
           : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     else
       ok = mbar_try_wait_cluster_sleep(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
-    if (POLL && (++turns & 15u)) continue;
-    const bool raised = *abort_flag != 0, late = globaltimer() - t0 > kWaitTimeoutNs;
+    if ((++turns & 15u)) continue;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    const bool raised = *abort_flag != 0, late = now - t0 > kWaitTimeoutNs;
     if (__any_sync(0xffffffffu, raised | late)) {
       mbar_give_up(abort_flag, err);
       return false;
@@ -194,15 +198,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
   if (warp == 0) {
     for (int i = lane; i < NBAR; i += 32) {
       uint32_t n = 1;
-      if (i == B_SE || i == B_SE + 1 || i == B_PF || i == B_OE) n = 16;
-      if (i >= B_IDXE && i < B_IDXE + NI) n = NSLOT + 2 + 8;
+      if (i == B_SE || i == B_SE + 1 || i == B_OE) n = 16;
+      if (i == B_PF || i == B_PF + 1) n = 8;
+      if (i >= B_IDXE && i < B_IDXE + NI) n = NSLOT + 1 + (rank == 0 ? 2 : 0) + 8;
       if (i == B_GRP || i == B_GRP + 1) n = 4;
       mbar_init(&bars[i], n);
     }
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == W_MMA) {
+  if (warp == W_QK) {
     tmem_alloc_pair(const_cast<uint32_t*>(tmem_base_ptr), 512);
     tmem_relinquish_pair();
   }
@@ -213,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
   const uint32_t tmem = *tmem_base_ptr;
   launch_dependents();
 
-  if (warp >= W_MMA) {
+  if (warp >= W_QK) {
     regs_dec<REGS_REST>();
     wait_for_previous();
     if (warp == W_SCHED) {
@@ -256,6 +261,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       uint64_t seen = 0;
       const bool from_start = j == 0;
       bool enter = true;
+      int fetch = -1;   // first row of a box to fetch to L2
+      const int sharers = 2 * a.head_blocks, share = 2 * rb + rank;   // CTAs that walk this range
       for (int it = 0; it < nt; ++it) {
         const int r = it % NI;
         if (enter) {
@@ -301,6 +308,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         *reinterpret_cast<int4*>(rows + r * TK + 8 * lane + 4) = make_int4(row[4], row[5], row[6], row[7]);
         reinterpret_cast<uint8_t*>(valid + 4 * r)[lane] = (uint8_t)there8;
         const bool all = __all_sync(0xffffffffu, there8 == 0xffu);
+        __syncwarp();
+        // the boxes of the tile one back, more than a tile ahead of its loads, to L2: by each CTA its share
+        if (fetch >= 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.rows_base + (int64_t)fetch * a.row_bytes),
+                       "r"(a.fetch_bytes)
+                       : "memory");
+        if (a.fetch_bytes) {
+          fetch = rows[r * TK + (lane & (TK / a.box_rows - 1)) * a.box_rows];   // of box `lane`
+          if (!all || lane >= TK / a.box_rows || lane % sharers != share) fetch = -1;
+        }
         const bool first = enter, last = (it == nt - 1) || (j == n - 1);
         if (lane == 0) {
           int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (all && a.box_rows > 0 ? F_BOX : 0);
@@ -327,59 +344,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (lane == 0 && bad && counts) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
     } else if (const int nt = doze(B_PLAN, 0) ? *plan : 0; warp >= W_LOAD && warp < W_LOAD + NSLOT) {
       // ----------------------------------------------------------------
-      // loads, a warp per ring slot.  A slot is two halves of 64 rows x 64 columns: of K the
-      // two halves of this CTA's 128 keys, of V (64 keys) its two 64-column groups.
+      // loads, a warp per slot of the K and the V ring.  A slot is two halves of 64 rows x 64
+      // columns: of K the two halves of this CTA's 128 keys, of V (64 keys) its two 64-column
+      // groups.
       // ----------------------------------------------------------------
       const int own = warp - W_LOAD;
+      const bool is_k = own < NK;
+      const int mine_slot = is_k ? own : own - NK, nslots = is_k ? NK : NV, stages = is_k ? NC : 8;
       const uint32_t dst = sbase + OFF_RING + own * SLOT_BYTES;
       const uint32_t full0 = map_peer(bar(B_FULL + own), 0);
       const uint32_t leader = elect_one();
       const int per_half = a.box_rows > 0 ? ROWS / a.box_rows : 1;   // boxes
       const int h = lane / per_half, at = (lane - h * per_half) * a.box_rows;   // of a lane with a box
-      const uint64_t k_policy = evict_normal_policy(), v_policy = a.head_blocks == 1 ? evict_first_policy() : k_policy;
+      // (the second read of a row, by the only block of query rows, marks it first to go)
+      const uint64_t policy = is_k || a.head_blocks > 1 ? evict_normal_policy() : evict_first_policy();
       int slot = 0;
       uint32_t used = 0;
       bool ok = true;
 #pragma unroll 1
-      for (int it = 0; it <= nt && ok; ++it) {
-        bool first = true;
-        if (it < nt) {
-          if (!doze(B_IDXF + it % NI, (it / NI) & 1)) { ok = false; break; }
-          first = (meta[it % NI].y & F_FIRST) != 0;
-        }
-        // the V of the tile before comes behind this tile's K, or in front of a request's first
+      for (int it = 0; it < nt && ok; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDXF + r, (it / NI) & 1)) { ok = false; break; }
+        const bool box = (meta[r].y & F_BOX) != 0;
+        const int32_t* tile_rows = rows + r * TK;
 #pragma unroll 1
-        for (int ph = 0; ph < 2 && ok; ++ph) {
-          const bool is_k = ph == (first ? 1 : 0);
-          const int tile = is_k ? it : it - 1;
-          if (tile < 0 || tile >= nt) continue;
-          const int r = tile % NI, stages = is_k ? NC : 8;
-          const bool box = (meta[r].y & F_BOX) != 0;
-          const int32_t* tile_rows = rows + r * TK;
-#pragma unroll 1
-          for (int st = 0; st < stages; ++st) {
-            const bool mine_now = slot == own;
-            if (++slot == NSLOT) slot = 0;
-            if (!mine_now) continue;
-            if (!doze(B_EMPTY + own, (used & 1) ^ 1)) { ok = false; break; }
-            if (rank == 0 && leader) mbar_arrive_expect_tx(&bars[B_FULL + own], 2u * SLOT_BYTES);
-            __syncwarp();
-            ++used;
-            // first row and column of half 0, and how half 1 differs
-            const int ra = is_k ? 128 * rank : 64 * (st & 3), rstep = is_k ? 64 : 0;
-            const int ca = is_k ? 64 * st : 256 * (st >> 2) + 128 * rank, cstep = is_k ? 0 : 64;
-            const uint64_t policy = is_k ? k_policy : v_policy;
-            if (box) {
-              if (h < 2)
-                load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
-            } else {
-              gather_half(leader, dst, &a.tmap_kv, ca, tile_rows + ra, full0, policy);
-              gather_half(leader, dst + HALF_BYTES, &a.tmap_kv, ca + cstep, tile_rows + ra + rstep, full0, policy);
-            }
-          }
+        for (int st = 0; st < stages; ++st) {
+          const bool mine_now = slot == mine_slot;
+          if (++slot == nslots) slot = 0;
+          if (!mine_now) continue;
+          if (!doze(B_EMPTY + own, (used & 1) ^ 1)) { ok = false; break; }
+          if (rank == 0 && leader) mbar_arrive_expect_tx(&bars[B_FULL + own], 2u * SLOT_BYTES);
           __syncwarp();
-          if (!is_k && lane == 0) mbar_arrive(&bars[B_IDXE + r]);   // (the tile's last use of its rows)
+          ++used;
+          // first row and column of half 0, and how half 1 differs
+          const int ra = is_k ? 128 * rank : 64 * (st & 3), rstep = is_k ? 64 : 0;
+          const int ca = is_k ? 64 * st : 256 * (st >> 2) + 128 * rank, cstep = is_k ? 0 : 64;
+          if (box) {
+            if (h < 2)
+              load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
+          } else {
+            gather_half(leader, dst, &a.tmap_kv, ca, tile_rows + ra, full0, policy);
+            gather_half(leader, dst + HALF_BYTES, &a.tmap_kv, ca + cstep, tile_rows + ra + rstep, full0, policy);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
       }
       if (!ok) {
         // a wait ran out: let loads in flight land before this CTA can leave
@@ -414,80 +423,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         for (int i = lane; i < mine * 64; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         for (int i = lane; i < mine; i += 32) a.lse[(int64_t)b * a.H + row0 + i] = -INFINITY;
       }
-    } else if (warp == W_MMA) {
+    } else if (warp == W_QK) {
       // ----------------------------------------------------------------
-      // MMA issuer (even CTA), in the ring's order
+      // QK issuer (even CTA)
       // ----------------------------------------------------------------
-      constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 256, false, false), IDESC_PV = idesc_bf16_f32(128, 256, false, true);
       const uint32_t leader = elect_one();
-      const uint64_t k_desc = sdesc_sw128(sbase + OFF_RING, 16, 1024), v_desc = sdesc_sw128(sbase + OFF_RING, HALF_BYTES, 1024);
-      const uint64_t q_desc = sdesc_sw128(sbase + OFF_Q, 16, 1024), p_desc = sdesc_sw128(sbase + OFF_P, 16, 1024);
-      uint32_t slot = 0, phase = 0;
-      int nq = -1;
-      bool ok = true;
+      if (rank == 0) {
+        constexpr uint32_t IDESC = idesc_bf16_f32(128, 256, false, false);
+        const uint64_t k_desc = sdesc_sw128(sbase + OFF_RING, 16, 1024), q_desc = sdesc_sw128(sbase + OFF_Q, 16, 1024);
+        uint32_t slot = 0, phase = 0;
+        int nq = -1;
+        bool ok = true;
 #pragma unroll 1
-      for (int it = 0; it <= nt && ok; ++it) {
-        bool first = true;
-        if (it < nt) {
-          if (!doze(B_IDXF + it % NI, (it / NI) & 1)) break;
-          first = (__shfl_sync(0xffffffffu, meta[it % NI].y, 0) & F_FIRST) != 0;
-        }
-#pragma unroll 1
-        for (int ph = 0; ph < 2 && ok; ++ph) {
-          const bool is_k = ph == (first ? 1 : 0);
-          const int tile = is_k ? it : it - 1;
-          if (tile < 0 || tile >= nt) continue;
-          const int r = tile % NI;
+        for (int it = 0; it < nt && ok; ++it) {
+          const int r = it % NI, sb = it & 1;
+          if (!doze(B_IDXF + r, (it / NI) & 1)) break;
           const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
-          if (rank != 0) {
-            if (!is_k && leader) mbar_arrive(&bars[B_IDXE + r]);
-            continue;
+          if (leader) mbar_arrive(&bars[B_IDXE + r]);
+          if (flags & F_FIRST) {
+            ++nq;
+            if (!poll(B_QF, nq & 1)) break;
           }
-          const int sb = tile & 1;
-          if (is_k) {
-            if (flags & F_FIRST) {
-              ++nq;
-              if (!poll(B_QF, nq & 1)) { ok = false; break; }
-            }
-            if (!poll(B_SE + sb, ((tile >> 1) & 1) ^ 1)) { ok = false; break; }
-            if (leader) DSA_TRACE(a.tr, tile, 3);
-          } else {
-            if (leader) mbar_arrive(&bars[B_IDXE + r]);
-            if (!poll(B_PF, tile & 1)) { ok = false; break; }
-            if ((flags & F_FIRST) && !poll(B_OE, (nq & 1) ^ 1)) { ok = false; break; }
-            if (leader) DSA_TRACE(a.tr, tile, 0);
-          }
-          const int stages = is_k ? NC : 8;
+          if (!poll(B_SE + sb, ((it >> 1) & 1) ^ 1)) break;
+          if (leader) DSA_TRACE(a.tr, it, 3);
 #pragma unroll 1
-          for (int st = 0; st < stages; ++st) {
+          for (int c = 0; c < NC; ++c) {
             if (!poll(B_FULL + slot, phase)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t at = (uint64_t)(slot * (SLOT_BYTES >> 4));
-            if (is_k)
-              mma_pair_x4_elected(leader, tmem + COL_S + sb * 128, q_desc + (uint64_t)(st * (Q_CHUNK >> 4)), k_desc + at, 2u, 2u,
-                                  IDESC_QK, st > 0 ? 1u : 0u);
-            else
-              mma_pair_x4_elected(leader, tmem + COL_O + (st >> 2) * 128, p_desc + (uint64_t)((st & 3) * (P_COLUMN >> 4)),
-                                  v_desc + at, 2u, 128u, IDESC_PV, (flags & F_FIRST) && (st & 3) == 0 ? 0u : 1u);
+            mma_pair_x4_elected(leader, tmem + COL_S + sb * 128, q_desc + (uint64_t)(c * (Q_CHUNK >> 4)),
+                                k_desc + (uint64_t)(slot * (SLOT_BYTES >> 4)), 2u, 2u, IDESC, c > 0 ? 1u : 0u);
             commit_pair_elected(leader, bar(B_EMPTY + slot));
-            if (++slot == NSLOT) { slot = 0; phase ^= 1; }
+            if (++slot == NK) { slot = 0; phase ^= 1; }
           }
           if (!ok) break;
-          if (is_k) {
-            if (leader) DSA_TRACE(a.tr, tile, 4);
-            commit_pair_elected(leader, bar(B_SF + sb));
-            if (flags & F_LAST) commit_pair_elected(leader, bar(B_QE));
-          } else {
-            if (leader) DSA_TRACE(a.tr, tile, 7);
-            commit_pair_elected(leader, bar(B_PE));
-            if (flags & F_LAST) commit_pair_elected(leader, bar(B_OF));
-          }
+          if (leader) DSA_TRACE(a.tr, it, 4);
+          commit_pair_elected(leader, bar(B_SF + sb));
+          if (flags & F_LAST) commit_pair_elected(leader, bar(B_QE));
+        }
+        commit_pair_elected(leader, bar(B_DRAIN));   // every MMA issued above has completed
+        if (leader) mbar_wait_drain(&bars[B_DRAIN], 0, err);
+      } else {
+        // relay: a releasing arrival from the softmax warps themselves takes 2000 cycles longer
+        const uint32_t pr0 = map_peer(bar(B_PR), 0);
+        for (int it = 0; it < nt; ++it) {
+          if (!poll(B_PF + (it & 1), (it >> 1) & 1)) break;
+          if (leader) mbar_arrive_remote(pr0 + 8u * (it & 1));
         }
       }
-      if (rank == 0) {   // every MMA issued above has completed
-        commit_pair_elected(leader, bar(B_DRAIN));
-        if (leader) mbar_wait_drain(&bars[B_DRAIN], 0, err);
+      __syncwarp();
+    } else if (warp == W_PV && rank == 0) {
+      // ----------------------------------------------------------------
+      // P.V issuer (even CTA).  (One warp for both products spent 380 cycles on a slot, whose
+      // four MMAs take 256: waiting, issuing and committing follow one another.)
+      // ----------------------------------------------------------------
+      constexpr uint32_t IDESC = idesc_bf16_f32(128, 256, false, true);
+      const uint32_t leader = elect_one();
+      const uint64_t v_desc = sdesc_sw128(sbase + OFF_RING + NK * SLOT_BYTES, HALF_BYTES, 1024), p_desc = sdesc_sw128(sbase + OFF_P, 16, 1024);
+      uint32_t slot = 0, phase = 0;
+      int nv = -1;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it < nt && ok; ++it) {
+        const int r = it % NI;
+        if (!doze(B_IDXF + r, (it / NI) & 1)) break;
+        const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
+        if (leader) mbar_arrive(&bars[B_IDXE + r]);
+        const int pb = it & 1;
+        if (!poll(B_PF + pb, (it >> 1) & 1) || !poll(B_PR + pb, (it >> 1) & 1)) break;
+        if (flags & F_FIRST) {
+          ++nv;
+          if (!poll(B_OE, (nv & 1) ^ 1)) break;
+        }
+        if (leader) DSA_TRACE(a.tr, it, 0);
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+          if (!poll(B_FULL + NK + slot, phase)) { ok = false; break; }
+          tc_fence_after();
+          mma_pair_x4_elected(leader, tmem + COL_O + (u >> 2) * 128, p_desc + (uint64_t)((pb * P_BYTES + (u & 3) * P_COLUMN) >> 4),
+                              v_desc + (uint64_t)(slot * (SLOT_BYTES >> 4)), 2u, 128u, IDESC,
+                              (flags & F_FIRST) && (u & 3) == 0 ? 0u : 1u);
+          commit_pair_elected(leader, bar(B_EMPTY + NK + slot));
+          if (++slot == NV) { slot = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if (leader) DSA_TRACE(a.tr, it, 7);
+        commit_pair_elected(leader, bar(B_PE + pb));
+        if (flags & F_LAST) commit_pair_elected(leader, bar(B_OF));
       }
+      commit_pair_elected(leader, bar(B_DRAIN + 1));
+      if (leader) mbar_wait_drain(&bars[B_DRAIN + 1], 0, err);
       __syncwarp();
     }
   } else {
@@ -507,11 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     const uint32_t sw = (uint32_t)(row & 7);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* sums = red + 2 * 4 * ROWS;
-    const uint32_t se0 = map_peer(bar(B_SE), 0), pf0 = map_peer(bar(B_PF), 0), oe0 = map_peer(bar(B_OE), 0);
-    auto arrive0 = [&](uint32_t at) {   // the warp's arrival on a barrier of the even CTA
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(at);
-    };
+    const uint32_t se0 = map_peer(bar(B_SE), 0), oe0 = map_peer(bar(B_OE), 0);
     uint32_t grp_phase = 0;
     auto group = [&]() {   // the four warps of these rows
       __syncwarp();
@@ -522,7 +542,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     };
     float m_run = -FLT_MAX, l_run = 0.f;   // (the lowest finite value, so that no difference of two is NaN)
     uint64_t word = 0;
-    int seg = -1;
+    // The part of a request that has ended: its last tile's meta, reference and this thread's sum.
+    bool pending = false;
+    int4 done = make_int4(0, 0, 0, 0);
+    float m_done = 0.f, l_done = 0.f;
+    int seg = 0;
+    auto epilogue = [&]() -> bool {
+      sums[part * ROWS + row] = l_done;
+      if (!group()) return false;
+      const bool live = token < done.w;   // (a padding token's row is zeros)
+      const float l = live ? (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]) : 0.f;
+      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      const bool is_part = (done.y & F_PART) != 0, there = q_row < a.H;
+      const int64_t slot_row = (int64_t)(2 * range + ((done.y & F_SLOT1) ? 1 : 0)) * (2 * ROWS * a.head_blocks) + q_row;
+      if (part == 0 && there) {
+        const float l2 = l != 0.f ? m_done + log2f(l) : -INFINITY;
+        if (is_part)
+          a.part_lse[slot_row] = l2;
+        else
+          a.lse[(int64_t)done.x * a.H + q_row] = l2 * 0.6931471805599453f;
+      }
+      if (!poll(B_OF, seg & 1)) return false;
+      ++seg;
+      tc_fence_after();
+      // output columns 256 wg + 128 half .. +127 of this row
+      const int col = 256 * wg + 128 * half;
+      uint4* out = reinterpret_cast<uint4*>(a.out + ((int64_t)done.x * a.H + q_row) * 512 + col);
+      float4* po = reinterpret_cast<float4*>(a.part_o + slot_row * 512 + col);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float o[32];
+        tmem_ld_cols<32>(t_lane + COL_O + wg * 128 + c, o);
+        tmem_ld_wait();
+        if (c == 96) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(oe0);   // (as above: O is read)
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = inv != 0.f ? o[i] * inv : 0.f;
+        if (there) {
+          if (is_part) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) po[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[c / 8 + i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          }
+        }
+      }
+      return true;
+    };
     wait_for_previous();
     const int nt = poll(B_PLAN, 0) ? *plan : 0;
 #pragma unroll 1
@@ -531,7 +603,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (!doze(B_IDXF + r, (it / NI) & 1)) break;
       const int4 mt = meta[r];
       if (mt.y & F_FIRST) {
-        ++seg;
         m_run = -FLT_MAX;
         l_run = 0.f;
         word = token < mt.w ? a.tree_mask[(int64_t)mt.x * a.n + token] : 0ull;
@@ -551,7 +622,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       tmem_ld_cols<64>(t_lane + COL_S + sb * 128 + wg * 64, t);
       tmem_ld_wait();
       tc_fence_before();
-      arrive0(se0 + 8u * sb);
+      // (a bare "read" signal: nothing of this warp to publish, and a releasing arrival
+      // takes 2000 cycles longer to get to the barrier below)
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(se0 + 8u * sb);
 #pragma unroll
       for (int i = 0; i < 64; i += 2) mul2(t[i], t[i + 1], t[i], t[i + 1], scale_log2, scale_log2);
       if (!(mt.y & F_FULL)) {
@@ -592,10 +666,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         pk[i / 2] = pack_bf16x2(x, y);
       }
       l_run += s0 + s1;
-      // the previous P.V must be done before P is overwritten and O rescaled
-      if (!poll(B_PE, sb ^ 1)) break;
-      tc_fence_after();
+      // O holds the P.V of the tile before when it is rescaled
       if (!(mt.y & F_FIRST) && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (!poll(B_PE + (sb ^ 1), ((it - 1) >> 1) & 1)) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
           float o[16];
@@ -608,60 +682,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         }
         tmem_st_wait();
       }
+      // P's buffer is free once the P.V two tiles back is done
+      if (!poll(B_PE + sb, ((it >> 1) & 1) ^ 1)) break;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        sts128(p_row + ((((uint32_t)c) ^ sw) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        sts128(p_row + sb * P_BYTES + ((((uint32_t)c) ^ sw) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       fence_proxy_async_smem();
       tc_fence_before();
-      arrive0(pf0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_PF + sb]);
       if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
-      if (!(mt.y & F_LAST)) continue;
-
-      // ---- epilogue of the request's part in this range
-      sums[part * ROWS + row] = l_run;
-      if (!group()) break;
-      const bool live = token < mt.w;   // (a padding token's row is zeros)
-      const float l = live ? (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]) : 0.f;
-      const float inv = l != 0.f ? 1.0f / l : 0.f;
-      const bool is_part = (mt.y & F_PART) != 0, there = q_row < a.H;
-      const int64_t slot_row = (int64_t)(2 * range + ((mt.y & F_SLOT1) ? 1 : 0)) * (2 * ROWS * a.head_blocks) + q_row;
-      if (part == 0 && there) {
-        const float l2 = l != 0.f ? m_run + log2f(l) : -INFINITY;
-        if (is_part)
-          a.part_lse[slot_row] = l2;
-        else
-          a.lse[(int64_t)mt.x * a.H + q_row] = l2 * 0.6931471805599453f;
+      // a request's outputs are stored once the next one's first P is
+      if (pending) {
+        if (!epilogue()) break;
+        pending = false;
       }
-      if (!poll(B_OF, seg & 1)) break;
-      tc_fence_after();
-      // output columns 256 wg + 128 half .. +127 of this row
-      const int col = 256 * wg + 128 * half;
-      uint4* out = reinterpret_cast<uint4*>(a.out + ((int64_t)mt.x * a.H + q_row) * 512 + col);
-      float4* po = reinterpret_cast<float4*>(a.part_o + slot_row * 512 + col);
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        float o[32];
-        tmem_ld_cols<32>(t_lane + COL_O + wg * 128 + c, o);
-        tmem_ld_wait();
-        if (c == 96) {
-          tc_fence_before();
-          arrive0(oe0);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = inv != 0.f ? o[i] * inv : 0.f;
-        if (there) {
-          if (is_part) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) po[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              out[c / 8 + i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-          }
-        }
+      if (mt.y & F_LAST) {
+        pending = true;
+        done = mt;
+        m_done = m_run;
+        l_done = l_run;
       }
     }
+    if (pending) epilogue();
   }
 
   __syncwarp();
@@ -669,7 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
   __syncthreads();
   cluster_sync();   // neither CTA leaves or frees tensor memory while the pair may still use it
   tc_fence_after();
-  if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
+  if (warp == W_QK) tmem_dealloc_pair(tmem, 512);
 }
 
 template <int NC>
@@ -707,7 +750,7 @@ static int launch_t(DecodeArgs& a, cudaStream_t stream) {
 int launch_tree_pair(DecodeArgs& a, int d_rope, int max_tiles, cudaStream_t stream) {
   const int r = d_rope ? treepair::launch_t<9>(a, stream) : treepair::launch_t<8>(a, stream);
   if (r != 0) return r;
-  return decode::launch_join(a, 2 * treepair::ROWS * a.head_blocks, max_tiles, stream);
+  return decode::launch_join(a, 2 * treepair::ROWS * a.head_blocks, max_tiles, true, stream);
 }
 
 }  // namespace dsa
