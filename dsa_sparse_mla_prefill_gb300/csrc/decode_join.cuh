@@ -157,12 +157,14 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   }
 }
 
-// The tree form's join, of up to thousands of query rows: a warp takes 128 columns of a row,
-// all parts of it, `DEEP` loads at a time; the borders inside a request share its rows.
-// (8 requests of 512 rows in 19 ranges, 38 MB of parts: 9 us against 21 with the kernel above,
-// whose CTAs take a row after the other.)
+// The tree form's join, of up to thousands of query rows: a warp takes 128 columns of a row, all
+// parts of it, eight loads at a time, or where there are more than eight parts the CTA's four
+// warps a fourth of them each; the borders inside a request share its rows.  (8 requests of 512
+// rows in 19 ranges, 38 MB of parts: 16 us cold against 21 with the kernel above, whose CTAs
+// take a row after the other.)
 template <int DEEP>
 __global__ void __launch_bounds__(NT_JOIN) tree_join_kernel(const __grid_constant__ DecodeArgs a, int rows_padded) {
+  __shared__ float4 acc[3][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   wait_for_previous();
@@ -174,13 +176,16 @@ __global__ void __launch_bounds__(NT_JOIN) tree_join_kernel(const __grid_constan
   auto slot_of = [&](int s) { return s == 0 ? first_slot : 2ll * (cut.first + s) * pitch; };
   const int pieces = 4 * a.H;
   const int c0 = (int)((int64_t)pieces * rank / nb), c1 = (int)((int64_t)pieces * (rank + 1) / nb);
+  const bool shared = S > DEEP;                      // a piece by the whole CTA
+  const int s0 = shared ? S * warp / 4 : 0, s1 = shared ? S * (warp + 1) / 4 : S;
+  const int step = (int)gridDim.y * (shared ? 1 : NT_JOIN / 32);
 #pragma unroll 1
-  for (int c = c0 + (int)blockIdx.y * (NT_JOIN / 32) + warp; c < c1; c += (int)gridDim.y * (NT_JOIN / 32)) {
+  for (int c = c0 + (shared ? (int)blockIdx.y : (int)blockIdx.y * (NT_JOIN / 32) + warp); c < c1; c += step) {
     const int row = c >> 2;
     const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)row * 128 + (c & 3) * 32 + lane;
     float4 v[DEEP];
 #pragma unroll
-    for (int k = 0; k < DEEP; ++k) v[k] = k < S ? src[slot_of(k) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < DEEP; ++k) v[k] = s0 + k < s1 ? src[slot_of(s0 + k) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
     float l[LSE], m = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int k = 0; k < LSE; ++k) l[k] = lane + 32 * k < S ? a.part_lse[slot_of(lane + 32 * k) + row] : -INFINITY;
@@ -197,21 +202,36 @@ __global__ void __launch_bounds__(NT_JOIN) tree_join_kernel(const __grid_constan
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s = 0; s < S; s += DEEP) {
-      // (DEEP parts lie in one of l's words)
-      const int word = s >> 5;
-      const float lw = word == 0 ? l[0] : word == 1 ? l[1] : word == 2 ? l[2] : word == 3 ? l[3] : l[4];
+    for (int s = s0; s < s1; s += DEEP) {
 #pragma unroll
       for (int k = 0; k < DEEP; ++k) {
+        const int word = (s + k) >> 5;
+        const float lw = word == 0 ? l[0] : word == 1 ? l[1] : word == 2 ? l[2] : word == 3 ? l[3] : l[4];
         const float w = __shfl_sync(0xffffffffu, lw, (s + k) & 31);
-        if (s + k < S) {
+        if (s + k < s1) {
           o.x += w * v[k].x;
           o.y += w * v[k].y;
           o.z += w * v[k].z;
           o.w += w * v[k].w;
-          if (s + DEEP + k < S) v[k] = src[slot_of(s + DEEP + k) * 128];
+          if (s + DEEP + k < s1) v[k] = src[slot_of(s + DEEP + k) * 128];
         }
       }
+    }
+    if (shared) {   // (the same in the whole CTA)
+      if (warp > 0) acc[warp - 1][lane] = o;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const float4 y = acc[q][lane];
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
+        }
+      }
+      __syncthreads();
+      if (warp > 0) continue;
     }
     reinterpret_cast<uint2*>(a.out + ((int64_t)cut.request * a.H + row) * 512 + (c & 3) * 128)[lane] =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));

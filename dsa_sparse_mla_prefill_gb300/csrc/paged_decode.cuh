@@ -1096,8 +1096,9 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
 static inline int launch_join(const DecodeArgs& a, int padded, int max_tiles, bool tree, cudaStream_t stream) {
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
   if (tree) {
-    // two pieces a warp where a request is cut once, about one where it is cut as often as the batch's mean
-    const int64_t mean = 2ll * a.H * a.B / a.groups, most = a.H / 2;
+    // about a piece for each warp, or CTA (see the kernel), where the batch's requests are cut
+    // equally often; at most two a warp where one is cut once
+    const int64_t cuts = (a.groups + a.B - 1) / a.B, mean = 4ll * a.H / (cuts > 8 ? cuts : 4 * cuts), most = a.H / 2;
     const int64_t y = mean < most ? mean : most;
     return launch_after(tree_join_kernel<8>, dim3((unsigned)(a.groups - 1), (unsigned)(y < 4 ? 4 : y)), NT_JOIN, 0, stream, a, padded);
   }

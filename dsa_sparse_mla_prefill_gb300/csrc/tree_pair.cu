@@ -207,6 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == W_Q && lane < 3) {
+    const CUtensorMap* map = lane == 0 ? &a.tmap_q : lane == 1 ? &a.tmap_kv : &a.tmap_box;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   if (warp == W_QK) {
     tmem_alloc_pair(const_cast<uint32_t*>(tmem_base_ptr), 512);
     tmem_relinquish_pair();
@@ -236,8 +240,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       const uint32_t x0 = (uint32_t)range < ng ? range_begin(range, total, ng) : 0;
       const int nt = (uint32_t)range < ng ? (int)(range_begin(range + 1, total, ng) - x0) : 0;
       if (lane == 0) {
-        *plan = nt;
-        mbar_arrive(&bars[B_PLAN]);
         if (range == 0 && counts) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
         if (counts) a.borders[1 + range] = make_int4(0, 0, 0, 0);
       }
@@ -257,8 +259,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       b = __shfl_sync(0xffffffffu, b, holder & 31);
       j = __shfl_sync(0xffffffffu, j, holder & 31);
       len = __shfl_sync(0xffffffffu, len, holder & 31);
+      if (lane == 0) {
+        plan[0] = nt;
+        plan[1] = b;
+        mbar_arrive(&bars[B_PLAN]);
+      }
       int bad = 0, seg = 0, drafted = 0, context = 0;
-      uint64_t seen = 0;
+      uint64_t seen = 0;   // drafted tokens that any token sees (worked out at the first tile that holds one)
+      bool looked = false;
       const bool from_start = j == 0;
       bool enter = true;
       int fetch = -1;   // first row of a box to fetch to L2
@@ -281,15 +289,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
           n = tiles_of(a, len);
           drafted = drafted_of(a, b);
           context = len - drafted;
-          uint64_t any = 0;
-          for (int i = lane; i < drafted; i += 32) any |= a.tree_mask[(int64_t)b * a.n + i];
-          seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
+          looked = false;
           if (len > a.cap) {
             if (j == 0 && lane == 0) ++bad;
             len = a.cap;
           }
         }
         if (!doze(B_IDXE + r, ((it / NI) & 1) ^ 1)) break;
+        if (!looked && (j + 1) * TK > context) {
+          uint64_t any = 0;
+          for (int i = lane; i < drafted; i += 32) any |= a.tree_mask[(int64_t)b * a.n + i];
+          seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
+          looked = true;
+        }
         const int32_t* bt = a.block_table + (int64_t)b * a.max_blocks;
         int32_t row[8];
         const uint32_t e0 = (uint32_t)j * TK + 8 * lane;
@@ -342,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       }
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && counts) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
-    } else if (const int nt = doze(B_PLAN, 0) ? *plan : 0; warp >= W_LOAD && warp < W_LOAD + NSLOT) {
+    } else if (const int nt = poll(B_PLAN, 0) ? plan[0] : 0; warp >= W_LOAD && warp < W_LOAD + NSLOT) {
       // ----------------------------------------------------------------
       // loads, a warp per slot of the K and the V ring.  A slot is two halves of 64 rows x 64
       // columns: of K the two halves of this CTA's 128 keys, of V (64 keys) its two 64-column
@@ -403,18 +415,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       // ----------------------------------------------------------------
       const uint32_t full0 = map_peer(bar(B_QF), 0);
       int nq = 0;
+      auto load_q = [&](int b) {
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars[B_QF], 2u * NC * Q_CHUNK);
+        __syncwarp();
+        if (lane < NC) tma_load_2d_pair(sbase + OFF_Q + lane * Q_CHUNK, &a.tmap_q, lane * 64, b * a.H + row0, full0);
+        ++nq;
+      };
+      if (nt > 0) load_q(plan[1]);   // (the first request's, while the scheduler looks up its rows)
       for (int it = 0; it < nt; ++it) {
         const int r = it % NI;
         if (!doze(B_IDXF + r, (it / NI) & 1)) break;
         const int4 mt = meta[r];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
-        if (!(mt.y & F_FIRST)) continue;
+        if (it == 0 || !(mt.y & F_FIRST)) continue;
         if (!doze(B_QE, (nq & 1) ^ 1)) break;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars[B_QF], 2u * NC * Q_CHUNK);
-        __syncwarp();
-        if (lane < NC) tma_load_2d_pair(sbase + OFF_Q + lane * Q_CHUNK, &a.tmap_q, lane * 64, mt.x * a.H + row0, full0);
-        ++nq;
+        load_q(mt.x);
       }
       const int mine = min(a.H - row0, ROWS);
       for (int b = range; b < a.B; b += a.groups) {
@@ -547,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     int4 done = make_int4(0, 0, 0, 0);
     float m_done = 0.f, l_done = 0.f;
     int seg = 0;
-    auto epilogue = [&]() -> bool {
+    auto epilogue = [&](int buffer) -> bool {
       sums[part * ROWS + row] = l_done;
       if (!group()) return false;
       const bool live = token < done.w;   // (a padding token's row is zeros)
@@ -565,10 +581,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (!poll(B_OF, seg & 1)) return false;
       ++seg;
       tc_fence_after();
-      // output columns 256 wg + 128 half .. +127 of this row
-      const int col = 256 * wg + 128 * half;
-      uint4* out = reinterpret_cast<uint4*>(a.out + ((int64_t)done.x * a.H + q_row) * 512 + col);
-      float4* po = reinterpret_cast<float4*>(a.part_o + slot_row * 512 + col);
+      // Output columns 256 wg + 128 half .. +127 of the warp's 32 rows, 32 at a time, turned in
+      // shared memory (the buffer of the P that the last P.V has read) so that a store fills
+      // whole 128-byte (parts) or 64-byte pieces of rows: a thread storing its own row in 16-byte
+      // pieces takes 8000 cycles for it.
+      const int col = 256 * wg + 128 * half, first_row = row0 + 32 * rg;
+      const uint32_t stage = sbase + OFF_P + (uint32_t)buffer * P_BYTES + (uint32_t)warp * 4096u;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float o[32];
@@ -581,22 +599,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = inv != 0.f ? o[i] * inv : 0.f;
-        if (there) {
-          if (is_part) {
+        __syncwarp();   // (the pieces before are read)
+        if (is_part) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) po[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else {
+          for (int i = 0; i < 8; ++i)
+            sts128(stage + lane * 128u + (((uint32_t)i ^ (lane & 7u)) << 4), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                   __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              out[c / 8 + i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3), at = lane & 7;
+            const uint4 x = lds128(stage + rr * 128u + (uint32_t)((at ^ (rr & 7)) << 4));
+            if (first_row + rr < a.H)
+              *reinterpret_cast<uint4*>(a.part_o + (slot_row - q_row + first_row + rr) * 512 + col + c + 4 * at) = x;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts128(stage + lane * 64u + (((uint32_t)i ^ ((lane >> 1) & 3u)) << 4), pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                   pack_bf16x2(o[8 * i + 2], o[8 * i + 3]), pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                   pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), at = lane & 3;
+            const uint4 x = lds128(stage + rr * 64u + (uint32_t)((at ^ ((rr >> 1) & 3)) << 4));
+            if (first_row + rr < a.H)
+              *reinterpret_cast<uint4*>(a.out + ((int64_t)done.x * a.H + first_row + rr) * 512 + col + c + 8 * at) = x;
           }
         }
       }
+      __syncwarp();
       return true;
     };
     wait_for_previous();
-    const int nt = poll(B_PLAN, 0) ? *plan : 0;
+    const int nt = poll(B_PLAN, 0) ? plan[0] : 0;
 #pragma unroll 1
     for (int it = 0; it < nt; ++it) {
       const int r = it % NI, sb = it & 1;
@@ -694,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
       // a request's outputs are stored once the next one's first P is
       if (pending) {
-        if (!epilogue()) break;
+        if (!epilogue(sb ^ 1)) break;
         pending = false;
       }
       if (mt.y & F_LAST) {
@@ -704,7 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         l_done = l_run;
       }
     }
-    if (pending) epilogue();
+    if (pending) epilogue((nt & 1) ^ 1);
   }
 
   __syncwarp();
