@@ -157,86 +157,93 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ D
   }
 }
 
-// The tree form's join, of up to thousands of query rows: a warp takes 128 columns of a row, all
-// parts of it, eight loads at a time, or where there are more than eight parts the CTA's four
-// warps a fourth of them each; the borders inside a request share its rows.  (8 requests of 512
-// rows in 19 ranges, 38 MB of parts: 16 us cold against 21 with the kernel above, whose CTAs
-// take a row after the other.)
+// The tree form's join, of up to thousands of query rows: a warp takes a row, all parts of it
+// DEEP at a time, or where there are more than eight parts the CTA's four warps a fourth of them
+// each; the borders inside a request share its rows.  (A warp per 128 columns, with the kernel
+// above's way to the weights, was bound by its 540 instructions a piece: 8 requests of 512 rows in
+// 19 ranges 17 us, and 21 with that kernel.)
 template <int DEEP>
 __global__ void __launch_bounds__(NT_JOIN) tree_join_kernel(const __grid_constant__ DecodeArgs a, int rows_padded) {
-  __shared__ float4 acc[3][32];
+  __shared__ float4 acc[3][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   wait_for_previous();
   Border cut;
   if (!border_of(reinterpret_cast<const uint2*>(a.borders)[0], a.borders[1 + blockIdx.x], blockIdx.x, a.B, a.groups, cut)) return;
   const int S = cut.parts, nb = S - 1, rank = (int)blockIdx.x - cut.first;
-  const int64_t pitch = rows_padded;
-  const int64_t first_slot = (2 * cut.first + (cut.whole_start ? 0 : 1)) * pitch;
-  auto slot_of = [&](int s) { return s == 0 ? first_slot : 2ll * (cut.first + s) * pitch; };
-  const int pieces = 4 * a.H;
-  const int c0 = (int)((int64_t)pieces * rank / nb), c1 = (int)((int64_t)pieces * (rank + 1) / nb);
-  const bool shared = S > DEEP;                      // a piece by the whole CTA
+  const uint32_t pitch = (uint32_t)rows_padded;      // (rows of all slots are below 2^23)
+  const uint32_t first_slot = (uint32_t)(2 * cut.first + (cut.whole_start ? 0 : 1)) * pitch;
+  auto slot_of = [&](int s) { return s == 0 ? first_slot : (uint32_t)(2 * (cut.first + s)) * pitch; };
+  const int r0 = (int)((int64_t)a.H * rank / nb), r1 = (int)((int64_t)a.H * (rank + 1) / nb);
+  const bool shared = S > 8;                         // a row by the whole CTA
   const int s0 = shared ? S * warp / 4 : 0, s1 = shared ? S * (warp + 1) / 4 : S;
   const int step = (int)gridDim.y * (shared ? 1 : NT_JOIN / 32);
 #pragma unroll 1
-  for (int c = c0 + (shared ? (int)blockIdx.y : (int)blockIdx.y * (NT_JOIN / 32) + warp); c < c1; c += step) {
-    const int row = c >> 2;
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (int64_t)row * 128 + (c & 3) * 32 + lane;
-    float4 v[DEEP];
-#pragma unroll
-    for (int k = 0; k < DEEP; ++k) v[k] = s0 + k < s1 ? src[slot_of(s0 + k) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
-    float l[LSE], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < LSE; ++k) l[k] = lane + 32 * k < S ? a.part_lse[slot_of(lane + 32 * k) + row] : -INFINITY;
-#pragma unroll
-    for (int k = 0; k < LSE; ++k) m = fmaxf(m, l[k]);
+  for (int row = r0 + (shared ? (int)blockIdx.y : (int)blockIdx.y * (NT_JOIN / 32) + warp); row < r1; row += step) {
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (uint64_t)row * 128 + lane;
+    const float* lse = a.part_lse + row;
+    // weights of the parts: lane s has part s's; those from 32 on are worked out as they come
+    const float l = lane < S ? lse[slot_of(lane)] : -INFINITY;
+    float m = l;
+    for (int s = 32 + lane; s < S; s += 32) m = fmaxf(m, lse[slot_of(s)]);
     m = warp_max(m);
     const float mr = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int k = 0; k < LSE; ++k) {
-      l[k] = exp2f(l[k] - mr);
-      sum += l[k];
-    }
+    const float w = exp2f(l - mr);
+    float sum = w;
+    for (int s = 32 + lane; s < S; s += 32) sum += exp2f(lse[slot_of(s)] - mr);
     sum = warp_sum(sum);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int s = s0; s < s1; s += DEEP) {
+      float4 v[DEEP][4];
+      float ws[DEEP];
 #pragma unroll
       for (int k = 0; k < DEEP; ++k) {
-        const int word = (s + k) >> 5;
-        const float lw = word == 0 ? l[0] : word == 1 ? l[1] : word == 2 ? l[2] : word == 3 ? l[3] : l[4];
-        const float w = __shfl_sync(0xffffffffu, lw, (s + k) & 31);
-        if (s + k < s1) {
-          o.x += w * v[k].x;
-          o.y += w * v[k].y;
-          o.z += w * v[k].z;
-          o.w += w * v[k].w;
-          if (s + DEEP + k < s1) v[k] = src[slot_of(s + DEEP + k) * 128];
+        const int at = min(s + k, s1 - 1);
+        const float4* from = src + (uint64_t)slot_of(at) * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[k][q] = from[32 * q];
+        ws[k] = at < 32 ? __shfl_sync(0xffffffffu, w, at) : exp2f(lse[slot_of(at)] - mr);
+        if (s + k >= s1) ws[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          fma2(o[q].x, o[q].y, v[k][q].x, v[k][q].y, ws[k], ws[k]);
+          fma2(o[q].z, o[q].w, v[k][q].z, v[k][q].w, ws[k], ws[k]);
         }
       }
     }
     if (shared) {   // (the same in the whole CTA)
-      if (warp > 0) acc[warp - 1][lane] = o;
+      if (warp > 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[warp - 1][32 * q + lane] = o[q];
+      }
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          const float4 y = acc[q][lane];
-          o.x += y.x;
-          o.y += y.y;
-          o.z += y.z;
-          o.w += y.w;
+        for (int p = 0; p < 3; ++p) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 y = acc[p][32 * q + lane];
+            o[q].x += y.x;
+            o[q].y += y.y;
+            o[q].z += y.z;
+            o[q].w += y.w;
+          }
         }
       }
       __syncthreads();
       if (warp > 0) continue;
     }
-    reinterpret_cast<uint2*>(a.out + ((int64_t)cut.request * a.H + row) * 512 + (c & 3) * 128)[lane] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if ((c & 3) == 0 && lane == 0)
-      a.lse[(int64_t)cut.request * a.H + row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    uint2* out = reinterpret_cast<uint2*>(a.out + ((int64_t)cut.request * a.H + row) * 512) + lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) out[32 * q] = make_uint2(pack_bf16x2(o[q].x * inv, o[q].y * inv), pack_bf16x2(o[q].z * inv, o[q].w * inv));
+    if (lane == 0) a.lse[(int64_t)cut.request * a.H + row] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }
 }
 

@@ -851,6 +851,7 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;
+  if (a.box_rows && form.ctas == 2 && !dsa::make_tile_map(&a.tmap_box8, cache, N, ld_kv, ld_kv, 8)) return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, form.rows / form.ctas)) return DSA_ERR_CUDA;
   const int r = form.ctas == 2 ? dsa::launch_tree_pair(a, d_rope, (int)max_tiles, (cudaStream_t)stream)
                 : tree         ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)

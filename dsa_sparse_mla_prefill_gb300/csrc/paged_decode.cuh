@@ -1096,11 +1096,12 @@ static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
 static inline int launch_join(const DecodeArgs& a, int padded, int max_tiles, bool tree, cudaStream_t stream) {
   if (max_tiles <= 1 || a.groups <= 1) return 0;   // no request can be cut
   if (tree) {
-    // about a piece for each warp, or CTA (see the kernel), where the batch's requests are cut
-    // equally often; at most two a warp where one is cut once
-    const int64_t cuts = (a.groups + a.B - 1) / a.B, mean = 4ll * a.H / (cuts > 8 ? cuts : 4 * cuts), most = a.H / 2;
-    const int64_t y = mean < most ? mean : most;
-    return launch_after(tree_join_kernel<8>, dim3((unsigned)(a.groups - 1), (unsigned)(y < 4 ? 4 : y)), NT_JOIN, 0, stream, a, padded);
+    // about a row for each warp, or CTA (see the kernel), where the batch's requests are cut
+    // equally often
+    const int64_t cuts = (a.groups + a.B - 1) / a.B, y = a.H / (cuts > 8 ? cuts : 4 * cuts) + 1;
+    const dim3 grid((unsigned)(a.groups - 1), (unsigned)y);
+    return cuts > 8 ? launch_after(tree_join_kernel<5>, grid, NT_JOIN, 0, stream, a, padded)
+                    : launch_after(tree_join_kernel<2>, grid, NT_JOIN, 0, stream, a, padded);
   }
   const dim3 grid((unsigned)(a.groups - 1), (unsigned)(JOIN_Y * a.head_blocks));
   return a.groups > 20 * a.B ? launch_after(join_kernel<10>, grid, NT_JOIN, 0, stream, a, padded)

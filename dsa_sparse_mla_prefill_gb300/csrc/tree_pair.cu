@@ -154,10 +154,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void gather_half(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, const int32_t* rows,
-                                            uint32_t bar, uint64_t policy) {
-#pragma unroll 4
-  for (int n = 0; n < 16; ++n) {
+// (n gathers of four rows x 128 bytes, issued by one elected lane)
+__device__ __forceinline__ void gather(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, const int32_t* rows,
+                                       int count, uint32_t bar, uint64_t policy) {
+#pragma unroll 2
+  for (int n = 0; n < count; ++n) {
     const int4 r = *reinterpret_cast<const int4*>(rows + 4 * n);
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
@@ -328,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
                        : "memory");
         if (a.fetch_bytes) {
           fetch = rows[r * TK + (lane & (TK / a.box_rows - 1)) * a.box_rows];   // of box `lane`
-          if (!all || lane >= TK / a.box_rows || lane % sharers != share) fetch = -1;
+          if (lane >= TK / a.box_rows || lane % sharers != share || fetch > a.N - a.box_rows) fetch = -1;
         }
         const bool first = enter, last = (it == nt - 1) || (j == n - 1);
         if (lane == 0) {
@@ -394,9 +395,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
           if (box) {
             if (h < 2)
               load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
+          } else if (a.box_rows > 0) {
+            // where keys are missing: a lane per eight rows, which are there, or none of them
+            // (read from behind the cache, as zeros), or some: gathered
+            const int g = lane >> 3 & 1, at8 = (lane & 7) * 8, first = ra + g * rstep + at8;
+            const uint32_t in = reinterpret_cast<const uint8_t*>(valid + 4 * r)[first >> 3];
+            uint32_t left = __ballot_sync(0xffffffffu, lane < 16 && in != 0 && in != 0xffu);
+            if (lane < 16 && (in == 0 || in == 0xffu))
+              load_box(dst + g * HALF_BYTES + at8 * 128, &a.tmap_box8, ca + g * cstep, in ? tile_rows[first] : a.N, full0, policy);
+            for (; left; left &= left - 1) {
+              const int l = __ffs(left) - 1, lg = l >> 3, lat = (l & 7) * 8;
+              gather(leader, dst + lg * HALF_BYTES + lat * 128, &a.tmap_kv, ca + lg * cstep, tile_rows + ra + lg * rstep + lat, 2,
+                     full0, policy);
+            }
           } else {
-            gather_half(leader, dst, &a.tmap_kv, ca, tile_rows + ra, full0, policy);
-            gather_half(leader, dst + HALF_BYTES, &a.tmap_kv, ca + cstep, tile_rows + ra + rstep, full0, policy);
+            gather(leader, dst, &a.tmap_kv, ca, tile_rows + ra, ROWS / 4, full0, policy);
+            gather(leader, dst + HALF_BYTES, &a.tmap_kv, ca + cstep, tile_rows + ra + rstep, ROWS / 4, full0, policy);
           }
         }
         __syncwarp();
