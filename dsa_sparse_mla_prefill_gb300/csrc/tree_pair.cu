@@ -396,13 +396,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
             if (h < 2)
               load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
           } else if (a.box_rows > 0) {
-            // where keys are missing: a lane per eight rows, which are there, or none of them
-            // (read from behind the cache, as zeros), or some: gathered
-            const int g = lane >> 3 & 1, at8 = (lane & 7) * 8, first = ra + g * rstep + at8;
-            const uint32_t in = reinterpret_cast<const uint8_t*>(valid + 4 * r)[first >> 3];
+            // where keys are missing: a half that is there, or none of it (read from behind the
+            // cache, as zeros), by its boxes; the others by a lane per eight rows, gathered
+            // where some of the eight are missing
+            const int g = lane >> 3 & 1, i = lane & 7, half_row = ra + g * rstep;
+            const uint64_t in64 = valid[4 * r + (half_row >> 6)];
+            const uint32_t in = (uint32_t)(in64 >> (8 * i)) & 0xffu;
+            const uint32_t half_dst = dst + g * HALF_BYTES;
+            const bool whole = in64 == 0 || in64 == ~0ull;
             uint32_t left = __ballot_sync(0xffffffffu, lane < 16 && in != 0 && in != 0xffu);
-            if (lane < 16 && (in == 0 || in == 0xffu))
-              load_box(dst + g * HALF_BYTES + at8 * 128, &a.tmap_box8, ca + g * cstep, in ? tile_rows[first] : a.N, full0, policy);
+            if (lane < 16) {
+              if (whole) {
+                if (i < per_half)
+                  load_box(half_dst + i * a.box_rows * 128, &a.tmap_box, ca + g * cstep, in64 ? tile_rows[half_row + i * a.box_rows] : a.N,
+                           full0, policy);
+              } else if (in == 0 || in == 0xffu) {
+                load_box(half_dst + i * 1024, &a.tmap_box8, ca + g * cstep, in ? tile_rows[half_row + 8 * i] : a.N, full0, policy);
+              }
+            }
             for (; left; left &= left - 1) {
               const int l = __ffs(left) - 1, lg = l >> 3, lat = (l & 7) * 8;
               gather(leader, dst + lg * HALF_BYTES + lat * 128, &a.tmap_kv, ca + lg * cstep, tile_rows + ra + lg * rstep + lat, 2,
@@ -443,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
         if (it == 0 || !(mt.y & F_FIRST)) continue;
-        if (!doze(B_QE, (nq & 1) ^ 1)) break;
+        if (!poll(B_QE, (nq & 1) ^ 1)) break;
         load_q(mt.x);
       }
       const int mine = min(a.H - row0, ROWS);
