@@ -34,6 +34,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import numpy as np
@@ -846,61 +847,76 @@ def dsa_paged_decode(q, cache, block_table, kv_lens, block_size: int, scale: flo
 # ---------------------------------------------------------------------------
 # norms in front of the rotation
 # ---------------------------------------------------------------------------
-def _norm_side(x, weight, name, d_norm, like):
-    """Checks of queries or keys and their weight; `like` = (dtype, device, T, d, weight dtype) of the other side."""
+def _norm_rows(x, weight, name, d_norm):
+    """(dtype, device, T, H, d, weight dtype) of queries or keys, checked with their weight."""
     torch = _torch
-    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a bf16 or fp32 tensor")
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"{name} must be a bf16 or fp32 tensor")
     dev = x.get_device()
-    if dev < 0 or x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1 and x.numel():
-        raise ValueError(f"{name} must be a 3-D CUDA tensor with unit stride in its last dimension")
+    if dev < 0 or x.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D CUDA tensor")
     T, H, d = x.shape
     if T > 0x7fffffff or H > 0x7fffffff:   # (the library counts them in 32 bits)
         raise DSAError(DSA_ERR_UNSUPPORTED, "dsa_qk_norm_rope")
-    if not isinstance(weight, torch.Tensor) or weight.dtype is not torch.bfloat16 and weight.dtype is not torch.float32:
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError(f"{name}'s weight must be a bf16 or fp32 tensor")
+    w_dtype = weight.dtype
+    if w_dtype is not torch.bfloat16 and w_dtype is not torch.float32:
         raise TypeError(f"{name}'s weight must be a bf16 or fp32 tensor")
     if d_norm is None:
         d_norm = d
-    if not 1 <= d_norm <= d:
+    elif not 1 <= d_norm <= d:
         raise ValueError("d_norm must be between 1 and the columns of a head")
     if weight.dim() != 1 or weight.shape[0] != d_norm or weight.get_device() != dev or not weight.is_contiguous():
         raise ValueError(f"{name}'s weight must be a contiguous [d_norm] tensor on its device")
-    mine = (x.dtype, dev, T, d, weight.dtype)
-    if like is not None and mine != like:
-        raise ValueError("q and k must have the same tokens, columns, dtype and device, and weights of one dtype")
-    return mine, d_norm
+    return dtype, dev, T, H, d, w_dtype
 
 
 def _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm):
-    """Checks shared by the norm and its gradient; (device, dtype flag, weight dtype flag, T, d, d_norm, positions pointer)."""
+    """Checks shared by the norm and its gradient; (device, dtype flag, weight dtype flag, T, d, d_norm, positions pointer, Hq,
+    Hk)."""
     torch = _torch or _load_torch()
-    if q is None and k is None:
-        raise ValueError("q or k is needed")
     if freqs is not None and not isinstance(freqs, RopeFreqs):
         raise TypeError("freqs must come from dsa_rope_freqs")
-    like, n = None, d_norm
+    Hq = Hk = 0
     if q is not None:
-        like, n = _norm_side(q, q_weight, "q", d_norm, None)
-    if k is not None:
-        like, n = _norm_side(k, k_weight, "k", d_norm, like)
-    dtype, dev, T, d, w_dtype = like
+        dtype, dev, T, Hq, d, w_dtype = _norm_rows(q, q_weight, "q", d_norm)
+        if k is not None:
+            k_dtype, k_dev, k_T, Hk, k_d, kw_dtype = _norm_rows(k, k_weight, "k", d_norm)
+            if k_dtype is not dtype or k_dev != dev or k_T != T or k_d != d or kw_dtype is not w_dtype:
+                raise ValueError("q and k must have the same tokens, columns, dtype and device, and weights of one dtype")
+    elif k is not None:
+        dtype, dev, T, Hk, d, w_dtype = _norm_rows(k, k_weight, "k", d_norm)
+    else:
+        raise ValueError("q or k is needed")
+    pos = None
     if freqs is not None:
         if freqs.d_rope > d:
             raise ValueError("freqs have more columns than a head")
         _int_tensor(positions, "positions", 1, dev)
         if positions.shape[0] != T:
             raise ValueError("positions must have one entry per token")
+        pos = positions.data_ptr()
     f32 = torch.float32
-    return dev, int(dtype is f32), int(w_dtype is f32), T, d, n, None if freqs is None else positions.data_ptr()
+    return dev, 1 if dtype is f32 else 0, 1 if w_dtype is f32 else 0, T, d, d if d_norm is None else d_norm, pos, Hq, Hk
 
 
-def _rows_like(t, x, name, dev):
-    """t, a tensor of x's shape and dtype with unit last stride."""
-    if not isinstance(t, _torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != dev:
+def _rows_like(t, x, name):
+    """t, a tensor of x's shape, dtype and device."""
+    if not isinstance(t, _torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.device != x.device:
         raise ValueError(f"{name} must have the shape, dtype and device of what it belongs to")
-    if t.stride(2) != 1 and t.shape[2] != 1 and t.numel():
-        raise ValueError(f"{name} must have unit stride in its last dimension")
     return t
+
+
+def _row_strides(t, name):
+    """Strides of tokens and heads of a tensor whose rows are contiguous."""
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] != 1 and t.numel():
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return s
 
 
 def dsa_qk_norm_rope(q, k, q_weight, k_weight, positions, freqs: RopeFreqs = None, eps: float = 1e-6,
@@ -913,23 +929,27 @@ def dsa_qk_norm_rope(q, k, q_weight, k_weight, positions, freqs: RopeFreqs = Non
     q_out, k_out: tensors or views of the same shapes (q and k themselves for in place); new contiguous
     ones if None.  Returns (q_out, k_out), None for a side that is not there.  Autograd does not see the
     call: see dsa_qk_norm_rope_gradient."""
-    dev, f32, w_f32, T, d, n, pos = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
-    args = []
-    outs = []
-    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name} without its input")
-            args += [None, 0, 0, None, 0, 0, 0]
-        else:
-            out = _empty(x.shape, x.dtype, x.device, stream) if out is None else _rows_like(out, x, name, dev)
-            xs, ys = x.stride(), out.stride()
-            args += [x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], x.shape[1]]
-        outs.append(out)
+    dev, f32, w_f32, T, d, n, pos, Hq, Hk = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
+    q_ptr = qo_ptr = qw_ptr = k_ptr = ko_ptr = kw_ptr = None
+    qs = qos = ks = kos = (0, 0)
+    if q is not None:
+        qs = _row_strides(q, "q")
+        q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else _rows_like(q_out, q, "q_out")
+        qos = _row_strides(q_out, "q_out")
+        q_ptr, qo_ptr, qw_ptr = q.data_ptr(), q_out.data_ptr(), q_weight.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without its input")
+    if k is not None:
+        ks = _row_strides(k, "k")
+        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else _rows_like(k_out, k, "k_out")
+        kos = _row_strides(k_out, "k_out")
+        k_ptr, ko_ptr, kw_ptr = k.data_ptr(), k_out.data_ptr(), k_weight.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without its input")
     _queue(lib().dsa_qk_norm_rope, "dsa_qk_norm_rope",
-           (*args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32, pos, T,
-            d, n, float(eps), freqs), dev, stream)
-    return tuple(outs)
+           (q_ptr, qs[0], qs[1], qo_ptr, qos[0], qos[1], Hq, k_ptr, ks[0], ks[1], ko_ptr, kos[0], kos[1], Hk, f32, qw_ptr, kw_ptr,
+            w_f32, pos, T, d, n, eps, freqs), dev, stream)
+    return q_out, k_out
 
 
 @functools.lru_cache(maxsize=64)
@@ -949,33 +969,31 @@ def dsa_qk_norm_rope_gradient(q_grad, k_grad, q, k, q_weight, k_weight, position
     dtype, the weights' in fp32; None for a side that is not there.  workspace: a CUDA uint8 tensor of
     dsa_qk_norm_rope_gradient_workspace(d_norm) bytes (calls sharing one must not overlap on the GPU);
     one per call if None."""
-    dev, f32, w_f32, T, d, n, pos = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
+    dev, f32, w_f32, T, d, n, pos, Hq, Hk = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
     torch = _torch
     device = (k if q is None else q).device
     args, outs, weights = [], [], []
-    for x, g, name in ((q, q_grad, "q_grad"), (k, k_grad, "k_grad")):
+    for x, g, name, H in ((q, q_grad, "q", Hq), (k, k_grad, "k", Hk)):
         if x is None:
             if g is not None:
-                raise ValueError(f"{name} without its input")
-            args += [None, 0, 0, None, 0, 0, None, 0]
+                raise ValueError(f"{name}_grad without its input")
+            args += (None, 0, 0, None, 0, 0, None, 0)
             outs.append(None)
             weights.append(None)
             continue
-        _rows_like(g, x, name, dev)
+        gs, xs = _row_strides(_rows_like(g, x, name + "_grad"), name + "_grad"), _row_strides(x, name)
         out = _empty(x.shape, x.dtype, device, stream)
-        gs, xs = g.stride(), x.stride()
-        args += [g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), x.shape[1]]
+        args += (g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), H)
         outs.append(out)
         # (no rows: the library leaves the sums alone)
-        weights.append(_empty((n,), torch.float32, device, stream) if x.shape[1] else
-                       torch.zeros(n, dtype=torch.float32, device=device))
+        weights.append(_empty((n,), torch.float32, device, stream) if H else torch.zeros(n, dtype=torch.float32, device=device))
     if workspace is None:
         workspace = _empty((dsa_qk_norm_rope_gradient_workspace(n),), torch.uint8, device, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _queue(lib().dsa_qk_norm_rope_gradient, "dsa_qk_norm_rope_gradient",
            (*args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32, pos, T,
-            d, n, float(eps), freqs, *(None if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
+            d, n, eps, freqs, *(None if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
             workspace.numel()), dev, stream)
     return (*outs, *weights)
 
@@ -984,6 +1002,7 @@ def dsa_qk_norm_rope_gradient(q_grad, k_grad, q, k, q_weight, k_weight, position
 # checking drafted tokens
 # ---------------------------------------------------------------------------
 TREE_MAX_TOKENS, TREE_MAX_ROWS, MAX_CACHES = 64, 2048, 128
+_DTYPE, _SHAPE = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1074,12 +1093,12 @@ def dsa_kv_keep(caches, block_table, kv_lens, keep, block_size: int, n: int, num
     dev, shape, dtype = first.get_device(), first.shape, first.dtype
     if dev < 0 or len(shape) != 2:
         raise ValueError("caches must be 2-D CUDA tensors")
-    pointers = (_VP * len(caches))()
-    for i, c in enumerate(caches):
-        if not isinstance(c, torch.Tensor) or c.dtype is not dtype or c.shape != shape or c.get_device() != dev or \
-                not c.is_contiguous():
-            raise ValueError("caches must be contiguous tensors of one shape and dtype on one device")
-        pointers[i] = c.data_ptr()
+    # (by maps: a model has dozens of them, and a loop over their attributes costs the host more than the call)
+    Tensor, n_caches = torch.Tensor, len(caches)
+    pointers = (_VP * n_caches)(*map(Tensor.data_ptr, caches))
+    if n_caches > 1 and (set(map(_DTYPE, caches)) != {dtype} or set(map(_SHAPE, caches)) != {shape} or
+                         set(map(Tensor.get_device, caches)) != {dev}) or not all(map(Tensor.is_contiguous, caches)):
+        raise ValueError("caches must be contiguous tensors of one shape and dtype on one device")
     _int_tensor(block_table, "block_table", 2, dev)
     _int_tensor(kv_lens, "kv_lens", 1, dev)
     _int_tensor(keep, "keep", 2, dev)
@@ -1099,7 +1118,7 @@ def dsa_kv_keep(caches, block_table, kv_lens, keep, block_size: int, n: int, num
         if new_lens.shape[0] != B:
             raise ValueError("new_lens must have one entry per request")
     _queue(lib().dsa_kv_keep, "dsa_kv_keep",
-           (pointers, len(caches), shape[1] * first.element_size(), shape[0], block_table.data_ptr(), block_table.shape[1],
+           (pointers, n_caches, shape[1] * (2 if dtype is torch.bfloat16 else 1), shape[0], block_table.data_ptr(), block_table.shape[1],
             int(block_size), kv_lens.data_ptr(), draft_ptr, int(n), keep.data_ptr(), keep.shape[1], B,
             new_lens.data_ptr()), dev, stream)
     return new_lens

@@ -43,7 +43,7 @@ using decode::warp_scan;
 constexpr int TK = 256;              // keys of a tile
 constexpr int ROWS = 64;             // query rows of a CTA
 constexpr int NI = 4;                // tiles of rows ahead
-constexpr int NK = 3, NV = 2;        // ring slots
+constexpr int NK = 4, NV = 3;        // ring slots
 constexpr int NSLOT = NK + NV;
 constexpr float kTau = 8.0f;         // lazy-rescale threshold (log2 units)
 constexpr uint16_t kBoth = 3;
@@ -58,14 +58,13 @@ constexpr uint32_t P_COLUMN = ROWS * 128u;         // 64 rows x 64 keys
 constexpr uint32_t OFF_RING = 0;
 constexpr uint32_t OFF_Q = OFF_RING + NSLOT * SLOT_BYTES;
 constexpr uint32_t OFF_P = OFF_Q + 9 * Q_CHUNK;
-constexpr uint32_t P_BYTES = 4 * P_COLUMN;
-constexpr uint32_t OFF_ROWS = OFF_P + 2 * P_BYTES;
+constexpr uint32_t OFF_ROWS = OFF_P + 4 * P_COLUMN;
 constexpr uint32_t OFF_META = OFF_ROWS + NI * TK * 4u;
 constexpr uint32_t OFF_VALID = OFF_META + NI * 16u;
 constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums
 constexpr uint32_t OFF_BAR = OFF_RED + 3u * 4u * ROWS * 4u;
-constexpr int NBAR = 48;
-constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8u;
+constexpr int NBAR = 53;
+constexpr uint32_t OFF_MISC = OFF_BAR + (NBAR + 1) / 2 * 16u;
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 64u + 1024u;
 static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
 constexpr uint32_t COL_O = 0, COL_S = 256;
@@ -77,21 +76,30 @@ enum {
   B_QE = 17,
   B_SF = 18,        // [2] one commit
   B_SE = 20,        // [2] even CTA: 16 softmax warps of the pair
-  B_PF = 22,        // [2] this CTA's 8 softmax warps: its rows of P are stored
-  B_PR = 24,        // [2] even CTA: the odd one's are (relayed)
-  B_PE = 26,        // [2] one commit: the P.V that reads this P is done
-  B_OF = 28,
-  B_OE = 29,        // even CTA: 16 warps of the pair
-  B_IDXF = 30,      // [NI]
-  B_IDXE = 34,      // [NI] the loaders, Q, softmax and (even CTA) issuing warps
-  B_GRP = 38,       // [2] the four warps of 32 query rows
-  B_PLAN = 40,
-  B_DRAIN = 41,     // [2] one per issuer
+  B_PF = 22,        // [4] per 64 keys: this CTA's two softmax warps have stored its rows of P
+  B_PR = 26,        // [4] even CTA: the odd one's have (relayed)
+  B_PE = 30,        // [4] one commit: the MMAs that read these columns of P are done
+  B_OF = 34,
+  B_OE = 35,        // even CTA: 16 warps of the pair
+  B_IDXF = 36,      // [NI]
+  B_IDXE = 40,      // [NI] the loaders, Q, softmax and (even CTA) issuing warps
+  B_GRP = 44,       // [2] the four warps of 32 query rows
+  B_PLAN = 46,
+  B_DRAIN = 47,     // [2] one per issuer
+  B_RS = 49,        // [2] this CTA's 8 softmax warps: O stands in the tile's reference
+  B_RR = 51,        // [2] even CTA: the odd one's does (relayed)
 };
 constexpr int F_FIRST = 1, F_LAST = 2, F_PART = 4, F_SLOT1 = 8, F_BOX = 16, F_FULL = 32;
 
 __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
   return len <= 0 ? 0 : (int)(((uint32_t)min(len, a.cap) + TK - 1) / TK);
+}
+
+// An arrival on a barrier of the even CTA behind stores that this CTA's own tensor core reads: the
+// fence to the async proxy has made them visible there, so the release need not go past the
+// CTA (one of cluster scope takes some 2000 cycles in a warp that has stored).
+__device__ __forceinline__ void arrive_even(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
 // As mbar_wait_vote, for barriers that the other CTA of the pair arrives on too.
@@ -200,7 +208,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     for (int i = lane; i < NBAR; i += 32) {
       uint32_t n = 1;
       if (i == B_SE || i == B_SE + 1 || i == B_OE) n = 16;
-      if (i == B_PF || i == B_PF + 1) n = 8;
+      if (i >= B_PF && i < B_PF + 4) n = 4;
+      if (i == B_RS || i == B_RS + 1) n = 16;
       if (i >= B_IDXE && i < B_IDXE + NI) n = NSLOT + 1 + (rank == 0 ? 2 : 0) + 8;
       if (i == B_GRP || i == B_GRP + 1) n = 4;
       mbar_init(&bars[i], n);
@@ -390,8 +399,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
           __syncwarp();
           ++used;
           // first row and column of half 0, and how half 1 differs
-          const int ra = is_k ? 128 * rank : 64 * (st & 3), rstep = is_k ? 64 : 0;
-          const int ca = is_k ? 64 * st : 256 * (st >> 2) + 128 * rank, cstep = is_k ? 0 : 64;
+          const int ra = is_k ? 128 * rank : 64 * (st >> 1), rstep = is_k ? 64 : 0;
+          const int ca = is_k ? 64 * st : 256 * (st & 1) + 128 * rank, cstep = is_k ? 0 : 64;
           if (box) {
             if (h < 2)
               load_box(dst + h * HALF_BYTES + at * 128, &a.tmap_box, ca + h * cstep, tile_rows[ra + h * rstep + at], full0, policy);
@@ -454,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
         if (it == 0 || !(mt.y & F_FIRST)) continue;
-        if (!poll(B_QE, (nq & 1) ^ 1)) break;
+        if (!doze(B_QE, (nq & 1) ^ 1)) break;
         load_q(mt.x);
       }
       const int mine = min(a.H - row0, ROWS);
@@ -504,12 +513,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         commit_pair_elected(leader, bar(B_DRAIN));   // every MMA issued above has completed
         if (leader) mbar_wait_drain(&bars[B_DRAIN], 0, err);
       } else {
-        // relay: a releasing arrival from the softmax warps themselves takes 2000 cycles longer
-        const uint32_t pr0 = map_peer(bar(B_PR), 0);
-        for (int it = 0; it < nt; ++it) {
-          if (!poll(B_PF + (it & 1), (it >> 1) & 1)) break;
-          if (leader) mbar_arrive_remote(pr0 + 8u * (it & 1));
-        }
       }
       __syncwarp();
     } else if (warp == W_PV && rank == 0) {
@@ -529,26 +532,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         if (!doze(B_IDXF + r, (it / NI) & 1)) break;
         const int flags = __shfl_sync(0xffffffffu, meta[r].y, 0);
         if (leader) mbar_arrive(&bars[B_IDXE + r]);
-        const int pb = it & 1;
-        if (!poll(B_PF + pb, (it >> 1) & 1) || !poll(B_PR + pb, (it >> 1) & 1)) break;
         if (flags & F_FIRST) {
           ++nv;
           if (!poll(B_OE, (nv & 1) ^ 1)) break;
         }
+        if (!poll(B_RS + (it & 1), (it >> 1) & 1)) break;
         if (leader) DSA_TRACE(a.tr, it, 0);
 #pragma unroll 1
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 8; ++u) {   // (64 keys, then the two blocks of output columns)
+          const int c = u >> 1, m = u & 1;
+          if (m == 0 && !poll(B_PF + c, it & 1)) { ok = false; break; }
           if (!poll(B_FULL + NK + slot, phase)) { ok = false; break; }
           tc_fence_after();
-          mma_pair_x4_elected(leader, tmem + COL_O + (u >> 2) * 128, p_desc + (uint64_t)((pb * P_BYTES + (u & 3) * P_COLUMN) >> 4),
-                              v_desc + (uint64_t)(slot * (SLOT_BYTES >> 4)), 2u, 128u, IDESC,
-                              (flags & F_FIRST) && (u & 3) == 0 ? 0u : 1u);
+          mma_pair_x4_elected(leader, tmem + COL_O + m * 128, p_desc + (uint64_t)(c * (P_COLUMN >> 4)),
+                              v_desc + (uint64_t)(slot * (SLOT_BYTES >> 4)), 2u, 128u, IDESC, (flags & F_FIRST) && c == 0 ? 0u : 1u);
           commit_pair_elected(leader, bar(B_EMPTY + NK + slot));
+          if (m == 1) commit_pair_elected(leader, bar(B_PE + c));
           if (++slot == NV) { slot = 0; phase ^= 1; }
         }
         if (!ok) break;
         if (leader) DSA_TRACE(a.tr, it, 7);
-        commit_pair_elected(leader, bar(B_PE + pb));
         if (flags & F_LAST) commit_pair_elected(leader, bar(B_OF));
       }
       commit_pair_elected(leader, bar(B_DRAIN + 1));
@@ -572,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     const uint32_t sw = (uint32_t)(row & 7);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* sums = red + 2 * 4 * ROWS;
-    const uint32_t se0 = map_peer(bar(B_SE), 0), oe0 = map_peer(bar(B_OE), 0);
+    const uint32_t se0 = map_peer(bar(B_SE), 0), pf0 = map_peer(bar(B_PF + part), 0), rs0 = map_peer(bar(B_RS), 0), oe0 = map_peer(bar(B_OE), 0);
     uint32_t grp_phase = 0;
     auto group = [&]() {   // the four warps of these rows
       __syncwarp();
@@ -588,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     int4 done = make_int4(0, 0, 0, 0);
     float m_done = 0.f, l_done = 0.f;
     int seg = 0;
-    auto epilogue = [&](int buffer) -> bool {
+    auto epilogue = [&]() -> bool {
       sums[part * ROWS + row] = l_done;
       if (!group()) return false;
       const bool live = token < done.w;   // (a padding token's row is zeros)
@@ -607,11 +610,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       ++seg;
       tc_fence_after();
       // Output columns 256 wg + 128 half .. +127 of the warp's 32 rows, 32 at a time, turned in
-      // shared memory (the buffer of the P that the last P.V has read) so that a store fills
+      // shared memory (the warp's own place in P, which the last P.V has read) so that a store fills
       // whole 128-byte (parts) or 64-byte pieces of rows: a thread storing its own row in 16-byte
       // pieces takes 8000 cycles for it.
       const int col = 256 * wg + 128 * half, first_row = row0 + 32 * rg;
-      const uint32_t stage = sbase + OFF_P + (uint32_t)buffer * P_BYTES + (uint32_t)warp * 4096u;
+      const uint32_t stage = sbase + OFF_P + part * P_COLUMN + rg * 4096u;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float o[32];
@@ -715,6 +718,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         m_run = top;
         l_run *= alpha;
       }
+      // O, which holds the P.V of the tile before then, in the new reference
+      if (!(mt.y & F_FIRST) && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (!poll(B_PE + 3, (it & 1) ^ 1)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          float o[16];
+          const uint32_t ta = t_lane + COL_O + wg * 128 + c;
+          tmem_ld16(ta, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] *= alpha;
+          tmem_st16(ta, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) arrive_even(rs0 + 8u * sb);
       const float neg = -m_run;
       float s0 = 0.f, s1 = 0.f;
       uint32_t pk[32];
@@ -728,37 +750,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         pk[i / 2] = pack_bf16x2(x, y);
       }
       l_run += s0 + s1;
-      // O holds the P.V of the tile before when it is rescaled
-      if (!(mt.y & F_FIRST) && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!poll(B_PE + (sb ^ 1), ((it - 1) >> 1) & 1)) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-          float o[16];
-          const uint32_t ta = t_lane + COL_O + wg * 128 + c;
-          tmem_ld16(ta, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= alpha;
-          tmem_st16(ta, o);
-        }
-        tmem_st_wait();
+      // these columns of P are free once the MMAs of the tile before that read them are done; a
+      // request's outputs are stored first, through them
+      if (!poll(B_PE + part, (it & 1) ^ 1)) break;
+      if (pending) {
+        if (!epilogue()) break;
+        pending = false;
       }
-      // P's buffer is free once the P.V two tiles back is done
-      if (!poll(B_PE + sb, ((it >> 1) & 1) ^ 1)) break;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        sts128(p_row + sb * P_BYTES + ((((uint32_t)c) ^ sw) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        sts128(p_row + ((((uint32_t)c) ^ sw) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_PF + sb]);
+      if (lane == 0) arrive_even(pf0);
       if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
-      // a request's outputs are stored once the next one's first P is
-      if (pending) {
-        if (!epilogue(sb ^ 1)) break;
-        pending = false;
-      }
       if (mt.y & F_LAST) {
         pending = true;
         done = mt;
@@ -766,7 +772,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
         l_done = l_run;
       }
     }
-    if (pending) epilogue((nt & 1) ^ 1);
+    if (pending) epilogue();
   }
 
   __syncwarp();
