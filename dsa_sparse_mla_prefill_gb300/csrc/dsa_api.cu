@@ -846,14 +846,15 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   const int run = block_size & -block_size;
   const int most_rows = form.ctas == 2 ? 64 : 128;   // (of a pair's half slot)
   a.box_rows = idx || none || run < 8 ? 0 : (run < most_rows ? run : most_rows);
-  a.fetch_bytes = a.box_rows && !fp8 ? dsa::decode_fetch_bytes(a.box_rows, 2ll * ld_kv, 2 * d_qk) : 0;
+  const bool fetch = a.box_rows && (!fp8 || form.ctas == 2);
+  a.fetch_bytes = fetch ? dsa::decode_fetch_bytes(a.box_rows, a.row_bytes, fp8 ? a.row_bytes : 2 * d_qk) : 0;
   if (a.box_rows &&
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;
-  if (a.box_rows && form.ctas == 2 && !dsa::make_tile_map(&a.tmap_box8, cache, N, ld_kv, ld_kv, 8)) return DSA_ERR_CUDA;
+  if (a.box_rows && form.ctas == 2 && !fp8 && !dsa::make_tile_map(&a.tmap_box8, cache, N, ld_kv, ld_kv, 8)) return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, form.rows / form.ctas)) return DSA_ERR_CUDA;
-  const int r = form.ctas == 2 ? dsa::launch_tree_pair(a, d_rope, (int)max_tiles, (cudaStream_t)stream)
+  const int r = form.ctas == 2 ? dsa::launch_tree_pair(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
                 : tree         ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
                                : dsa::launch_paged_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream);
   return r == 0 ? DSA_OK : (r == -2 ? DSA_ERR_UNSUPPORTED : DSA_ERR_CUDA);

@@ -262,19 +262,19 @@ inline int decode_heads_per_cta(int H, bool fp8) { return H <= 16 ? 16 : (H <= 3
 constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
 
 // How a decode or tree call is cut: query rows of a block (the CTAs that walk the same keys),
-// keys of a tile, CTAs of a block.  More than 64 rows of a tree over bf16 rows are blocks
-// of 128 to a CTA pair (tree_pair.cu).
+// keys of a tile, CTAs of a block.  More than 64 rows of a tree are blocks of 128 to a
+// CTA pair (tree_pair.cu).
 struct DecodeForm {
   int rows, keys, ctas;
 };
 inline DecodeForm decode_form(int H, bool fp8, bool tree) {
-  if (tree && H > 64 && !fp8) return {128, 256, 2};
+  if (tree && H > 64) return {128, 256, 2};
   return {decode_heads_per_cta(H, fp8), 128, 1};
 }
 // max_tiles: an upper bound of a request's key tiles (1: nothing is split).
 int launch_paged_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
 int launch_tree_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
-int launch_tree_pair(DecodeArgs& a, int d_rope, int max_tiles, cudaStream_t stream);
+int launch_tree_pair(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream);
 
 // Rows that move in the caches of one or more layers (kv_keep.cu).
 struct KeepArgs {

@@ -47,10 +47,16 @@ constexpr int NK = 4, NV = 3;        // ring slots
 constexpr int NSLOT = NK + NV;
 constexpr float kTau = 8.0f;         // lazy-rescale threshold (log2 units)
 constexpr uint16_t kBoth = 3;
-constexpr int W_QK = 8, W_SCHED = 9, W_Q = 10, W_LOAD = 11, W_PV = 18;
-constexpr int NTHREADS = 640;        // 20 warps (the last without work), launched at 96 registers
-constexpr int REGS_SOFTMAX = 168, REGS_REST = 48;
-static_assert(256 * REGS_SOFTMAX + (NTHREADS - 256) * REGS_REST <= NTHREADS * 96, "registers");
+constexpr int W_QK = 8, W_SCHED = 9, W_Q = 10;
+constexpr int NTHREADS = 640;        // 20 warps, launched at 96 registers
+template <bool F8>
+struct Cfg {
+  // bf16 rows: a loading warp per ring slot (and a warp without work); FP8 rows: four converting
+  // warps for each ring
+  static constexpr int W_PV = F8 ? 11 : 18, W_LOAD = F8 ? 12 : 11, NPROD = F8 ? 8 : NSLOT;
+  static constexpr int REGS_SOFTMAX = F8 ? 144 : 168, REGS_REST = 48, REGS_PROD = F8 ? 72 : 48;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST + 256 * REGS_PROD <= NTHREADS * 96, "registers");
+};
 
 constexpr uint32_t SLOT_BYTES = 16384u, HALF_BYTES = 8192u;
 constexpr uint32_t Q_CHUNK = ROWS * 128u;
@@ -70,7 +76,7 @@ static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
 constexpr uint32_t COL_O = 0, COL_S = 256;
 
 enum {
-  B_FULL = 0,       // [NK K slots, then NV V slots] even CTA: armed for both CTAs' bytes
+  B_FULL = 0,       // [NK K slots, then NV V slots] even CTA: armed for both CTAs' bytes (FP8: 8 warps)
   B_EMPTY = 8,      // one commit
   B_QF = 16,        // even CTA
   B_QE = 17,
@@ -179,8 +185,10 @@ __device__ __forceinline__ void gather(uint32_t leader, uint32_t dst, const CUte
   }
 }
 
-template <int NC>
+template <int NC, bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pair_kernel(const __grid_constant__ DecodeArgs a) {
+  using C = Cfg<F8>;
+  constexpr int W_PV = C::W_PV, W_LOAD = C::W_LOAD;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);   // (the same offset in both CTAs)
@@ -210,7 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (i == B_SE || i == B_SE + 1 || i == B_OE) n = 16;
       if (i >= B_PF && i < B_PF + 4) n = 4;
       if (i == B_RS || i == B_RS + 1) n = 16;
-      if (i >= B_IDXE && i < B_IDXE + NI) n = NSLOT + 1 + (rank == 0 ? 2 : 0) + 8;
+      if (i >= B_IDXE && i < B_IDXE + NI) n = C::NPROD + 1 + (rank == 0 ? 2 : 0) + 8;
+      if (F8 && i < NSLOT) n = 8;   // (the four converting warps of a ring, of both CTAs)
       if (i == B_GRP || i == B_GRP + 1) n = 4;
       mbar_init(&bars[i], n);
     }
@@ -232,8 +241,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
   const uint32_t tmem = *tmem_base_ptr;
   launch_dependents();
 
-  if (warp >= W_QK) {
-    regs_dec<REGS_REST>();
+  if (F8 && warp >= W_LOAD) {
+    regs_dec<C::REGS_PROD>();
+    wait_for_previous();
+    if constexpr (F8) {
+      const int nt = poll(B_PLAN, 0) ? plan[0] : 0;
+      // ----------------------------------------------------------------
+      // FP8 rows: four warps fill the K ring, four the V ring, straight from global memory: a
+      // thread takes 64 codes of a row (the next 64 being on their way), converts them by the
+      // arithmetic of the dequantize kernel and stores them as the bf16 rows would have
+      // landed.  The RoPE columns are copied.  Every row is converted twice, for K and for V, whose
+      // slots are needed a tile apart.
+      // ----------------------------------------------------------------
+      const int cw = warp - W_LOAD, w4 = cw & 3;
+      const bool is_k = cw < 4;
+      const int nslots = is_k ? NK : NV, first_slot = is_k ? 0 : NK, stages = is_k ? NC : 8;
+      // this thread's row of a slot, of the tile's rows from where the slot begins, and its place
+      const int in_slot = is_k ? 32 * w4 + lane : 32 * (w4 & 1) + lane, group = is_k ? 0 : w4 >> 1;
+      const uint32_t place = sbase + OFF_RING + first_slot * SLOT_BYTES + group * HALF_BYTES + in_slot * 128;
+      const uint32_t sw = (uint32_t)(in_slot & 7);
+      const uint32_t full0 = map_peer(bar(B_FULL + first_slot), 0);
+      // bytes of stage st of a row (the RoPE columns' first 64 of 128), and where its row is
+      auto at = [&](int st) { return is_k ? (st < 8 ? 64 * st : 528) : 128 * (2 * (st & 1) + rank) + 64 * group; };
+      auto row_of = [&](int r, int st) { return rows[r * TK + (is_k ? 128 * rank : 64 * (st >> 1)) + in_slot]; };
+      uint4 raw[4];
+      int32_t x = -1;
+      float scale = 0.f;
+      auto load = [&](int r, int st) {
+        x = row_of(r, st);
+        const uint8_t* src = a.rows_base + (int64_t)x * a.row_bytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = x >= 0 ? *reinterpret_cast<const uint4*>(src + at(st) + 16 * i) : make_uint4(0, 0, 0, 0);
+        if (x >= 0 && (!is_k || st < 8)) scale = *reinterpret_cast<const float*>(src + 512 + 4 * (at(st) >> 7));
+      };
+      int slot = 0;
+      uint32_t phase = 1;   // (the slots' first use waits for nothing)
+      bool ok = true;
+      if (nt > 0) {
+        ok = doze(B_IDXF, 0);
+        if (ok) load(0, 0);
+      }
+#pragma unroll 1
+      for (int it = 0; it < nt && ok; ++it) {
+        const int r = it % NI;
+#pragma unroll 1
+        for (int st = 0; st < stages; ++st) {
+          const uint4 now[4] = {raw[0], raw[1], raw[2], raw[3]};
+          const float s = scale;
+          const int32_t row = x;
+          // the stage behind, of the next tile's rows after the last
+          if (st + 1 < stages) {
+            load(r, st + 1);
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
+            if (it + 1 < nt) {
+              if (!doze(B_IDXF + (it + 1) % NI, ((it + 1) / NI) & 1)) { ok = false; break; }
+              load((it + 1) % NI, 0);
+            }
+          }
+          if (!doze(B_EMPTY + first_slot + slot, phase)) { ok = false; break; }
+          const uint32_t dst = place + slot * SLOT_BYTES;
+          if (is_k && st == 8) {
+            const uint8_t* src = a.rows_base + (int64_t)row * a.row_bytes + 528 + 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 y = row >= 0 ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
+              sts128(dst + ((((uint32_t)i) ^ sw) << 4), now[i].x, now[i].y, now[i].z, now[i].w);
+              sts128(dst + ((((uint32_t)(4 + i)) ^ sw) << 4), y.x, y.y, y.z, y.w);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[8];
+              e4m3x4_dequant_bf16x4(now[i].x, s, v[0], v[1]);
+              e4m3x4_dequant_bf16x4(now[i].y, s, v[2], v[3]);
+              e4m3x4_dequant_bf16x4(now[i].z, s, v[4], v[5]);
+              e4m3x4_dequant_bf16x4(now[i].w, s, v[6], v[7]);
+              sts128(dst + ((((uint32_t)(2 * i)) ^ sw) << 4), v[0], v[1], v[2], v[3]);
+              sts128(dst + ((((uint32_t)(2 * i + 1)) ^ sw) << 4), v[4], v[5], v[6], v[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_even(full0 + 8u * slot);
+          if (++slot == nslots) { slot = 0; phase ^= 1u; }
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp >= W_QK) {
+    regs_dec<C::REGS_REST>();
     wait_for_previous();
     if (warp == W_SCHED) {
       // ----------------------------------------------------------------
@@ -364,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       }
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && counts) atomicAdd(err + ERR_BAD_INDEX, (unsigned)bad);
-    } else if (const int nt = poll(B_PLAN, 0) ? plan[0] : 0; warp >= W_LOAD && warp < W_LOAD + NSLOT) {
+    } else if (const int nt = poll(B_PLAN, 0) ? plan[0] : 0; !F8 && warp >= W_LOAD && warp < W_LOAD + NSLOT) {
       // ----------------------------------------------------------------
       // loads, a warp per slot of the K and the V ring.  A slot is two halves of 64 rows x 64
       // columns: of K the two halves of this CTA's 128 keys, of V (64 keys) its two 64-column
@@ -559,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       __syncwarp();
     }
   } else {
-    regs_inc<REGS_SOFTMAX>();
+    regs_inc<C::REGS_SOFTMAX>();
     // --------------------------------------------------------------------
     // softmax and epilogue: warps w, w + 2 (the odd CTA's keys), w + 4 (the second 64 keys
     // of a half) and w + 6 have query rows 32 w .. 32 w + 31, w = 0, 1
@@ -783,10 +881,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
   if (warp == W_QK) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int NC>
+template <int NC, bool F8>
 static int launch_t(DecodeArgs& a, cudaStream_t stream) {
   static int done[64] = {0}, clusters[64] = {0};
-  if (allow_smem(reinterpret_cast<const void*>(tree_pair_kernel<NC>), SMEM_BYTES, done) != 0) return -1;
+  if (allow_smem(reinterpret_cast<const void*>(tree_pair_kernel<NC, F8>), SMEM_BYTES, done) != 0) return -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   // pairs that the GPU holds at a time: a range more would run behind all others
@@ -802,7 +900,7 @@ static int launch_t(DecodeArgs& a, cudaStream_t stream) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&most, tree_pair_kernel<NC>, &cfg) != cudaSuccess || most < 1) {
+    if (cudaOccupancyMaxActiveClusters(&most, tree_pair_kernel<NC, F8>, &cfg) != cudaSuccess || most < 1) {
       cudaGetLastError();
       most = kDecodeMaxCtas / 2;
     }
@@ -810,13 +908,16 @@ static int launch_t(DecodeArgs& a, cudaStream_t stream) {
   }
   most = most / a.head_blocks;
   if (a.groups > most) a.groups = most > 0 ? most : 1;
-  return launch_after(tree_pair_kernel<NC>, dim3((unsigned)(2 * a.groups * a.head_blocks)), NTHREADS, SMEM_BYTES, stream, a);
+  return launch_after(tree_pair_kernel<NC, F8>, dim3((unsigned)(2 * a.groups * a.head_blocks)), NTHREADS, SMEM_BYTES, stream, a);
 }
 
 }  // namespace treepair
 
-int launch_tree_pair(DecodeArgs& a, int d_rope, int max_tiles, cudaStream_t stream) {
-  const int r = d_rope ? treepair::launch_t<9>(a, stream) : treepair::launch_t<8>(a, stream);
+int launch_tree_pair(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cudaStream_t stream) {
+  using namespace treepair;
+  int r;
+  if (fp8) r = d_rope ? launch_t<9, true>(a, stream) : launch_t<8, true>(a, stream);
+  else r = d_rope ? launch_t<9, false>(a, stream) : launch_t<8, false>(a, stream);
   if (r != 0) return r;
   return decode::launch_join(a, 2 * treepair::ROWS * a.head_blocks, max_tiles, true, stream);
 }
