@@ -48,14 +48,14 @@ constexpr int NSLOT = NK + NV;
 constexpr float kTau = 8.0f;         // lazy-rescale threshold (log2 units)
 constexpr uint16_t kBoth = 3;
 constexpr int W_QK = 8, W_SCHED = 9, W_Q = 10;
-constexpr int NTHREADS = 640;        // 20 warps, launched at 96 registers
 template <bool F8>
 struct Cfg {
-  // bf16 rows: a loading warp per ring slot (and a warp without work); FP8 rows: four converting
-  // warps for each ring
-  static constexpr int W_PV = F8 ? 11 : 18, W_LOAD = F8 ? 12 : 11, NPROD = F8 ? 8 : NSLOT;
-  static constexpr int REGS_SOFTMAX = F8 ? 144 : 168, REGS_REST = 48, REGS_PROD = F8 ? 72 : 48;
-  static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST + 256 * REGS_PROD <= NTHREADS * 96, "registers");
+  // a loading warp per ring slot, or two that convert (and one or two without work)
+  static constexpr int NTHREADS = F8 ? 896 : 640, REGS = F8 ? 72 : 96;   // registers at launch
+  static constexpr int NPROD = F8 ? 2 * NSLOT : NSLOT;
+  static constexpr int W_PV = F8 ? 11 : 18, W_LOAD = F8 ? 12 : 11;
+  static constexpr int REGS_SOFTMAX = F8 ? 136 : 168, REGS_REST = F8 ? 32 : 48, REGS_PROD = 48;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST + (NTHREADS - 384) * REGS_PROD <= NTHREADS * REGS, "registers");
 };
 
 constexpr uint32_t SLOT_BYTES = 16384u, HALF_BYTES = 8192u;
@@ -76,7 +76,7 @@ static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
 constexpr uint32_t COL_O = 0, COL_S = 256;
 
 enum {
-  B_FULL = 0,       // [NK K slots, then NV V slots] even CTA: armed for both CTAs' bytes (FP8: 8 warps)
+  B_FULL = 0,       // [NK K slots, then NV V slots] even CTA: armed for both CTAs' bytes (FP8: 4 warps)
   B_EMPTY = 8,      // one commit
   B_QF = 16,        // even CTA
   B_QE = 17,
@@ -186,7 +186,7 @@ __device__ __forceinline__ void gather(uint32_t leader, uint32_t dst, const CUte
 }
 
 template <int NC, bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pair_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1) tree_pair_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<F8>;
   constexpr int W_PV = C::W_PV, W_LOAD = C::W_LOAD;
   extern __shared__ uint8_t smem_raw[];
@@ -219,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
       if (i >= B_PF && i < B_PF + 4) n = 4;
       if (i == B_RS || i == B_RS + 1) n = 16;
       if (i >= B_IDXE && i < B_IDXE + NI) n = C::NPROD + 1 + (rank == 0 ? 2 : 0) + 8;
-      if (F8 && i < NSLOT) n = 8;   // (the four converting warps of a ring, of both CTAs)
+      if (F8 && i < NSLOT) n = 4;   // (the slot's converting warps of both CTAs)
       if (i == B_GRP || i == B_GRP + 1) n = 4;
       mbar_init(&bars[i], n);
     }
@@ -245,89 +245,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1) tree_pa
     regs_dec<C::REGS_PROD>();
     wait_for_previous();
     if constexpr (F8) {
-      const int nt = poll(B_PLAN, 0) ? plan[0] : 0;
+      const int nt = warp < W_LOAD + C::NPROD && poll(B_PLAN, 0) ? plan[0] : 0;
       // ----------------------------------------------------------------
-      // FP8 rows: four warps fill the K ring, four the V ring, straight from global memory: a
-      // thread takes 64 codes of a row (the next 64 being on their way), converts them by the
-      // arithmetic of the dequantize kernel and stores them as the bf16 rows would have
-      // landed.  The RoPE columns are copied.  Every row is converted twice, for K and for V, whose
-      // slots are needed a tile apart.
+      // FP8 rows: two warps per ring slot fill it.  Each copies the codes of its 64 rows x 64
+      // columns to the upper half of their place (eight rows x 64 bytes to an instruction),
+      // converts them by the arithmetic of the dequantize kernel and stores them, in order, as
+      // the bf16 rows would have landed: what a store covers has been read.  The RoPE columns
+      // are copied.  Every row is converted twice, for K and for V, whose slots are needed a
+      // tile apart.
       // ----------------------------------------------------------------
-      const int cw = warp - W_LOAD, w4 = cw & 3;
-      const bool is_k = cw < 4;
-      const int nslots = is_k ? NK : NV, first_slot = is_k ? 0 : NK, stages = is_k ? NC : 8;
-      // this thread's row of a slot, of the tile's rows from where the slot begins, and its place
-      const int in_slot = is_k ? 32 * w4 + lane : 32 * (w4 & 1) + lane, group = is_k ? 0 : w4 >> 1;
-      const uint32_t place = sbase + OFF_RING + first_slot * SLOT_BYTES + group * HALF_BYTES + in_slot * 128;
-      const uint32_t sw = (uint32_t)(in_slot & 7);
-      const uint32_t full0 = map_peer(bar(B_FULL + first_slot), 0);
-      // bytes of stage st of a row (the RoPE columns' first 64 of 128), and where its row is
-      auto at = [&](int st) { return is_k ? (st < 8 ? 64 * st : 528) : 128 * (2 * (st & 1) + rank) + 64 * group; };
-      auto row_of = [&](int r, int st) { return rows[r * TK + (is_k ? 128 * rank : 64 * (st >> 1)) + in_slot]; };
-      uint4 raw[4];
-      int32_t x = -1;
-      float scale = 0.f;
-      auto load = [&](int r, int st) {
-        x = row_of(r, st);
-        const uint8_t* src = a.rows_base + (int64_t)x * a.row_bytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[i] = x >= 0 ? *reinterpret_cast<const uint4*>(src + at(st) + 16 * i) : make_uint4(0, 0, 0, 0);
-        if (x >= 0 && (!is_k || st < 8)) scale = *reinterpret_cast<const float*>(src + 512 + 4 * (at(st) >> 7));
+      const int own = (warp - W_LOAD) >> 1, half = (warp - W_LOAD) & 1;
+      const bool is_k = own < NK;
+      const int nslots = is_k ? NK : NV, stages = is_k ? NC : 8;
+      const int g = lane >> 2, c = lane & 3;   // row of eight, 16 bytes of a row's 64
+      const uint32_t base = sbase + OFF_RING + own * SLOT_BYTES + half * HALF_BYTES;
+      const uint32_t dst = base + g * 128u, raw = base + HALF_BYTES / 2 + lane * 16u;
+      const uint32_t lo = (uint32_t)((2 * c) ^ g) << 4, hi = (uint32_t)((2 * c + 1) ^ g) << 4;
+      const uint32_t full0 = map_peer(bar(B_FULL + own), 0);
+      auto first_row = [&](int t, int st) { return rows + (t % NI) * TK + (is_k ? 128 * rank + 64 * half : 64 * (st >> 1)); };
+      auto byte_of = [&](int32_t x) { return a.rows_base + (int64_t)x * a.row_bytes; };
+      auto rope = [&](const int32_t* rr, int b16, int i) {
+        const int32_t x = rr[8 * i + g];
+        return x >= 0 ? *reinterpret_cast<const uint4*>(byte_of(x) + 528 + 16 * b16) : make_uint4(0, 0, 0, 0);
       };
-      int slot = 0;
-      uint32_t phase = 1;   // (the slots' first use waits for nothing)
-      bool ok = true;
-      if (nt > 0) {
-        ok = doze(B_IDXF, 0);
-        if (ok) load(0, 0);
-      }
+      int tile = 0, st = is_k ? own : own - NK;
+      uint32_t used = 0;
+      bool ok = nt > 0 && doze(B_IDXF, 0);
 #pragma unroll 1
-      for (int it = 0; it < nt && ok; ++it) {
-        const int r = it % NI;
-#pragma unroll 1
-        for (int st = 0; st < stages; ++st) {
-          const uint4 now[4] = {raw[0], raw[1], raw[2], raw[3]};
-          const float s = scale;
-          const int32_t row = x;
-          // the stage behind, of the next tile's rows after the last
-          if (st + 1 < stages) {
-            load(r, st + 1);
-          } else {
+      while (ok) {
+        const int32_t* rr = first_row(tile, st);
+        if (is_k && st == 8) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = rope(rr, c, i);
+          if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {   // rows 0-31, 32-63; their first 64 bytes, their last
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sts128(dst + (4 * (q >> 1) + i) * 1024u + ((uint32_t)((4 * (q & 1) + c) ^ g) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+              if (q < 3) v[i] = rope(rr, 4 * ((q + 1) & 1) + c, 4 * ((q + 1) >> 1) + i);
+            }
+          }
+        } else {
+          const int block = is_k ? st >> 1 : 2 * (st & 1) + rank;
+          const int at = (is_k ? 64 * st : 128 * block + 64 * half) + 16 * c;
+          float scale[2];   // of rows lane, lane + 32
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int32_t x = rr[32 * i + lane];
+            scale[i] = x >= 0 ? *reinterpret_cast<const float*>(byte_of(x) + 512 + 4 * block) : 0.f;
+          }
+          if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int32_t x = rr[8 * i + g];
+            cp_async16(raw + i * 512u, byte_of(x < 0 ? 0 : x) + at, x < 0 ? 0u : 16u);
+          }
+          cp_async_wait_all();
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const uint4 w[2] = {lds128(raw + i * 512u), lds128(raw + (i + 1) * 512u)};
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_IDXE + r]);
-            if (it + 1 < nt) {
-              if (!doze(B_IDXF + (it + 1) % NI, ((it + 1) / NI) & 1)) { ok = false; break; }
-              load((it + 1) % NI, 0);
-            }
-          }
-          if (!doze(B_EMPTY + first_slot + slot, phase)) { ok = false; break; }
-          const uint32_t dst = place + slot * SLOT_BYTES;
-          if (is_k && st == 8) {
-            const uint8_t* src = a.rows_base + (int64_t)row * a.row_bytes + 528 + 64;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 y = row >= 0 ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
-              sts128(dst + ((((uint32_t)i) ^ sw) << 4), now[i].x, now[i].y, now[i].z, now[i].w);
-              sts128(dst + ((((uint32_t)(4 + i)) ^ sw) << 4), y.x, y.y, y.z, y.w);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int k = 0; k < 2; ++k) {
+              const float s = __shfl_sync(0xffffffffu, scale[i >> 2], 8 * ((i + k) & 3) + g);
               uint32_t v[8];
-              e4m3x4_dequant_bf16x4(now[i].x, s, v[0], v[1]);
-              e4m3x4_dequant_bf16x4(now[i].y, s, v[2], v[3]);
-              e4m3x4_dequant_bf16x4(now[i].z, s, v[4], v[5]);
-              e4m3x4_dequant_bf16x4(now[i].w, s, v[6], v[7]);
-              sts128(dst + ((((uint32_t)(2 * i)) ^ sw) << 4), v[0], v[1], v[2], v[3]);
-              sts128(dst + ((((uint32_t)(2 * i + 1)) ^ sw) << 4), v[4], v[5], v[6], v[7]);
+              e4m3x4_dequant_bf16x4(w[k].x, s, v[0], v[1]);
+              e4m3x4_dequant_bf16x4(w[k].y, s, v[2], v[3]);
+              e4m3x4_dequant_bf16x4(w[k].z, s, v[4], v[5]);
+              e4m3x4_dequant_bf16x4(w[k].w, s, v[6], v[7]);
+              sts128(dst + (i + k) * 1024u + lo, v[0], v[1], v[2], v[3]);
+              sts128(dst + (i + k) * 1024u + hi, v[4], v[5], v[6], v[7]);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive_even(full0 + 8u * slot);
-          if (++slot == nslots) { slot = 0; phase ^= 1u; }
+        }
+        ++used;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_even(full0);
+        st += nslots;
+        if (st >= stages) {
+          st -= stages;
+          if (lane == 0) mbar_arrive(&bars[B_IDXE + tile % NI]);
+          if (++tile == nt) break;
+          if (!doze(B_IDXF + tile % NI, (tile / NI) & 1)) break;
         }
       }
+      cp_async_wait_all();
       __syncwarp();
     }
   } else if (warp >= W_QK) {
@@ -892,7 +897,7 @@ static int launch_t(DecodeArgs& a, cudaStream_t stream) {
   if (most == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kDecodeMaxCtas);
-    cfg.blockDim = dim3(NTHREADS);
+    cfg.blockDim = dim3(Cfg<F8>::NTHREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -908,7 +913,7 @@ static int launch_t(DecodeArgs& a, cudaStream_t stream) {
   }
   most = most / a.head_blocks;
   if (a.groups > most) a.groups = most > 0 ? most : 1;
-  return launch_after(tree_pair_kernel<NC, F8>, dim3((unsigned)(2 * a.groups * a.head_blocks)), NTHREADS, SMEM_BYTES, stream, a);
+  return launch_after(tree_pair_kernel<NC, F8>, dim3((unsigned)(2 * a.groups * a.head_blocks)), Cfg<F8>::NTHREADS, SMEM_BYTES, stream, a);
 }
 
 }  // namespace treepair
