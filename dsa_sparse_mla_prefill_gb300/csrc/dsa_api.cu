@@ -848,7 +848,7 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   a.box_rows = idx || none || run < 8 ? 0 : (run < most_rows ? run : most_rows);
   const bool fetch = a.box_rows && (!fp8 || form.ctas == 2);
   a.fetch_bytes = fetch ? dsa::decode_fetch_bytes(a.box_rows, a.row_bytes, fp8 ? a.row_bytes : 2 * d_qk) : 0;
-  if (a.box_rows &&
+  if (a.box_rows && !(fp8 && form.ctas == 2) &&
       !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
             : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
     return DSA_ERR_CUDA;

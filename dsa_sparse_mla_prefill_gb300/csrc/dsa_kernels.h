@@ -262,13 +262,18 @@ inline int decode_heads_per_cta(int H, bool fp8) { return H <= 16 ? 16 : (H <= 3
 constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is sized for
 
 // How a decode or tree call is cut: query rows of a block (the CTAs that walk the same keys),
-// keys of a tile, CTAs of a block.  More than 64 rows of a tree are blocks of 128 to a
-// CTA pair (tree_pair.cu).
+// keys of a tile, CTAs of a block.  Many rows of a tree are blocks of 128 to a CTA pair
+// (tree_pair.cu), fewer as many heads would be.  In us, one CTA against a pair, for 32 requests of
+// 512..16384 keys and for one of 777:
+//   bf16  32 rows  51 : 59   17 : 18      FP8  32 rows  57 : 80   17 : 22
+//         48       69 : 59   22 : 18           64       93 : 82   17 : 23
+//         64       71 : 61   22 : 19           80      128 : 83   19 : 23
+//         80       92 : 62   24 : 19          128      165 : 84   19 : 23
 struct DecodeForm {
   int rows, keys, ctas;
 };
 inline DecodeForm decode_form(int H, bool fp8, bool tree) {
-  if (tree && H > 64) return {128, 256, 2};
+  if (tree && H > (fp8 ? 64 : 32)) return {128, 256, 2};
   return {decode_heads_per_cta(H, fp8), 128, 1};
 }
 // max_tiles: an upper bound of a request's key tiles (1: nothing is split).

@@ -1113,7 +1113,8 @@ static int launch_decode(DecodeArgs& a, bool fp8, int d_rope, int max_tiles, cud
   const int hb = decode_heads_per_cta(a.H, fp8);
   int r = -2;
   if (hb == 64) {
-    r = d_rope ? launch_t<64, 9, false, TREE>(a, stream) : launch_t<64, 8, false, TREE>(a, stream);
+    // (so many rows of a tree go to CTA pairs)
+    if constexpr (!TREE) r = d_rope ? launch_t<64, 9, false, false>(a, stream) : launch_t<64, 8, false, false>(a, stream);
   } else if (hb == 16) {
     if (fp8) r = d_rope ? launch_t<16, 9, true, TREE>(a, stream) : launch_t<16, 8, true, TREE>(a, stream);
     else r = d_rope ? launch_t<16, 9, false, TREE>(a, stream) : launch_t<16, 8, false, TREE>(a, stream);

@@ -226,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == W_Q && lane < 3) {
+  if (warp == W_Q && lane < (F8 ? 1 : 3)) {
     const CUtensorMap* map = lane == 0 ? &a.tmap_q : lane == 1 ? &a.tmap_kv : &a.tmap_box;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }

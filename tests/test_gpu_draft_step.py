@@ -387,7 +387,7 @@ FMTS = ["bf16", "fp8"]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,H", [(1, 16), (3, 5), (4, 16), (8, 16), (5, 24), (2, 128), (64, 4), (16, 16)])
+@pytest.mark.parametrize("n,H", [(1, 16), (3, 5), (2, 16), (11, 3), (4, 16), (5, 13), (8, 16), (5, 24), (2, 128), (64, 4), (16, 16)])
 @pytest.mark.parametrize("lens", [[300], [128], [129, 0, 131], [70, 255, 64, 66]])
 def test_tree_small(fmt, n, H, lens):
     t = Tree(n, lens, n, H, fmt=fmt)
@@ -404,7 +404,7 @@ def test_tree_shapes(fmt, n, H, d_rope, bs):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,H", [(4, 16), (8, 16), (8, 32), (4, 128)])
+@pytest.mark.parametrize("n,H", [(2, 8), (4, 8), (4, 16), (8, 16), (8, 32), (4, 128)])
 def test_tree_long_context_is_split(fmt, n, H):
     t = Tree(7, [20011], n, H, bs=64, fmt=fmt)
     t.check(t.run())
@@ -421,7 +421,7 @@ def test_tree_ragged(fmt, n, H):
     t.check(t.run())
 
 
-@pytest.mark.parametrize("n,H", [(5, 16), (9, 16), (3, 64)])
+@pytest.mark.parametrize("n,H", [(5, 3), (5, 6), (5, 9), (5, 16), (9, 16), (3, 64)])
 def test_tree_masks(n, H):
     """Tokens that see nothing, not themselves, later ones; bits behind the last token; no context at all."""
     words = [[0, 1, (1 << 64) - 1] + [1 << (n - 1)] * (n - 3), [0] * n, ancestors(range(-1, n - 1)), [(1 << 64) - 2] * n]
@@ -430,7 +430,7 @@ def test_tree_masks(n, H):
         t.check(t.run())
 
 
-@pytest.mark.parametrize("n,H", [(4, 16), (8, 32)])
+@pytest.mark.parametrize("n,H", [(4, 8), (4, 16), (8, 32)])
 def test_tree_wide_and_rising_scores(n, H):
     t = Tree(10, [900, 4000], n, H, spread=30.0)
     t.check(t.run())
@@ -465,6 +465,22 @@ def test_tree_bad_entries_are_absent(fmt):
     t.check(t.run(), bad=17)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,H", [(2, 16), (3, 16), (5, 16), (9, 16)])
+def test_tree_queries_of_other_rows_stay_there(fmt, n, H):
+    """NaN and infinite queries of padding requests and of one token's first head reach no other row."""
+    t = Tree(21, [300, 0, 700, 0], n, H, fmt=fmt)
+    want = t.run()
+    t.check(want)
+    t.q[1], t.q[3] = 0x7fc0, 0x7f80
+    t.q[2, n - 1, 0] = 0x7fc0
+    out, lse = t.run()
+    keep = torch.ones(4, n, H, dtype=torch.bool, device="cuda")
+    keep[2, n - 1, 0] = False
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+    assert torch.isnan(out[~keep]).all()
+
+
 def test_tree_empty():
     import dsa_sparse_mla_prefill_gb300 as dsa
     q = bf(normal_bf16(np.random.default_rng(1), (2, 3, 16, 576)))
@@ -477,7 +493,7 @@ def test_tree_empty():
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,H", [(4, 16), (8, 16), (4, 128)])
+@pytest.mark.parametrize("n,H", [(4, 8), (4, 16), (8, 16), (4, 128)])
 def test_tree_same_bits_and_shared_workspace(fmt, n, H):
     import dsa_sparse_mla_prefill_gb300 as dsa
     t, e = Tree(14, [3000, 777, 129], n, H, fmt=fmt), Tree(15, [2500], n, H, fmt=fmt)
@@ -502,7 +518,7 @@ def test_tree_of_one_token_is_decode():
     assert torch.equal(out[:, 0], want[0]) and torch.equal(lse[:, 0], want[1])
 
 
-@pytest.mark.parametrize("n,H", [(4, 16), (8, 16), (2, 128)])
+@pytest.mark.parametrize("n,H", [(4, 8), (4, 16), (8, 16), (2, 128)])
 def test_tree_on_another_stream_and_outputs_kept(n, H):
     t = Tree(17, [500, 1500], n, H)
     big, lse = torch.full((4, n, H, 512), 5.0, dtype=BF, device="cuda"), torch.full((4, n, H), 5.0, device="cuda")
@@ -518,7 +534,7 @@ def test_tree_on_another_stream_and_outputs_kept(n, H):
     t.check(got)
 
 
-@pytest.mark.parametrize("n,H", [(4, 16), (8, 16)])
+@pytest.mark.parametrize("n,H", [(4, 8), (4, 16), (8, 16)])
 def test_tree_graph_follows_its_tensors(n, H):
     """One captured call, replayed as lengths, tables, masks and numbers of drafted tokens change."""
     import dsa_sparse_mla_prefill_gb300 as dsa
