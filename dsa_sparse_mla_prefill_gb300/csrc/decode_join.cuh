@@ -32,8 +32,10 @@ struct Border {
 // request that ends the range, its tiles, and its tiles up to there.  False where no
 // request is cut, and for entries that no call can have (a range whose waits ran out
 // before its last tile leaves zeros): whatever they hold, a border that is returned
-// names a request and ranges of this call.
-__host__ __device__ __forceinline__ bool border_of(uint2 head, int4 at, uint32_t g, int B, int groups, Border& cut) {
+// names a request and ranges of this call.  Where tiles are counted with `gap` blank ones in front
+// of every request, a range that begins among them begins with the request.
+__host__ __device__ __forceinline__ bool border_of(uint2 head, int4 at, uint32_t g, int B, int groups, Border& cut,
+                                                   uint32_t gap = 0) {
   const uint32_t total = head.x, ng = head.y;
   if (ng > (uint32_t)groups || total < ng || total > 0x7fffffffu || g + 1 >= ng) return false;
   if (at.x < 0 || at.x >= B || at.z < 1 || at.z >= at.y) return false;
@@ -43,7 +45,7 @@ __host__ __device__ __forceinline__ bool border_of(uint2 head, int4 at, uint32_t
   cut.request = at.x;
   cut.first = (int)range_of(p0, total, ng);
   cut.parts = (int)range_of(p0 + (uint32_t)at.y - 1, total, ng) - cut.first + 1;
-  cut.whole_start = range_begin((uint32_t)cut.first, total, ng) == p0;
+  cut.whole_start = p0 - range_begin((uint32_t)cut.first, total, ng) <= gap;
   return true;
 }
 
@@ -169,7 +171,8 @@ __global__ void __launch_bounds__(NT_JOIN) tree_join_kernel(const __grid_constan
   launch_dependents();
   wait_for_previous();
   Border cut;
-  if (!border_of(reinterpret_cast<const uint2*>(a.borders)[0], a.borders[1 + blockIdx.x], blockIdx.x, a.B, a.groups, cut)) return;
+  const int4 head = a.borders[0];
+  if (!border_of(make_uint2(head.x, head.y), a.borders[1 + blockIdx.x], blockIdx.x, a.B, a.groups, cut, head.z)) return;
   const int S = cut.parts, nb = S - 1, rank = (int)blockIdx.x - cut.first;
   const uint32_t pitch = (uint32_t)rows_padded;      // (rows of all slots are below 2^23)
   const uint32_t first_slot = (uint32_t)(2 * cut.first + (cut.whole_start ? 0 : 1)) * pitch;

@@ -152,7 +152,7 @@ struct DecodeArgs {
   const int32_t* idx;         // [B, ld] positions, or null: every position < kv_len
   uint16_t* out;              // [B, H, 512] bf16
   float* lse;                 // [B, H]
-  int4* borders;              // [1 + groups]: tiles and ranges, then where each range ends
+  int4* borders;              // [1 + groups]: tiles, ranges and blank tiles, then where each range ends
   float* part_o;              // [2 groups][heads padded][512] normalised partial outputs
   float* part_lse;            // [2 groups][heads padded] their log-sum-exp, base 2
   unsigned int* err;

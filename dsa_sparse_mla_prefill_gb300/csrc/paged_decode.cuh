@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
       if (lane == 0) {
         *plan = nt;
         mbar_arrive(&bars[B_PLAN]);
-        if (range == 0 && hb == 0) reinterpret_cast<uint2*>(a.borders)[0] = make_uint2(total, ng);
+        if (range == 0 && hb == 0) a.borders[0] = make_int4(total, ng, 0, 0);
         // (nothing to join until the range's last tile is reached: a wait may run out before it)
         if (hb == 0) a.borders[1 + range] = make_int4(0, 0, 0, 0);
       }
