@@ -834,25 +834,28 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   // (a GPU with fewer SMs than the workspace is sized for runs fewer ranges)
   const int most = decode_groups(form, B, H, max_tiles, d->num_sms);
   a.groups = groups < most ? groups : most;
-  // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
-  const bool none = N == 0;
-  const bool mapped = fp8 ? dsa::make_row_gather_map_u8(&a.tmap_kv, none ? (const void*)q : cache,
-                                                        none ? (int64_t)B * H : N, none ? 2 * d_qk : a.row_bytes)
-                          : dsa::make_row_gather_map(&a.tmap_kv, none ? (const void*)q : cache,
-                                                     none ? (int64_t)B * H : N, none ? d_qk : ld_kv,
-                                                     none ? d_qk : ld_kv);
-  if (!mapped) return DSA_ERR_CUDA;
   // whole-context calls load runs of rows: the largest power of two in the page size, at most a tile
+  const bool none = N == 0, pair_fp8 = fp8 && form.ctas == 2;
   const int run = block_size & -block_size;
   const int most_rows = form.ctas == 2 ? 64 : 128;   // (of a pair's half slot)
   a.box_rows = idx || none || run < 8 ? 0 : (run < most_rows ? run : most_rows);
   const bool fetch = a.box_rows && (!fp8 || form.ctas == 2);
   a.fetch_bytes = fetch ? dsa::decode_fetch_bytes(a.box_rows, a.row_bytes, fp8 ? a.row_bytes : 2 * d_qk) : 0;
-  if (a.box_rows && !(fp8 && form.ctas == 2) &&
-      !(fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
-            : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows)))
-    return DSA_ERR_CUDA;
-  if (a.box_rows && form.ctas == 2 && !fp8 && !dsa::make_tile_map(&a.tmap_box8, cache, N, ld_kv, ld_kv, 8)) return DSA_ERR_CUDA;
+  // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
+  bool mapped = true;
+  if (!pair_fp8)
+    mapped = fp8 ? dsa::make_row_gather_map_u8(&a.tmap_kv, none ? (const void*)q : cache, none ? (int64_t)B * H : N,
+                                               none ? 2 * d_qk : a.row_bytes)
+                 : dsa::make_row_gather_map(&a.tmap_kv, none ? (const void*)q : cache, none ? (int64_t)B * H : N,
+                                            none ? d_qk : ld_kv, none ? d_qk : ld_kv);
+  if (mapped && a.box_rows)
+    mapped = fp8 ? dsa::make_tile_map_u8(&a.tmap_box, cache, N, a.row_bytes, a.box_rows)
+                 : dsa::make_tile_map(&a.tmap_box, cache, N, ld_kv, ld_kv, a.box_rows);
+  if (mapped && a.box_rows && form.ctas == 2)
+    mapped = fp8 ? dsa::make_tile_map_u8(&a.tmap_box8, cache, N, a.row_bytes, a.box_rows, 64) &&
+                       dsa::make_tile_map_u8(&a.tmap_kv, cache, N, a.row_bytes, a.box_rows, 16)
+                 : dsa::make_tile_map(&a.tmap_box8, cache, N, ld_kv, ld_kv, 8);
+  if (!mapped) return DSA_ERR_CUDA;
   if (!dsa::make_tile_map(&a.tmap_q, q, (int64_t)B * H, d_qk, d_qk, form.rows / form.ctas)) return DSA_ERR_CUDA;
   const int r = form.ctas == 2 ? dsa::launch_tree_pair(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)
                 : tree         ? dsa::launch_tree_decode(a, fp8, d_rope, (int)max_tiles, (cudaStream_t)stream)

@@ -139,9 +139,10 @@ inline int decode_fetch_bytes(int rows, int64_t row_bytes, int read_bytes) {
 }
 
 struct DecodeArgs {
-  CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box
+  CUtensorMap tmap_kv;        // cache rows, 64-column (or 128-byte) x 1-row box (pair form over FP8 rows: 16 bytes x
+                              // box_rows, unswizzled, unset when box_rows = 0)
   CUtensorMap tmap_box;       // cache rows, 64-column x box_rows box (unset when box_rows = 0)
-  CUtensorMap tmap_box8;      // the same with 8 rows (pair form)
+  CUtensorMap tmap_box8;      // the same with 8 rows (pair form; over FP8 rows: 64 bytes x box_rows, unswizzled)
   CUtensorMap tmap_q;         // q viewed [B*H, d_qk], 64-column x HB-row box
   const uint8_t* rows_base;   // the cache rows as bytes, and their pitch
   int row_bytes;

@@ -76,17 +76,17 @@ inline bool make_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The byte map with box = 128 bytes x `box_rows` rows.
-inline bool make_tile_map_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows) {
+// The byte map with box = 128 bytes x `box_rows` rows, or `width` bytes (16 .. 64) that land unswizzled.
+inline bool make_tile_map_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows, int width = 128) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (fn == nullptr || rows < 1 || row_bytes < 128 || (row_bytes % 16) != 0 || box_rows < 1 || box_rows > 256)
     return false;
   cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -292,6 +292,17 @@ extern "C" int dsa_selftest_border(unsigned total, unsigned ng, int request, int
   cut[3] = c.whole_start;
   return 1;
 }
+// The same with `gap` blank tiles counted in front of every request.
+extern "C" int dsa_selftest_border_gap(unsigned total, unsigned ng, unsigned gap, int request, int tiles, int so_far, unsigned g,
+                                       int B, int groups, int* cut) {
+  dsa::decode::Border c;
+  if (!dsa::decode::border_of(make_uint2(total, ng), make_int4(request, tiles, so_far, 0), g, B, groups, c, gap)) return 0;
+  cut[0] = c.request;
+  cut[1] = c.first;
+  cut[2] = c.parts;
+  cut[3] = c.whole_start;
+  return 1;
+}
 extern "C" unsigned dsa_selftest_range_begin(unsigned g, unsigned total, unsigned ng) {
   return dsa::decode::range_begin(g, total, ng);
 }

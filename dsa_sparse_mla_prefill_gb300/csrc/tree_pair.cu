@@ -35,6 +35,7 @@ using decode::drafted_of;
 using decode::elect_one;
 using decode::evict_first_policy;
 using decode::evict_normal_policy;
+using decode::load_2d_hint;
 using decode::range_begin;
 using decode::row_at;
 using decode::warp_scan;
@@ -68,7 +69,7 @@ constexpr uint32_t OFF_META = OFF_ROWS + NI * TK * 4u;
 constexpr uint32_t OFF_VALID = OFF_META + NI * 16u;
 constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums
 constexpr uint32_t OFF_BAR = OFF_RED + 3u * 4u * ROWS * 4u;
-constexpr int NBAR = 53;
+constexpr int NBAR = 61;
 constexpr uint32_t OFF_MISC = OFF_BAR + (NBAR + 1) / 2 * 16u;
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 64u + 1024u;
 static_assert(SMEM_BYTES <= 227u * 1024u, "shared memory budget");
@@ -82,17 +83,16 @@ enum {
   B_SF = 18,        // [2] one commit
   B_SE = 20,        // [2] even CTA: 16 softmax warps of the pair
   B_PF = 22,        // [4] per 64 keys: this CTA's two softmax warps have stored its rows of P
-  B_PR = 26,        // [4] even CTA: the odd one's have (relayed)
-  B_PE = 30,        // [4] one commit: the MMAs that read these columns of P are done
-  B_OF = 34,
-  B_OE = 35,        // even CTA: 16 warps of the pair
-  B_IDXF = 36,      // [NI]
-  B_IDXE = 40,      // [NI] the loaders, Q, softmax and (even CTA) issuing warps
-  B_GRP = 44,       // [2] the four warps of 32 query rows
-  B_PLAN = 46,
-  B_DRAIN = 47,     // [2] one per issuer
-  B_RS = 49,        // [2] this CTA's 8 softmax warps: O stands in the tile's reference
-  B_RR = 51,        // [2] even CTA: the odd one's does (relayed)
+  B_PE = 26,        // [4] one commit: the MMAs that read these columns of P are done
+  B_OF = 30,
+  B_OE = 31,        // even CTA: 16 warps of the pair
+  B_IDXF = 32,      // [NI]
+  B_IDXE = 36,      // [NI] the loaders, Q, softmax and (even CTA) issuing warps
+  B_GRP = 40,       // [2] the four warps of 32 query rows
+  B_PLAN = 42,
+  B_DRAIN = 43,     // [2] one per issuer
+  B_RS = 45,        // [2] this CTA's 8 softmax warps: O stands in the tile's reference
+  B_RAW = 47,       // [2 NSLOT] FP8: codes and scales of a converting warp have landed
 };
 constexpr int F_FIRST = 1, F_LAST = 2, F_PART = 4, F_SLOT1 = 8, F_BOX = 16, F_FULL = 32;
 
@@ -246,12 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
     if constexpr (F8) {
       const int nt = warp < W_LOAD + C::NPROD && poll(B_PLAN, 0) ? plan[0] : 0;
       // ----------------------------------------------------------------
-      // FP8 rows: two warps per ring slot fill it.  Each copies the codes of its 64 rows x 64
-      // columns to the upper half of their place (eight rows x 64 bytes to an instruction),
-      // converts them by the arithmetic of the dequantize kernel and stores them, in order, as
-      // the bf16 rows would have landed: what a store covers has been read.  The RoPE columns
-      // are copied.  Every row is converted twice, for K and for V, whose slots are needed a
-      // tile apart.
+      // FP8 rows: two warps per ring slot fill it, each 64 rows x 64 columns of 8 KB.  The codes
+      // land in the upper half of that place and the rows' scales at its start, by boxes or, from
+      // pages without runs and in tiles with missing keys, by 16-byte copies (eight rows x 64
+      // bytes to an instruction).  The warp converts them by the arithmetic of the dequantize
+      // kernel and stores them, in order, as the bf16 rows would have landed: what a store covers
+      // has been read.  The RoPE columns are copied.  Every row is converted twice, for K and for
+      // V, whose slots are needed a tile apart.
       // ----------------------------------------------------------------
       const int own = (warp - W_LOAD) >> 1, half = (warp - W_LOAD) & 1;
       const bool is_k = own < NK;
@@ -267,41 +268,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         const int32_t x = rr[8 * i + g];
         return x >= 0 ? *reinterpret_cast<const uint4*>(byte_of(x) + 528 + 16 * b16) : make_uint4(0, 0, 0, 0);
       };
+      const int b_raw = B_RAW + warp - W_LOAD;
+      const uint64_t policy = evict_normal_policy();
       int tile = 0, st = is_k ? own : own - NK;
-      uint32_t used = 0;
+      uint32_t used = 0, landed = 0;
       bool ok = nt > 0 && doze(B_IDXF, 0);
 #pragma unroll 1
       while (ok) {
         const int32_t* rr = first_row(tile, st);
-        if (is_k && st == 8) {
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = rope(rr, c, i);
+        const bool is_rope = is_k && st == 8;
+        const bool box = (meta[tile % NI].y & F_BOX) != 0;
+        const int block = is_k ? st >> 1 : 2 * (st & 1) + rank;
+        const int at = is_k ? 64 * st : 128 * block + 64 * half;
+        if (box) {
           if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bars[b_raw], is_rope ? 64 * 128 : 64 * (64 + 16));
+          __syncwarp();
+          const int r = lane * a.box_rows;
+          if (r < 64) {
+            const int x = rr[r];
+            if (is_rope) {
+              load_2d_hint(base + r * 128, &a.tmap_box, 528, x, &bars[b_raw], policy);
+            } else {
+              load_2d_hint(base + HALF_BYTES / 2 + r * 64, &a.tmap_box8, at, x, &bars[b_raw], policy);
+              load_2d_hint(base + r * 16, &a.tmap_kv, 512, x, &bars[b_raw], policy);
+            }
+          }
+          if (!poll(b_raw, landed & 1)) break;
+          ++landed;
+        }
+        if (is_rope) {
+          if (!box) {
+            uint4 v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // rows 0-31, 32-63; their first 64 bytes, their last
+            for (int i = 0; i < 4; ++i) v[i] = rope(rr, c, i);
+            if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sts128(dst + (4 * (q >> 1) + i) * 1024u + ((uint32_t)((4 * (q & 1) + c) ^ g) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
-              if (q < 3) v[i] = rope(rr, 4 * ((q + 1) & 1) + c, 4 * ((q + 1) >> 1) + i);
+            for (int q = 0; q < 4; ++q) {   // rows 0-31, 32-63; their first 64 bytes, their last
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                sts128(dst + (4 * (q >> 1) + i) * 1024u + ((uint32_t)((4 * (q & 1) + c) ^ g) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+                if (q < 3) v[i] = rope(rr, 4 * ((q + 1) & 1) + c, 4 * ((q + 1) >> 1) + i);
+              }
             }
           }
         } else {
-          const int block = is_k ? st >> 1 : 2 * (st & 1) + rank;
-          const int at = (is_k ? 64 * st : 128 * block + 64 * half) + 16 * c;
           float scale[2];   // of rows lane, lane + 32
+          if (box) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int32_t x = rr[32 * i + lane];
-            scale[i] = x >= 0 ? *reinterpret_cast<const float*>(byte_of(x) + 512 + 4 * block) : 0.f;
-          }
-          if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+            for (int i = 0; i < 2; ++i) scale[i] = lds_f32(base + 16u * (lane + 32 * i) + 4u * block);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int32_t x = rr[8 * i + g];
-            cp_async16(raw + i * 512u, byte_of(x < 0 ? 0 : x) + at, x < 0 ? 0u : 16u);
+            for (int i = 0; i < 2; ++i) {
+              const int32_t x = rr[32 * i + lane];
+              scale[i] = x >= 0 ? *reinterpret_cast<const float*>(byte_of(x) + 512 + 4 * block) : 0.f;
+            }
+            if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int32_t x = rr[8 * i + g];
+              cp_async16(raw + i * 512u, byte_of(x < 0 ? 0 : x) + at + 16 * c, x < 0 ? 0u : 16u);
+            }
+            cp_async_wait_all();
           }
-          cp_async_wait_all();
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const uint4 w[2] = {lds128(raw + i * 512u), lds128(raw + (i + 1) * 512u)};
@@ -332,6 +361,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         }
       }
       cp_async_wait_all();
+      if (tile < nt) {
+        // a wait ran out: let loads in flight land before this CTA can leave
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 20000ull) {
+        }
+      }
       __syncwarp();
     }
   } else if (warp >= W_QK) {

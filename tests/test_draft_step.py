@@ -211,3 +211,46 @@ def test_binding_refuses_before_the_library(lib):
         dsa.dsa_kv_keep(x[0], pos, pos, pos, 16, 4)
     with pytest.raises(TypeError):
         dsa.dsa_kv_keep(x[0].float(), pos, pos, pos, 16, 4)
+
+
+@pytest.mark.parametrize("tiles,groups", [([7], 76), ([1, 1, 1], 76), ([400], 76), ([3, 0, 0, 9, 1, 1, 40], 9), ([1] * 300, 76),
+                                          ([2, 1] * 90, 38), ([0, 0, 5], 2), ([17, 64, 30, 128, 90, 44, 23, 50], 19), ([2 ** 25, 3, 2 ** 29], 76)])
+def test_split_with_blank_tiles(tiles, groups):
+    """The pair form's split, a blank tile in front of every request: what a range holds, written down tile by tile,
+    against the border that the joining kernel takes from its end (request, first range, parts, and whether the
+    request is the first one of its first range)."""
+    import ctypes
+    import os
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    from dsa_sparse_mla_prefill_gb300 import build
+    build.build()
+    lib = ctypes.CDLL(os.path.join(os.path.dirname(dsa.__file__), "libdsa_selftest.so"))
+    u, i = ctypes.c_uint, ctypes.c_int
+    total, ng = sum(n + 1 for n in tiles if n), min(sum(tiles), groups)
+    begin = [g * total // ng for g in range(ng + 1)]
+    held = [[] for _ in range(ng)]            # of each range: (request, first tile, behind the last)
+    at = 0
+    for b, n in enumerate(tiles):
+        if n == 0:
+            continue
+        at += 1
+        for g in range(ng):
+            lo, hi = max(begin[g], at), min(begin[g + 1], at + n)
+            if lo < hi:
+                held[g].append((b, lo - at, hi - at))
+        at += n
+    assert sum(hi - lo for h in held for _, lo, hi in h) == sum(tiles)
+    cuts = 0
+    for g in range(ng):
+        cut = (ctypes.c_int * 4)()
+        b, _, hi = held[g][-1] if held[g] else (0, 0, 0)
+        got = lib.dsa_selftest_border_gap(u(total), u(ng), u(1), i(b), i(tiles[b] if held[g] else 0), i(hi), u(g), i(len(tiles)),
+                                          i(groups), cut)
+        if hi == tiles[b] or not held[g]:
+            assert not got
+            continue
+        of = [x for x in range(ng) if any(s[0] == b for s in held[x])]
+        assert got and of == list(range(of[0], of[-1] + 1))
+        assert tuple(cut) == (b, of[0], len(of), int(held[of[0]][0][0] == b))
+        cuts += 1
+    assert cuts > 0 or max(tiles) < 3

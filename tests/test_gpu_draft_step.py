@@ -588,11 +588,12 @@ def test_tree_graphs_at_once():
         t.check(o)
 
 
-@pytest.mark.parametrize("n,H", [(4, 8), (8, 16)])
-def test_tree_many_requests(n, H):
-    """Hundreds of short requests, padding ones in long runs among them; a prefix in shared pages."""
+@pytest.mark.parametrize("most", [300, 1500])
+@pytest.mark.parametrize("n,H", [(4, 8), (3, 16), (8, 16)])
+def test_tree_many_requests(n, H, most):
+    """Hundreds of short requests, padding ones in long runs among them."""
     rng = np.random.default_rng(5)
-    lens = np.where(rng.random(400) < 0.3, rng.integers(n, 300, 400), 0).astype(np.int32)
+    lens = np.where(rng.random(400) < 0.3, rng.integers(n, most, 400), 0).astype(np.int32)
     t = Tree(20, lens, n, H)
     t.check(t.run())
 
