@@ -888,6 +888,12 @@ int dsa_tree_decode(const uint16_t* q, const void* cache, int cache_format, int 
                      tree_mask, num_draft, n, B, n * H, d_qk, d_v, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
+// Two ranges of bytes that share some.
+static bool ranges_meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < (uint64_t)a_bytes : x - y < (uint64_t)b_bytes);
+}
+
 int dsa_kv_keep(void* const* caches, int num_caches, int64_t row_bytes, int N, const int32_t* block_table,
                 int max_blocks, int block_size, const int32_t* kv_lens, const int32_t* num_draft, int n,
                 const int32_t* keep, int m, int B, int32_t* new_lens, dsa_stream_t stream) {
@@ -897,15 +903,20 @@ int dsa_kv_keep(void* const* caches, int num_caches, int64_t row_bytes, int N, c
   if (num_caches > DSA_MAX_CACHES || n > DSA_TREE_MAX_TOKENS || m > DSA_TREE_MAX_TOKENS || row_bytes > (1 << 24))
     return DSA_ERR_UNSUPPORTED;
   if (B == 0) return DSA_OK;
-  if (!block_table || !kv_lens || (!keep && m > 0) || !new_lens || new_lens == kv_lens) return DSA_ERR_INVALID_ARG;
+  if (!block_table || !kv_lens || (!keep && m > 0) || !new_lens) return DSA_ERR_INVALID_ARG;
   if (!aligned4(block_table) || !aligned4(kv_lens) || !aligned4(num_draft) || !aligned4(keep) || !aligned4(new_lens))
+    return DSA_ERR_INVALID_ARG;
+  // (every cache's CTAs read these while one cache's store the lengths)
+  const int64_t lens = 4ll * B;
+  if (ranges_meet(new_lens, lens, kv_lens, lens) || ranges_meet(new_lens, lens, num_draft, num_draft ? lens : 0) ||
+      ranges_meet(new_lens, lens, keep, lens * m) || ranges_meet(new_lens, lens, block_table, lens * max_blocks))
     return DSA_ERR_INVALID_ARG;
   dsa::KeepArgs a;
   memset(&a, 0, sizeof(a));
   for (int i = 0; i < num_caches; ++i) {
     if ((!caches[i] && N > 0) || !aligned16(caches[i])) return DSA_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
-      if (N > 0 && caches[j] == caches[i]) return DSA_ERR_INVALID_ARG;
+      if (ranges_meet(caches[j], N * row_bytes, caches[i], N * row_bytes)) return DSA_ERR_INVALID_ARG;
     a.caches[i] = caches[i];
   }
   DevInfo* d;

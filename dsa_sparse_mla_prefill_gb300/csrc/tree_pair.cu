@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int32_t x = rr[8 * i + g];
-              cp_async16(raw + i * 512u, byte_of(x < 0 ? 0 : x) + at + 16 * c, x < 0 ? 0u : 16u);
+              cp_async16(raw + i * 512u, x < 0 ? static_cast<const void*>(a.borders) : byte_of(x) + at + 16 * c, x < 0 ? 0u : 16u);
             }
             cp_async_wait_all();
           }

@@ -610,7 +610,7 @@ int dsa_tree_decode(const uint16_t* q, const void* cache, int cache_format, int 
  *
  * caches       HOST array of num_caches (1 .. DSA_MAX_CACHES) DEVICE pointers, copied into
  *              the launch: the cache of each layer, [N] packed rows of row_bytes bytes
- *              (a multiple of 16), any format, 16-byte aligned, all different.
+ *              (a multiple of 16), any format, 16-byte aligned, none reaching into another.
  * kv_lens      DEVICE int32 [B], drafted tokens included; zero or less: a padding
  *              request, left alone (new_lens[b] = kv_lens[b]).
  * num_draft    DEVICE int32 [B] or NULL, as for dsa_tree_decode; n <= DSA_TREE_MAX_TOKENS.
@@ -618,7 +618,7 @@ int dsa_tree_decode(const uint16_t* q, const void* cache, int cache_format, int 
  *              in ascending order, the first -1 ends it.  Any other entry that is not
  *              in [0, n_b) or not above the one before it ends the path as well
  *              and is counted (counts[0] of dsa_last_device_error).
- * new_lens     DEVICE int32 [B] (out), another array than kv_lens.
+ * new_lens     DEVICE int32 [B] (out), memory of its own: no part of the four arrays above.
  * A request with n_b outside [0, n] or above its length is left alone and counted. A
  * row whose block id or row is out of range does not move and is counted.
  * Requests must not share the pages of their drafted positions. */

@@ -481,15 +481,18 @@ def test_tree_queries_of_other_rows_stay_there(fmt, n, H):
     assert torch.isnan(out[~keep]).all()
 
 
-def test_tree_empty():
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("H", [4, 16, 64])
+def test_tree_empty(fmt, H):
     import dsa_sparse_mla_prefill_gb300 as dsa
-    q = bf(normal_bf16(np.random.default_rng(1), (2, 3, 16, 576)))
-    cache = torch.empty(0, 576, dtype=BF, device="cuda")
+    q = bf(normal_bf16(np.random.default_rng(1), (2, 3, H, 576)))
+    cache = torch.empty(0, 576, dtype=BF, device="cuda") if fmt == "bf16" else torch.empty(0, 656, dtype=torch.uint8, device="cuda")
     mask = torch.tensor([[1, 2, 4], [1, 3, 7]], device="cuda")
-    out, lse = dsa.dsa_tree_decode(q, cache, i32([[0], [0]]), i32([5, 0]), mask, 16, 1.0)
-    assert bad_count() == 5 and (out == 0).all() and torch.isneginf(lse).all()
+    for bs in (16, 3):
+        out, lse = dsa.dsa_tree_decode(q, cache, i32([[0, 0], [0, 0]]), i32([5, 0]), mask, bs, 1.0)
+        assert bad_count() == 5 and (out == 0).all() and torch.isneginf(lse).all()
     out, lse = dsa.dsa_tree_decode(q[:0], cache, i32(np.zeros((0, 1))), i32(np.zeros(0)), mask[:0], 16, 1.0)
-    assert out.shape == (0, 3, 16, 512)
+    assert out.shape == (0, 3, H, 512)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
