@@ -789,7 +789,7 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   const bool fp8 = cache_format == DSA_CACHE_FP8;
   const dsa::DecodeForm form = dsa::decode_form(H, fp8, tree != nullptr);
   const int64_t max_tiles = decode_tiles(form, idx ? k : (int64_t)max_blocks * block_size);
-  if (B * (max_tiles + 1) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (B * (max_tiles + (form.ctas == 2)) > INT32_MAX) return DSA_ERR_UNSUPPORTED;   // (a pair's split counts one more a request)
   if (B == 0) return DSA_OK;
   if (!q || (!cache && N > 0) || !block_table || !kv_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned4(block_table) || !aligned4(kv_lens) || !aligned4(idx) ||

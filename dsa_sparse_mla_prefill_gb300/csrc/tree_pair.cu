@@ -1,7 +1,7 @@
-// Attention of a tree of drafted tokens over bf16 latent rows, for more than 64 query rows per
-// request (tokens x heads): CTA pairs with the query rows on the tensor cores' M side.
+// Attention of a tree of drafted tokens over the paged latent cache (see tree_decode.cu) for many
+// query rows (tokens x heads) per request: CTA pairs with the query rows on the tensor cores' M side.
 //
-// Bound: at 128 rows and more a key row's flops (2 * 1088 each query row) take longer than its
+// Bound: from some 120 rows on a key row's flops (2 * 1088 each query row) take longer than its
 // 1152 bytes take from HBM, so the tensor cores are the roof, and what feeds them.
 //
 // A pair (2-CTA cluster, cta_group::2) holds a block of 128 query rows of one request, 64 in
@@ -14,16 +14,27 @@
 //                 memory as the A operand of the same CTA's rows.
 //   O += P V      M = 128, N = 256 for output columns 256 m + ..: CTA r supplies columns 256 m +
 //                 128 r .. +127 of all 256 keys.  O takes 2 x 128 TMEM columns, S twice 128.
-// With the query rows as M, nothing of P or the maxima crosses the pair, and each CTA's MMAs
-// read 4.2 KB of shared memory per 64 query rows x key (with the keys as M, as the decode kernel has it,
-// 64 rows to a CTA: 5.8) and load 1.1 KB (2.2).
+// With the query rows as M, nothing of P or the maxima crosses the pair, and for 64 query rows
+// and a key each CTA's MMAs read 1.6 KB of shared memory and its loads bring 1.1 KB (with the keys
+// as M and 64 rows to a CTA, as the decode kernel has it: 3.2 and 2.2).
 //
-// Loads go through two rings of 16 KB slots, a tile's nine 64-column chunks of 128 keys and its
-// eight V slots (64 keys x 128 columns), each with a loading warp per slot and an issuing
-// warp of its own, so that a tile's softmax and P.V run beside the next tile's QK.
+// Loads go through two rings of 16 KB slots: a tile's nine 64-column chunks of 128 keys through
+// four, its eight V slots (64 keys x 128 columns) through three, a loading warp per slot (FP8
+// rows: two converting ones) and an issuing warp per ring, so that a tile's softmax and P V run
+// beside the next tile's QK.  (Five and two slots: 114 against 97 us on 8 x 4096..32768 at 512
+// rows, three and four 102; one ring of five with P in two places 111.)  P has one place, whose
+// four columns of 64 keys are handed over one by one (with P handed over as a whole the three
+// slots less would have cost more than they give).  A request's O leaves through the place of P
+// while the next one's first QK runs.  The scheduling warp asks L2 for the boxes of a tile more
+// than a tile ahead of its loads.
 //
 // Split over the length, join and the rows of absent keys as in paged_decode.cuh; a range of
-// tiles is walked by the pairs of all row blocks at the same time.
+// tiles is walked by the pairs of all row blocks at the same time.  A tile takes some 5200 cycles
+// (its MMAs 4352), a range 7000 to its first scores, a request's change some 5000, the join 7 us:
+// 8 x 4096..32768 at 512 rows 93 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
+// 61 (27 at the copy rate), 1 x 131072 at 256 rows 62 (38).
+// FP8 rows: 24 x 1024..16384 at 256 rows 119 us (one CTA per 32 rows 283), 12000 cycles a tile
+// for the conversion: see there.
 #include <cfloat>
 
 #include "paged_decode.cuh"
@@ -253,6 +264,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       // kernel and stores them, in order, as the bf16 rows would have landed: what a store covers
       // has been read.  The RoPE columns are copied.  Every row is converted twice, for K and for
       // V, whose slots are needed a tile apart.
+      //
+      // What bounds it: a slot's way from the MMAs that free it to the ones that read it again
+      // (wait 0.7k cycles, codes landing 1.2k, conversion 2k with 14 warps at it, hand-over 0.6k),
+      // times 17 slots' worth a tile in seven slots.  On 24 x 1024..16384 at 256 rows, 119 us:
+      // without the loads it would take 103, without the arithmetic no less; all by 16-byte copies
+      // 122 (load-store wavefronts 62 % of peak); half or all of the codes through registers,
+      // ahead of the free slot, 137 to 160 (a load's data in flight takes room in 28 KB of L1);
+      // one warp a slot 170; four warps on every slot in turn 185.
       // ----------------------------------------------------------------
       const int own = (warp - W_LOAD) >> 1, half = (warp - W_LOAD) & 1;
       const bool is_k = own < NK;
