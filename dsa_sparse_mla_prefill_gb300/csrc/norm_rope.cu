@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(NT, kGradientCtas<sizeof(E), NP>) norm_rope_gr
         }
       }
     }
-    const float r = rsqrtf(row_sum<G>(s0 + s1) * inv_n + a.eps);
+    // (a row that is not there adds zeros: with eps = 0 its root would be infinite)
+    const float rs = row_sum<G>(s0 + s1), r = live ? rsqrtf(rs * inv_n + a.eps) : 0.f;
     const float k = -(row_sum<G>(d0 + d1) * inv_n * r * r);
     ahead.load(ln);   // (into the slots of the row before this one)
 #pragma unroll

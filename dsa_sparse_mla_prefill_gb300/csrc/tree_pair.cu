@@ -689,7 +689,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         }
         commit_pair_elected(leader, bar(B_DRAIN));   // every MMA issued above has completed
         if (leader) mbar_wait_drain(&bars[B_DRAIN], 0, err);
-      } else {
       }
       __syncwarp();
     } else if (warp == W_PV && rank == 0) {

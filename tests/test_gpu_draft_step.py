@@ -181,6 +181,15 @@ def test_norm_sizes_of_x():
             c.check_gradient(c.gradient())
 
 
+@pytest.mark.parametrize("d,T", [(64, 7), (128, 1), (256, 33), (576, 3)])
+def test_norm_gradient_without_eps_where_lanes_lack_rows(d, T):
+    """eps = 0 with fewer rows than the groups of lanes take at a time: those without one add nothing."""
+    for dtype in (BF, F32):
+        c = Norm(d + T, T, 1, 3, d, None, 0, dtype=dtype, eps=0.0)
+        c.check_forward(c.forward())
+        c.check_gradient(c.gradient())
+
+
 def test_norm_views_and_places():
     """Columns of a wider projection, in place, odd offsets, broadcast inputs, results in the caller's tensors."""
     c = Norm(8, 20, 3, 2, 192)
