@@ -32,6 +32,7 @@ Norms in front of the rotation, and the step that checks drafted tokens over tha
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import operator
@@ -131,7 +132,7 @@ _SIGNATURES = {
     "dsa_tree_decode_workspace": (_L, [_I, _I, _I, _L]),
     "dsa_tree_decode": (_I, [_VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _F, _VP, _VP, _VP, _L,
                              _VP]),
-    "dsa_kv_keep": (_I, [ctypes.POINTER(_VP), _I, _L, _I, _VP, _I, _I, _VP, _VP, _I, _VP, _I, _I, _VP, _VP]),
+    "dsa_kv_keep": (_I, [_VP, _I, _L, _I, _VP, _I, _I, _VP, _VP, _I, _VP, _I, _I, _VP, _VP]),
     "dsa_form_calibration_default": (_I, [ctypes.POINTER(FormCalibration)]),
     "dsa_choose_form": (_I, [ctypes.POINTER(FormQuery), ctypes.POINTER(FormCalibration),
                              ctypes.POINTER(FormEstimate)]),
@@ -1095,7 +1096,7 @@ def dsa_kv_keep(caches, block_table, kv_lens, keep, block_size: int, n: int, num
         raise ValueError("caches must be 2-D CUDA tensors")
     # (by maps: a model has dozens of them, and a loop over their attributes costs the host more than the call)
     Tensor, n_caches = torch.Tensor, len(caches)
-    pointers = (_VP * n_caches)(*map(Tensor.data_ptr, caches))
+    pointers = array.array("Q", map(Tensor.data_ptr, caches))
     if n_caches > 1 and (set(map(_DTYPE, caches)) != {dtype} or set(map(_SHAPE, caches)) != {shape} or
                          set(map(Tensor.get_device, caches)) != {dev}) or not all(map(Tensor.is_contiguous, caches)):
         raise ValueError("caches must be contiguous tensors of one shape and dtype on one device")
@@ -1118,7 +1119,7 @@ def dsa_kv_keep(caches, block_table, kv_lens, keep, block_size: int, n: int, num
         if new_lens.shape[0] != B:
             raise ValueError("new_lens must have one entry per request")
     _queue(lib().dsa_kv_keep, "dsa_kv_keep",
-           (pointers, n_caches, shape[1] * (2 if dtype is torch.bfloat16 else 1), shape[0], block_table.data_ptr(), block_table.shape[1],
+           (pointers.buffer_info()[0], n_caches, shape[1] * (2 if dtype is torch.bfloat16 else 1), shape[0], block_table.data_ptr(), block_table.shape[1],
             int(block_size), kv_lens.data_ptr(), draft_ptr, int(n), keep.data_ptr(), keep.shape[1], B,
             new_lens.data_ptr()), dev, stream)
     return new_lens
