@@ -839,8 +839,11 @@ static int decode_call(const uint16_t* q, const void* cache, int cache_format, i
   const int run = block_size & -block_size;
   const int most_rows = form.ctas == 2 ? 64 : 128;   // (of a pair's half slot)
   a.box_rows = idx || none || run < 8 ? 0 : (run < most_rows ? run : most_rows);
-  const bool fetch = a.box_rows && (!fp8 || form.ctas == 2);
-  a.fetch_bytes = fetch ? dsa::decode_fetch_bytes(a.box_rows, a.row_bytes, fp8 ? a.row_bytes : 2 * d_qk) : 0;
+  // (CTA pairs: where several blocks of query rows walk the same rows.  With one block the loads of all
+  // pairs' first tiles wait behind what is fetched: 32 x 512..16384 at 128 rows 61 us, 58 without;
+  // 1 x 131072 at 256 rows 62, 68 without, 8 x 4096..32768 at 512 rows 94 and 100)
+  const bool fetch = a.box_rows && !fp8 && (form.ctas == 1 || a.head_blocks > 1);
+  a.fetch_bytes = fetch ? dsa::decode_fetch_bytes(a.box_rows, a.row_bytes, 2 * d_qk) : 0;
   // With N = 0 every position is absent and the cache map is never used: it is encoded over q.
   bool mapped = true;
   if (!pair_fp8)

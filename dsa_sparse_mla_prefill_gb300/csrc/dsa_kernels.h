@@ -147,7 +147,7 @@ struct DecodeArgs {
   const uint8_t* rows_base;   // the cache rows as bytes, and their pitch
   int row_bytes;
   int box_rows;               // rows that a page holds in one run: 8 .. 128, a power of two; 0 = gather rows
-  int fetch_bytes;            // fetched to L2 of each run by the 64-head form (decode_fetch_bytes)
+  int fetch_bytes;            // fetched to L2 of each run by the 64-head form and by pairs (decode_fetch_bytes)
   const int32_t* block_table; // [B, max_blocks]
   const int32_t* kv_lens;     // [B]
   const int32_t* idx;         // [B, ld] positions, or null: every position < kv_len

@@ -25,14 +25,16 @@
 // rows, three and four 102; one ring of five with P in two places 111.)  P has one place, whose
 // four columns of 64 keys are handed over one by one (with P handed over as a whole the three
 // slots less would have cost more than they give).  A request's O leaves through the place of P
-// while the next one's first QK runs.  The scheduling warp asks L2 for the boxes of a tile more
-// than a tile ahead of its loads.
+// while the next one's first QK runs.  Where several pairs walk the same rows, their scheduling
+// warps ask L2 for the boxes of a tile more than a tile ahead of its loads, each for its share (not
+// kept: line by line, 96 us against 94 on 8 x 4096..32768; a ring slot's next chunk, 95).
 //
 // Split over the length, join and the rows of absent keys as in paged_decode.cuh; a range of
 // tiles is walked by the pairs of all row blocks at the same time.  A tile takes some 5200 cycles
 // (its MMAs 4352), a range 7000 to its first scores, a request's change some 5000, the join 7 us:
-// 8 x 4096..32768 at 512 rows 93 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
-// 61 (27 at the copy rate), 1 x 131072 at 256 rows 62 (38).
+// 8 x 4096..32768 at 512 rows 94 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
+// 58 (27 at the copy rate; 8300 cycles a tile, four slots of K in flight from HBM), 1 x 131072 at
+// 256 rows 62 (38).
 // FP8 rows: 24 x 1024..16384 at 256 rows 119 us (one CTA per 32 rows 283), 12000 cycles a tile
 // for the conversion: see there.
 #include <cfloat>
@@ -509,11 +511,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         const bool all = __all_sync(0xffffffffu, there8 == 0xffu);
         __syncwarp();
         // the boxes of the tile one back, more than a tile ahead of its loads, to L2: by each CTA its share
-        if (fetch >= 0)
+        if (!F8 && fetch >= 0)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.rows_base + (int64_t)fetch * a.row_bytes),
                        "r"(a.fetch_bytes)
                        : "memory");
-        if (a.fetch_bytes) {
+        if (!F8 && a.fetch_bytes) {
           fetch = rows[r * TK + (lane & (TK / a.box_rows - 1)) * a.box_rows];   // of box `lane`
           if (lane >= TK / a.box_rows || lane % sharers != share || fetch > a.N - a.box_rows) fetch = -1;
         }
