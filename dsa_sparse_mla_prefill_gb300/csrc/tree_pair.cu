@@ -35,7 +35,7 @@
 // 8 x 4096..32768 at 512 rows 94 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
 // 58 (27 at the copy rate; 8300 cycles a tile, four slots of K in flight from HBM), 1 x 131072 at
 // 256 rows 62 (38).
-// FP8 rows: 24 x 1024..16384 at 256 rows 119 us (one CTA per 32 rows 283), 12000 cycles a tile
+// FP8 rows: 24 x 1024..16384 at 256 rows 117 us (one CTA per 32 rows 283), 12000 cycles a tile
 // for the conversion: see there.
 #include <cfloat>
 
@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int NTHREADS = F8 ? 896 : 640, REGS = F8 ? 72 : 96;   // registers at launch
   static constexpr int NPROD = F8 ? 2 * NSLOT : NSLOT;
   static constexpr int W_PV = F8 ? 11 : 18, W_LOAD = F8 ? 12 : 11;
-  static constexpr int REGS_SOFTMAX = F8 ? 136 : 168, REGS_REST = F8 ? 32 : 48, REGS_PROD = 48;
+  static constexpr int REGS_SOFTMAX = F8 ? 120 : 168, REGS_REST = F8 ? 32 : 48, REGS_PROD = F8 ? 56 : 48;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST + (NTHREADS - 384) * REGS_PROD <= NTHREADS * REGS, "registers");
 };
 
@@ -263,17 +263,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       // land in the upper half of that place and the rows' scales at its start, by boxes or, from
       // pages without runs and in tiles with missing keys, by 16-byte copies (eight rows x 64
       // bytes to an instruction).  The warp converts them by the arithmetic of the dequantize
-      // kernel and stores them, in order, as the bf16 rows would have landed: what a store covers
-      // has been read.  The RoPE columns are copied.  Every row is converted twice, for K and for
+      // kernel and stores them as the bf16 rows would have landed: what a store covers has been
+      // read.  The RoPE columns are copied.  Every row is converted twice, for K and for
       // V, whose slots are needed a tile apart.
       //
-      // What bounds it: a slot's way from the MMAs that free it to the ones that read it again
-      // (wait 0.7k cycles, codes landing 1.2k, conversion 2k with 14 warps at it, hand-over 0.6k),
-      // times 17 slots' worth a tile in seven slots.  On 24 x 1024..16384 at 256 rows, 119 us:
-      // without the loads it would take 103, without the arithmetic no less; all by 16-byte copies
-      // 122 (load-store wavefronts 62 % of peak); half or all of the codes through registers,
-      // ahead of the free slot, 137 to 160 (a load's data in flight takes room in 28 KB of L1);
-      // one warp a slot 170; four warps on every slot in turn 185.
+      // What bounds it: shared memory, some 85 % of whose cycles are taken (load-store 49 %: codes
+      // read, rows stored; operands of the MMAs 27 %; codes landing), and so a slot's way from one
+      // use to the next: free 0.4k cycles, asked for 0.7k, landed 1k, converted 2.4k, handed over
+      // 0.8k.  On 24 x 1024..16384 at 256 rows, 117 us: without the loads it would take 103, without
+      // the arithmetic no less; all by 16-byte copies 122; half or all of the codes through
+      // registers, ahead of the free slot, 137 to 160 (a load's data in flight takes room in 28 KB
+      // of L1); one warp a slot 170; four warps on every slot in turn 185.
       // ----------------------------------------------------------------
       const int own = (warp - W_LOAD) >> 1, half = (warp - W_LOAD) & 1;
       const bool is_k = own < NK;
@@ -302,12 +302,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         const int block = is_k ? st >> 1 : 2 * (st & 1) + rank;
         const int at = is_k ? 64 * st : 128 * block + 64 * half;
         if (box) {
+          const int r = lane * a.box_rows, x = r < 64 ? rr[r] : 0;
           if (!poll(B_EMPTY + own, (used & 1) ^ 1)) break;
+          // (whatever has landed before, the phase waits for this arrival)
           if (lane == 0) mbar_arrive_expect_tx(&bars[b_raw], is_rope ? 64 * 128 : 64 * (64 + 16));
-          __syncwarp();
-          const int r = lane * a.box_rows;
           if (r < 64) {
-            const int x = rr[r];
             if (is_rope) {
               load_2d_hint(base + r * 128, &a.tmap_box, 528, x, &bars[b_raw], policy);
             } else {
@@ -352,21 +351,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
             }
             cp_async_wait_all();
           }
+          uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const uint4 w[2] = {lds128(raw + i * 512u), lds128(raw + (i + 1) * 512u)};
-            __syncwarp();
+          for (int i = 0; i < 8; ++i) w[i] = lds128(raw + i * 512u);
+          __syncwarp();   // (all is read)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float s = __shfl_sync(0xffffffffu, scale[i >> 2], 8 * ((i + k) & 3) + g);
-              uint32_t v[8];
-              e4m3x4_dequant_bf16x4(w[k].x, s, v[0], v[1]);
-              e4m3x4_dequant_bf16x4(w[k].y, s, v[2], v[3]);
-              e4m3x4_dequant_bf16x4(w[k].z, s, v[4], v[5]);
-              e4m3x4_dequant_bf16x4(w[k].w, s, v[6], v[7]);
-              sts128(dst + (i + k) * 1024u + lo, v[0], v[1], v[2], v[3]);
-              sts128(dst + (i + k) * 1024u + hi, v[4], v[5], v[6], v[7]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float s = __shfl_sync(0xffffffffu, scale[i >> 2], 8 * (i & 3) + g);
+            uint32_t v[8];
+            e4m3x4_dequant_bf16x4(w[i].x, s, v[0], v[1]);
+            e4m3x4_dequant_bf16x4(w[i].y, s, v[2], v[3]);
+            e4m3x4_dequant_bf16x4(w[i].z, s, v[4], v[5]);
+            e4m3x4_dequant_bf16x4(w[i].w, s, v[6], v[7]);
+            sts128(dst + i * 1024u + lo, v[0], v[1], v[2], v[3]);
+            sts128(dst + i * 1024u + hi, v[4], v[5], v[6], v[7]);
           }
         }
         ++used;
