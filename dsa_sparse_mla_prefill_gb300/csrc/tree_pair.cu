@@ -267,10 +267,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       // read.  The RoPE columns are copied.  Every row is converted twice, for K and for
       // V, whose slots are needed a tile apart.
       //
-      // What bounds it: shared memory, some 85 % of whose cycles are taken (load-store 49 %: codes
-      // read, rows stored; operands of the MMAs 27 %; codes landing), and so a slot's way from one
-      // use to the next: free 0.4k cycles, asked for 0.7k, landed 1k, converted 2.4k, handed over
-      // 0.8k.  On 24 x 1024..16384 at 256 rows, 117 us: without the loads it would take 103, without
+      // What bounds it: a slot's way from one use to the next, 5000 cycles for 17 uses a tile in
+      // seven slots (free 400, asked for 700, landed 1000, converted 2400 beside the other warps,
+      // handed over 800), the load-store pipe at half of its peak.  On 24 x 1024..16384 at 256 rows, 117 us: without the loads it would take 103, without
       // the arithmetic no less; all by 16-byte copies 122; half or all of the codes through
       // registers, ahead of the free slot, 137 to 160 (a load's data in flight takes room in 28 KB
       // of L1); one warp a slot 170; four warps on every slot in turn 185.
