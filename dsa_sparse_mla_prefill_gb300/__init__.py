@@ -907,7 +907,7 @@ def _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm):
 
 def _rows_like(t, x, name):
     """t, a tensor of x's shape, dtype and device."""
-    if not isinstance(t, _torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.device != x.device:
+    if not isinstance(t, _torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have the shape, dtype and device of what it belongs to")
     return t
 
@@ -973,30 +973,31 @@ def dsa_qk_norm_rope_gradient(q_grad, k_grad, q, k, q_weight, k_weight, position
     dev, f32, w_f32, T, d, n, pos, Hq, Hk = _norm_call(q, k, q_weight, k_weight, positions, freqs, d_norm)
     torch = _torch
     device = (k if q is None else q).device
-    args, outs, weights = [], [], []
-    for x, g, name, H in ((q, q_grad, "q", Hq), (k, k_grad, "k", Hk)):
+
+    def side(x, g, name, H):
+        """(the library's arguments, gradient, weight's gradient, its address) of q or k"""
         if x is None:
             if g is not None:
                 raise ValueError(f"{name}_grad without its input")
-            args += (None, 0, 0, None, 0, 0, None, 0)
-            outs.append(None)
-            weights.append(None)
-            continue
+            return (None, 0, 0, None, 0, 0, None, 0), None, None, None
         gs, xs = _row_strides(_rows_like(g, x, name + "_grad"), name + "_grad"), _row_strides(x, name)
         out = _empty(x.shape, x.dtype, device, stream)
-        args += (g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), H)
-        outs.append(out)
         # (no rows: the library leaves the sums alone)
-        weights.append(_empty((n,), torch.float32, device, stream) if H else torch.zeros(n, dtype=torch.float32, device=device))
+        dw = _empty((n,), torch.float32, device, stream) if H else torch.zeros(n, dtype=torch.float32, device=device)
+        return (g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), H), out, dw, dw.data_ptr()
+    q_args, gq, gqw, gqw_ptr = side(q, q_grad, "q", Hq)
+    k_args, gk, gkw, gkw_ptr = side(k, k_grad, "k", Hk)
     if workspace is None:
-        workspace = _empty((dsa_qk_norm_rope_gradient_workspace(n),), torch.uint8, device, stream)
+        nbytes = dsa_qk_norm_rope_gradient_workspace(n)
+        workspace = _empty((nbytes,), torch.uint8, device, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    else:
+        nbytes = workspace.numel()
     _queue(lib().dsa_qk_norm_rope_gradient, "dsa_qk_norm_rope_gradient",
-           (*args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32, pos, T,
-            d, n, eps, freqs, *(None if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
-            workspace.numel()), dev, stream)
-    return (*outs, *weights)
+           (*q_args, *k_args, f32, None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(), w_f32,
+            pos, T, d, n, eps, freqs, gqw_ptr, gkw_ptr, workspace.data_ptr(), nbytes), dev, stream)
+    return gq, gk, gqw, gkw
 
 
 # ---------------------------------------------------------------------------
