@@ -266,10 +266,10 @@ constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is 
 // keys of a tile, CTAs of a block.  Many rows of a tree are blocks of 128 to a CTA pair
 // (tree_pair.cu), fewer as many heads would be.  In us, one CTA against a pair, for 32 requests of
 // 512..16384 keys and for one of 777:
-//   bf16  32 rows  51 : 59   17 : 18      FP8  32 rows  57 : 80   17 : 22
-//         48       69 : 59   22 : 18           64       93 : 82   17 : 23
-//         64       71 : 61   22 : 19           80      128 : 83   19 : 23
-//         80       92 : 62   24 : 19          128      165 : 84   19 : 23
+//   bf16  32 rows  51 : 54   17 : 18      FP8  32 rows  57 : 81   17 : 22
+//         48       69 : 55   22 : 18           64       93 : 82   17 : 23
+//         64       71 : 56   22 : 19           80      128 : 82   19 : 23
+//         80       92 : 57   24 : 19          128      165 : 82   19 : 24
 struct DecodeForm {
   int rows, keys, ctas;
 };
