@@ -600,6 +600,33 @@ def test_tree_graphs_at_once():
         t.check(o)
 
 
+def test_calls_from_two_threads():
+    """Two host threads with a stream each, calling the operators at the same time."""
+    import threading
+    ts = [Tree(40, [900, 33, 2000], 4, 16), Tree(41, [1500, 260], 9, 16, fmt="fp8", bs=64)]
+    ns = [Norm(42, 300, 4, 2, 192), Norm(43, 77, 8, 1, 128, None, 64, "half", F32)]
+    want = [(*t.run(), *c.forward(), *c.gradient()) for t, c in zip(ts, ns)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = (*ts[i].run(), *ns[i].forward(), *ns[i].gradient())
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong
+    for t, w in zip(ts, want):
+        t.check(w[:2])
+
+
 @pytest.mark.parametrize("most", [300, 1500])
 @pytest.mark.parametrize("n,H", [(4, 8), (3, 16), (8, 16)])
 def test_tree_many_requests(n, H, most):
