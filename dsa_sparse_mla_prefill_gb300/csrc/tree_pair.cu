@@ -771,6 +771,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       if (!group()) return false;
       const bool live = token < done.w;   // (a padding token's row is zeros)
       const float l = live ? (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]) : 0.f;
+      // (all four warps have read: another part may end right behind this one, and nothing else would
+      // keep a warp's sums of that one from this one's readers)
+      if (!group()) return false;
       const float inv = l != 0.f ? 1.0f / l : 0.f;
       const bool is_part = (done.y & F_PART) != 0, there = q_row < a.H;
       const int64_t slot_row = (int64_t)(2 * range + ((done.y & F_SLOT1) ? 1 : 0)) * (2 * ROWS * a.head_blocks) + q_row;
