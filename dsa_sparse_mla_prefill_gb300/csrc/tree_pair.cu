@@ -80,8 +80,8 @@ constexpr uint32_t OFF_P = OFF_Q + 9 * Q_CHUNK;
 constexpr uint32_t OFF_ROWS = OFF_P + 4 * P_COLUMN;
 constexpr uint32_t OFF_META = OFF_ROWS + NI * TK * 4u;
 constexpr uint32_t OFF_VALID = OFF_META + NI * 16u;
-constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums
-constexpr uint32_t OFF_BAR = OFF_RED + 3u * 4u * ROWS * 4u;
+constexpr uint32_t OFF_RED = OFF_VALID + NI * 32u;  // [parity][part][row] maxima, [part][row] sums of each kind
+constexpr uint32_t OFF_BAR = OFF_RED + 4u * 4u * ROWS * 4u;
 constexpr int NBAR = 61;
 constexpr uint32_t OFF_MISC = OFF_BAR + (NBAR + 1) / 2 * 16u;
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 64u + 1024u;
@@ -759,22 +759,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       grp_phase ^= 1u;
       return ok;
     };
-    float m_run = -FLT_MAX, l_run = 0.f;   // (the lowest finite value, so that no difference of two is NaN)
+    // Sums of the weights as they are, for the log-sum-exp, and as P has them in bf16, which O is
+    // divided by: what their rounding adds to O is then in the divisor too.
+    float m_run = -FLT_MAX, l_run = 0.f, l_used = 0.f;   // (the lowest finite value, so that no difference of two is NaN)
     uint64_t word = 0;
-    // The part of a request that has ended: its last tile's meta, reference and this thread's sum.
+    // The part of a request that has ended: its last tile's meta, reference and this thread's sums.
     bool pending = false;
     int4 done = make_int4(0, 0, 0, 0);
-    float m_done = 0.f, l_done = 0.f;
+    float m_done = 0.f, l_done = 0.f, l_used_done = 0.f;
     int seg = 0;
     auto epilogue = [&]() -> bool {
       sums[part * ROWS + row] = l_done;
+      sums[(4 + part) * ROWS + row] = l_used_done;
       if (!group()) return false;
       const bool live = token < done.w;   // (a padding token's row is zeros)
-      const float l = live ? (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]) : 0.f;
+      auto sum_of = [&](const float* s) { return live ? (s[row] + s[ROWS + row]) + (s[2 * ROWS + row] + s[3 * ROWS + row]) : 0.f; };
+      const float l = sum_of(sums), used = sum_of(sums + 4 * ROWS);
       // (all four warps have read: another part may end right behind this one, and nothing else would
       // keep a warp's sums of that one from this one's readers)
       if (!group()) return false;
-      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      const float inv = used != 0.f ? 1.0f / used : 0.f;
       const bool is_part = (done.y & F_PART) != 0, there = q_row < a.H;
       const int64_t slot_row = (int64_t)(2 * range + ((done.y & F_SLOT1) ? 1 : 0)) * (2 * ROWS * a.head_blocks) + q_row;
       if (part == 0 && there) {
@@ -847,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       const int4 mt = meta[r];
       if (mt.y & F_FIRST) {
         m_run = -FLT_MAX;
-        l_run = 0.f;
+        l_run = l_used = 0.f;
         word = token < mt.w ? a.tree_mask[(int64_t)mt.x * a.n + token] : 0ull;
       }
       uint64_t vis = ~0ull;
@@ -895,6 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         alpha = exp2f(m_run - top);
         m_run = top;
         l_run *= alpha;
+        l_used *= alpha;
       }
       // O, which holds the P.V of the tile before then, in the new reference
       if (!(mt.y & F_FIRST) && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -943,11 +948,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       __syncwarp();
       if (lane == 0) arrive_even(pf0);
       if (threadIdx.x == 0) DSA_TRACE(a.tr, it, 6);
+      // (here, where nothing waits for it)
+      float u0 = 0.f, u1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) add2(u0, u1, u0, u1, __uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u));
+      l_used += u0 + u1;
       if (mt.y & F_LAST) {
         pending = true;
         done = mt;
         m_done = m_run;
         l_done = l_run;
+        l_used_done = l_used;
       }
     }
     if (pending) epilogue();

@@ -2,13 +2,14 @@
 ways that random inputs do not show.  GPU, against the 64-bit oracle or exact values.
 
 Tolerances are those of test_gpu_draft_step.py, or exact; the others are derived where
-they stand.
+they stand.  u = 2^-24, half a step of float32.
 """
 import numpy as np
 import pytest
 
-from gpu_util import need_gpu, torch
-from test_gpu_draft_step import Tree
+import oracle.dsa_oracle as O
+from gpu_util import bf, i32, need_gpu, torch
+from test_gpu_draft_step import BF, U, Tree, bad_count, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,37 @@ def test_tree_requests_that_end_behind_one_another(fmt, n, H, per_range):
     for _ in range(20):
         again = t.run()
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def rounds_by_much():
+    """x on bf16's grid whose exp(-x) rounds to bf16 up and down by most of half a step."""
+    x = O.bf16_to_f64(np.arange(0x3f00, 0x4080, dtype=np.uint16))          # 0.5 .. 4
+    p = np.exp(-x)
+    by = O.bf16_to_f64(O._f32_to_bf16_bits(p.astype(np.float32))) / p - 1
+    return float(x[by.argmax()]), float(x[by.argmin()])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,H", [(1, 16), (2, 16), (4, 16), (5, 16), (8, 32)])
+def test_tree_weights_that_round_alike(fmt, n, H):
+    """One key with weight 1 and 199 whose weights round to bf16 the same way, by nearly half a step: where all rows
+    are the same the result is that row whatever the weights, so what a weight's rounding adds to the sum of products
+    has to be in the sum it is divided by.  (Divided by the unrounded weights' sum it would be off by 2^-8 of itself,
+    a whole step of bf16 below 2.)  The log-sum-exp is of the weights as they are: 200 additions, the 2-ulp
+    exponential and logarithm, 300 u relative to the sum."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    value = 255 / 128                                   # all mantissa bits: steps are 2^-8 of it
+    for x in rounds_by_much():
+        rows = np.zeros((256, 576))
+        rows[:, :512] = value
+        rows[1:, 512] = -x
+        kv = O._f32_to_bf16_bits(rows.astype(np.float32))
+        cache = bf(kv) if fmt == "bf16" else torch.from_numpy(O.kv_fp8_quantize(kv, 64)).cuda()
+        q = torch.zeros(1, n, H, 576, dtype=BF, device="cuda")
+        q[..., 512] = 1
+        mask = torch.full((1, n), (1 << n) - 1, device="cuda")
+        out, lse = dsa.dsa_tree_decode(q, cache, i32([list(range(4))]), i32([200]), mask, 64, 1.0)
+        assert torch.equal(out, torch.full_like(out, value)), (out.float().min(), out.float().max())
+        want = np.log(1 + 199 * np.exp(-x))
+        assert np.abs(f64(lse) - want).max() <= 300 * U + 4 * U * want
+        assert bad_count() == 0
