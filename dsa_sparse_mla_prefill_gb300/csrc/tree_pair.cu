@@ -482,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
           }
         }
         if (!doze(B_IDXE + r, ((it / NI) & 1) ^ 1)) break;
-        if (!looked && (j + 1) * TK > context) {
+        if (!looked && j * TK > context - TK) {   // (the last tile may end past 2^31)
           uint64_t any = 0;
           for (int i = lane; i < drafted; i += 32) any |= a.tree_mask[(int64_t)b * a.n + i];
           seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
@@ -519,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
         const bool first = enter, last = (it == nt - 1) || (j == n - 1);
         if (lane == 0) {
           int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) | (all && a.box_rows > 0 ? F_BOX : 0);
-          if (all && (j + 1) * TK <= context) flags |= F_FULL;
+          if (all && j * TK <= context - TK) flags |= F_FULL;
           if (last) {
             const bool whole = (seg > 0 || from_start) && j == n - 1;
             if (!whole) flags |= F_PART | (seg > 0 ? F_SLOT1 : 0);

@@ -8,8 +8,8 @@ import numpy as np
 import pytest
 
 import oracle.dsa_oracle as O
-from gpu_util import bf, i32, need_gpu, torch
-from test_gpu_draft_step import BF, U, Tree, bad_count, f64
+from gpu_util import bf, f32, i32, need_gpu, torch
+from test_gpu_draft_step import BF, U, Tree, bad_count, f64, signed
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,29 @@ def test_tree_weights_that_round_alike(fmt, n, H):
         want = np.log(1 + 199 * np.exp(-x))
         assert np.abs(f64(lse) - want).max() <= 300 * U + 4 * U * want
         assert bad_count() == 0
+
+
+@pytest.mark.parametrize("n,H", [(2, 16), (3, 16)])
+def test_tree_last_positions_of_31_bits(n, H):
+    """A request that fills a table of 2^31 - 1 positions and more: its drafted tokens, in the last tile, are seen."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    bs = 1 << 16
+    blocks = (1 << 31) // bs
+    rng = np.random.default_rng(n)
+    rows = np.zeros((2 * bs, 576), dtype=np.float32)    # (the context's scores are 0)
+    last = (1 << 31) - 1 - n                            # first drafted position
+    at = bs + last % bs                                 # its row: the last block is the second of the cache's
+    drafted = rng.standard_normal((n, 576)).astype(np.float32)
+    drafted[:, 512] = 60                                # (a score of 60 outweighs 2^31 of 0 by e^38)
+    rows[at:at + n] = drafted
+    kv = O._f32_to_bf16_bits(rows)
+    bt = np.zeros((1, blocks), dtype=np.int32)
+    bt[0, -1] = 1
+    q = torch.zeros(1, n, H, 576, dtype=BF, device="cuda")
+    q[..., 512] = 1
+    mask = [1 << i for i in range(n)]                   # each sees itself alone
+    out, lse = dsa.dsa_tree_decode(q, bf(kv), i32(bt), i32([(1 << 31) - 1]), torch.from_numpy(signed([mask])).cuda(), bs, 1.0)
+    assert bad_count() == 0
+    want = O.bf16_to_f64(kv[at:at + n, :512])[None, :, None]
+    assert np.abs(f32(out) - want).max() <= 2.0 ** -8 * np.abs(want).max() + 1e-12
+    assert np.abs(f64(lse) - 60).max() <= 60 * 8 * U
