@@ -192,23 +192,34 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on `stream` (None: the current one) to write.  Another stream's is made
-    as that stream's own memory: the current stream's may have been freed there while its queued
-    kernels still use it, and nothing orders the call behind them.  The current stream, which the
-    caller most likely reads the tensor on, is recorded as its user."""
+def _other_stream(device, stream):
+    """The stream of a call on `stream` as torch's, None where that is the current one."""
     torch = _torch or _load_torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
+        return None
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == here.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):   # a handle: 0 and 1 are names of the default stream
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(here)
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # a handle: 0 and 1 are names of the default stream
+    return torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype, device, stream, zeros=False):
+    """A new tensor for a call on `stream` (None: the current one) to write, or of zeros that the
+    stream writes.  Another stream's is made as that stream's own memory: the current stream's may
+    have been freed there while its queued kernels still use it, and nothing orders the call behind
+    them.  The current stream, which the caller most likely reads the tensor on, is recorded as its
+    user."""
+    torch = _torch or _load_torch()
+    other = _other_stream(device, stream)
+    make = torch.zeros if zeros else torch.empty
+    if other is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -983,7 +994,7 @@ def dsa_qk_norm_rope_gradient(q_grad, k_grad, q, k, q_weight, k_weight, position
         gs, xs = _row_strides(_rows_like(g, x, name + "_grad"), name + "_grad"), _row_strides(x, name)
         out = _empty(x.shape, x.dtype, device, stream)
         # (no rows: the library leaves the sums alone)
-        dw = _empty((n,), torch.float32, device, stream) if H else torch.zeros(n, dtype=torch.float32, device=device)
+        dw = _empty((n,), torch.float32, device, stream, zeros=not H)
         return (g.data_ptr(), gs[0], gs[1], x.data_ptr(), xs[0], xs[1], out.data_ptr(), H), out, dw, dw.data_ptr()
     q_args, gq, gqw, gqw_ptr = side(q, q_grad, "q", Hq)
     k_args, gk, gkw, gkw_ptr = side(k, k_grad, "k", Hk)

@@ -9,7 +9,7 @@ import pytest
 
 import oracle.dsa_oracle as O
 from gpu_util import bf, f32, i32, need_gpu, torch
-from test_gpu_draft_step import BF, U, Tree, bad_count, f64, signed
+from test_gpu_draft_step import BF, U, Norm, Tree, bad_count, f64, signed
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,35 @@ def test_tree_last_positions_of_31_bits(n, H):
     want = O.bf16_to_f64(kv[at:at + n, :512])[None, :, None]
     assert np.abs(f32(out) - want).max() <= 2.0 ** -8 * np.abs(want).max() + 1e-12
     assert np.abs(f64(lse) - 60).max() <= 60 * 8 * U
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_gradient_of_a_side_without_heads_on_another_stream(as_handle):
+    """The weights' gradient of a side without heads is zeros, there in the order of the call's stream and that
+    stream's memory: not a block that the current stream's queued kernels still write."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    c = Norm(3, 40, 4, 2, 192)
+    c.x[0], c.g[0] = c.x[0][:, :0], c.g[0][:, :0]
+    want = c.gradient()
+    torch.cuda.synchronize()
+    pos = i32(c.pos)
+    s = torch.cuda.Stream()
+    for i in range(3):
+        with torch.cuda.stream(s):                      # (blocks of that stream that hold something else)
+            old = [torch.full((192,), 5.0, device="cuda") for _ in range(8)]
+        spare = [torch.full((192,), 3.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        blocks = {x.data_ptr() for x in spare}
+        torch.cuda._sleep(20_000_000)
+        for x in spare:
+            x.fill_(1)
+        del spare, x, old
+        got = dsa.dsa_qk_norm_rope_gradient(*c.g, *c.x, *c.w, pos, c.freqs, eps=c.eps, stream=s.cuda_stream if as_handle else s)
+        with torch.cuda.stream(s):
+            seen = got[2].clone()
+        s.synchronize()                                 # (the current stream still sleeps)
+        assert not torch.cuda.current_stream().query()
+        with torch.cuda.stream(s):
+            assert seen.tolist() == [0.0] * 192 and got[2].data_ptr() not in blocks
+        torch.cuda.synchronize()
+        assert torch.equal(got[3], want[3]) and (got[2] == 0).all()
