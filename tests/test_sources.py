@@ -33,3 +33,11 @@ def test_kernels_that_start_early_read_through_coherent_loads():
     assert len(early) >= 3
     found = {name: re.findall(r"__ldg\w*\s*\(|\.nc\b|__restrict__", text) for name, text in early.items()}
     assert not {name: f for name, f in found.items() if f}
+
+
+def test_signals_between_ctas_are_of_cluster_scope():
+    """An arrival on another CTA's barrier that releases at CTA scope, or a wait for one that acquires there, orders
+    nothing between the two."""
+    found = {name: re.findall(r"mbarrier\.arrive\S*\.cta\.shared::cluster\S*", text) for name, text in sources().items()}
+    assert not {name: f for name, f in found.items() if f}
+    assert "acquire.cta" not in sources()["tree_pair.cu"]     # (its waits are for both CTAs' arrivals)
