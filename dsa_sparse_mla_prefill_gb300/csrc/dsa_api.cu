@@ -1,5 +1,6 @@
 // C-ABI shim: argument validation, host-side request tables and kernel
 // launches for the entry points declared in include/dsa.h.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -20,26 +21,29 @@ __device__ unsigned int g_dsa_err[4];
 constexpr int kMaxDev = 64;
 
 struct DevInfo {
-  bool init = false;
-  int num_sms = 0;
-  unsigned int* err = nullptr;
+  std::atomic<bool> init{false};   // behind the others
+  std::atomic<int> num_sms{0};
+  std::atomic<unsigned int*> err{nullptr};
 };
 DevInfo g_dev[kMaxDev];
 
 // diagnostic timeline buffer (dsa_debug_trace)
 dsa::TraceArgs g_trace = {nullptr, 0};
 
-// Per-device set-up: SM count and the device address of the error counters.
+// Per-device set-up: SM count and the device address of the error counters.  (Every host thread
+// that comes before one has finished works out the same.)
 bool dev_info(DevInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
   DevInfo& d = g_dev[dev];
-  if (!d.init) {
-    if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+  if (!d.init.load(std::memory_order_acquire)) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_dsa_err) != cudaSuccess) return false;
-    d.err = static_cast<unsigned int*>(p);
-    d.init = true;
+    d.num_sms.store(n, std::memory_order_relaxed);
+    d.err.store(static_cast<unsigned int*>(p), std::memory_order_relaxed);
+    d.init.store(true, std::memory_order_release);
   }
   *out = &d;
   return true;

@@ -49,6 +49,7 @@
 // (the warps of a stream share every stage).
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "dsa_launch.cuh"
 
 namespace dsa {
 namespace grouped {
@@ -804,35 +805,10 @@ grouped_prefill_kernel(const __grid_constant__ GroupedArgs a) {
 template <int NC>
 static int launch_t(const GroupedArgs& a, int num_sms, cudaStream_t stream) {
   using C = Cfg;
-  static int attr_set[64] = {0};
-  static int max_clusters[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(grouped_prefill_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_BYTES) != cudaSuccess)
-      return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
-    cfg.blockDim = dim3(NTHREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grouped_prefill_kernel<NC>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = num_sms / 2;
-    }
-    max_clusters[dev] = n;
-    attr_set[dev] = 1;
-  }
+  static PerDevice done, pairs;
+  if (allow_smem(reinterpret_cast<const void*>(grouped_prefill_kernel<NC>), C::SMEM_BYTES, done) != 0) return -1;
   if (a.num_groups == 0) return 0;
-  int ncl = dev < 64 ? max_clusters[dev] : num_sms / 2;
+  int ncl = resident_pairs(grouped_prefill_kernel<NC>, 2 * (num_sms / 2), NTHREADS, C::SMEM_BYTES, pairs);
   if (ncl > a.num_groups) ncl = a.num_groups;
   grouped_prefill_kernel<NC><<<2 * ncl, NTHREADS, C::SMEM_BYTES, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;

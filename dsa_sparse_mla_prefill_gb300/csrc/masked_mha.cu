@@ -43,6 +43,7 @@
 //               the S columns it came from, and the epilogue.
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "dsa_launch.cuh"
 
 namespace dsa {
 namespace masked {
@@ -476,15 +477,8 @@ template <int DQK, int DV>
 static int launch_t(const MaskedArgs& a, cudaStream_t stream) {
   static_assert(Cfg<DQK, DV>::SMEM_BYTES <= 227u * 1024u, "shared memory budget");
   using C = Cfg<DQK, DV>;
-  static int attr_set[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(masked_mha_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_BYTES) != cudaSuccess)
-      return -1;
-    attr_set[dev] = 1;
-  }
+  static PerDevice done;
+  if (allow_smem(reinterpret_cast<const void*>(masked_mha_kernel<DQK, DV>), C::SMEM_BYTES, done) != 0) return -1;
   const long long grid = (long long)a.num_qtiles * a.H;
   if (grid == 0) return 0;
   masked_mha_kernel<DQK, DV><<<(unsigned)grid, NTHREADS, C::SMEM_BYTES, stream>>>(a);

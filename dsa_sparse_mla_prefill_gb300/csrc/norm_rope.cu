@@ -663,7 +663,7 @@ static int launch_t(NormArgs& a, bool gradient, int num_sms, cudaStream_t stream
   if (!gradient) {
     constexpr int CTAS = kForwardCtas<NP>;
     const uint32_t smem = staged_bytes<G>(a) + kForwardStages * Ahead<E, G, NP, RM, 1, 2>::STAGE_BYTES;
-    static int done[64] = {0};
+    static PerDevice done;
     if (allow_smem(reinterpret_cast<const void*>(norm_rope_kernel<E, G, NP, RM>), kMostSmem, done) != 0) return -1;
     const int ctas = share_ctas(a, (int64_t)CTAS * num_sms, NT / G);
     return launch_after(norm_rope_kernel<E, G, NP, RM>, dim3((unsigned)ctas), NT, smem, stream, a);
@@ -677,7 +677,7 @@ static int launch_t(NormArgs& a, bool gradient, int num_sms, cudaStream_t stream
     const uint32_t ahead = staged_bytes<G>(a) + kGradientStages<sizeof(E), NP> * Ahead<E, G, NP, RM, 2, 2>::STAGE_BYTES;
     const uint32_t sums = (uint32_t)(NT / 32 * a.d_norm * 4);
     if (ctas > 0) {   // (no tokens: the sums below are of nothing)
-      static int done[64] = {0};
+      static PerDevice done;
       if (allow_smem(reinterpret_cast<const void*>(norm_rope_gradient_kernel<E, G, NP, RM>), kMostSmem, done) != 0) return -1;
       const int r = launch_after(norm_rope_gradient_kernel<E, G, NP, RM>, dim3((unsigned)ctas), NT,
                                  ahead > sums ? ahead : sums, stream, a);

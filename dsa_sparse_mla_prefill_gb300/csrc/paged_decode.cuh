@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
 template <int HB, int NC, bool F8, bool TREE>
 static int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<HB, NC, F8>;
-  static int done[64] = {0};
+  static PerDevice done;
   if (allow_smem(reinterpret_cast<const void*>(decode_kernel<HB, NC, F8, TREE>), C::SMEM_BYTES, done) != 0) return -1;
   // (programmatic: the start, up to griddepcontrol.wait, overlaps the end of the kernel before)
   return launch_after(decode_kernel<HB, NC, F8, TREE>, dim3((unsigned)(a.groups * a.head_blocks)), C::NTHREADS, C::SMEM_BYTES, stream,

@@ -369,7 +369,7 @@ extern "C" int dsa_selftest_fetch(int rows, long long row_bytes, int read_bytes)
 
 // What allow_smem says of `smem` bytes for one kernel, and 10 more if it leaves an error pending.
 extern "C" int dsa_selftest_allow_smem(unsigned smem) {
-  static int done[64] = {0};
+  static dsa::PerDevice done;
   const int r = dsa::allow_smem(reinterpret_cast<const void*>(selftest_wait_kernel<true>), smem, done);
   return (r == 0 ? 0 : 1) + (cudaPeekAtLastError() == cudaSuccess ? 0 : 10);
 }

@@ -53,6 +53,7 @@
 //   Warps 0-3 run at 176 registers, warps 4-23 at 56 (768 threads at 80).
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "dsa_launch.cuh"
 
 namespace dsa {
 namespace sparse {
@@ -1004,15 +1005,8 @@ sparse_prefill_kernel(const __grid_constant__ SparseArgs a) {
 template <int H, int NC, bool F8, bool STREAM>
 static int launch_t(const SparseArgs& a, int num_sms, cudaStream_t stream) {
   using C = Cfg<H, NC, F8>;
-  static int attr_set[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(sparse_prefill_kernel<H, NC, F8, STREAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_BYTES) != cudaSuccess)
-      return -1;
-    attr_set[dev] = 1;
-  }
+  static PerDevice done;
+  if (allow_smem(reinterpret_cast<const void*>(sparse_prefill_kernel<H, NC, F8, STREAM>), C::SMEM_BYTES, done) != 0) return -1;
   const int grid = a.T < num_sms ? a.T : num_sms;
   sparse_prefill_kernel<H, NC, F8, STREAM><<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;

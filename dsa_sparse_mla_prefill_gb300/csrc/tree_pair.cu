@@ -984,30 +984,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
 
 template <int NC, bool F8>
 static int launch_t(DecodeArgs& a, cudaStream_t stream) {
-  static int done[64] = {0}, clusters[64] = {0};
+  static PerDevice done, pairs;
   if (allow_smem(reinterpret_cast<const void*>(tree_pair_kernel<NC, F8>), SMEM_BYTES, done) != 0) return -1;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  // pairs that the GPU holds at a time: a range more would run behind all others
-  int most = dev < 64 ? clusters[dev] : 0;
-  if (most == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kDecodeMaxCtas);
-    cfg.blockDim = dim3(Cfg<F8>::NTHREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&most, tree_pair_kernel<NC, F8>, &cfg) != cudaSuccess || most < 1) {
-      cudaGetLastError();
-      most = kDecodeMaxCtas / 2;
-    }
-    if (dev < 64) clusters[dev] = most;
-  }
-  most = most / a.head_blocks;
+  // (a range more than the GPU holds at a time would run behind all others)
+  const int most = resident_pairs(tree_pair_kernel<NC, F8>, kDecodeMaxCtas, Cfg<F8>::NTHREADS, SMEM_BYTES, pairs) / a.head_blocks;
   if (a.groups > most) a.groups = most > 0 ? most : 1;
   return launch_after(tree_pair_kernel<NC, F8>, dim3((unsigned)(2 * a.groups * a.head_blocks)), Cfg<F8>::NTHREADS, SMEM_BYTES, stream, a);
 }

@@ -4,6 +4,10 @@ ways that random inputs do not show.  GPU, against the 64-bit oracle or exact va
 Tolerances are those of test_gpu_draft_step.py, or exact; the others are derived where
 they stand.  u = 2^-24, half a step of float32.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -136,3 +140,58 @@ def test_gradient_of_a_side_without_heads_on_another_stream(as_handle):
             assert seen.tolist() == [0.0] * 192 and got[2].data_ptr() not in blocks
         torch.cuda.synchronize()
         assert torch.equal(got[3], want[3]) and (got[2] == 0).all()
+
+
+FIRST_USE = """
+import sys, threading
+sys.path[:0] = [{root!r}, {tests!r}]
+import os
+import subprocess
+import sys
+
+import numpy as np
+import torch
+import dsa_sparse_mla_prefill_gb300 as dsa
+import oracle.dsa_oracle as O
+from gpu_util import bf, i32
+from test_gpu_draft_step import Norm, Tree, bad_count
+sizes = [(4, 16, 'bf16'), (2, 16, 'bf16'), (8, 16, 'fp8'), (3, 16, 'fp8')]
+trees = [Tree(i, [900, 33, 600], n, H, fmt=fmt, bs=64) for i, (n, H, fmt) in enumerate(sizes) for _ in range(2)]
+norms = [Norm(9, 50, 4, 2, 192), Norm(9, 50, 4, 2, 192)]
+moved = torch.arange(64 * 576, device='cuda').reshape(64, 576).to(torch.bfloat16)
+before, table, lens, keep = moved.clone(), i32([[0]]), i32([9]), i32([[1, 3, -1, -1]])
+work = [t.run for t in trees] + [c.forward for c in norms] + [c.gradient for c in norms]
+work.append(lambda: dsa.dsa_kv_keep(moved, table, lens, keep, 64, 4))
+start, got, streams = threading.Barrier(len(work)), [None] * len(work), [torch.cuda.Stream() for _ in work]
+torch.cuda.synchronize()
+
+def one(i):
+    with torch.cuda.stream(streams[i]):
+        start.wait()
+        try:
+            got[i] = work[i]()
+        except Exception as e:
+            got[i] = e
+threads = [threading.Thread(target=one, args=(i,)) for i in range(len(work))]
+for x in threads: x.start()
+for x in threads: x.join()
+torch.cuda.synchronize()
+wrong = [(i, g) for i, g in enumerate(got) if isinstance(g, Exception)]
+assert not wrong, wrong
+for t, g in zip(trees, got): t.check(g)
+for c, g in zip(norms, got[8:10]): c.check_forward(g)
+for c, g in zip(norms, got[10:12]): c.check_gradient(g)
+before[[5, 6]] = before[[6, 8]]
+assert got[12].tolist() == [7] and torch.equal(moved, before) and bad_count() == 0
+print('all right')
+"""
+
+
+def test_first_calls_of_a_process_from_several_threads():
+    """Every operator's first call at the same time as the others', two of each kernel: what a call keeps for later
+    ones (the devices, attributes, the tensor maps' encoder) is complete for whoever uses it."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", FIRST_USE.format(root=os.path.dirname(here), tests=here)], capture_output=True,
+                           text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.strip().endswith("all right"), r.stderr[-2000:]

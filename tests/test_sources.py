@@ -41,3 +41,14 @@ def test_signals_between_ctas_are_of_cluster_scope():
     found = {name: re.findall(r"mbarrier\.arrive\S*\.cta\.shared::cluster\S*", text) for name, text in sources().items()}
     assert not {name: f for name, f in found.items() if f}
     assert "acquire.cta" not in sources()["tree_pair.cu"]     # (its waits are for both CTAs' arrivals)
+
+
+def test_what_a_call_keeps_may_be_set_by_several_threads():
+    """Local variables that outlive a call are constants or atomic: calls run without the interpreter's lock, so the
+    first ones of a process may come from several threads at once."""
+    plain = re.compile(r"^\s+static\s+(?!const\b|constexpr\b|__device__|(?:dsa::)?PerDevice\b)[\w:<>]+\s+\w+\s*[\[=;{].*", re.M)
+    found = {name: plain.findall(text) for name, text in sources().items()}
+    assert not {name: f for name, f in found.items() if f}
+    assert "using PerDevice = std::atomic<int>[64];" in sources()["dsa_launch.cuh"]
+    info = re.search(r"struct DevInfo \{(.*?)\n\};", sources()["dsa_api.cu"], re.S).group(1)
+    assert info.count("std::atomic<") == info.count(";") == 3
