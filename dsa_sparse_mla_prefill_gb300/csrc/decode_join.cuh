@@ -1,5 +1,5 @@
 // The split of a paged decode call into ranges of key tiles, and the kernel that joins
-// the parts of requests that a range border cuts (see paged_decode.cu).
+// the parts of requests that a range border cuts (see paged_decode.cuh).
 #pragma once
 #include <cstdint>
 

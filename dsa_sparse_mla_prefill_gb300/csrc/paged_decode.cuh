@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<HB, NC, F8>::NTHREADS, 1) decode_kernel(co
                          : "memory");
           fetch = fetch_next;
           fetch_next = __shfl_sync(0xffffffffu, row[0], (lane * a.box_rows / 4) & 31);   // of box `lane`
-          if (!box || a.fetch_bytes == 0 || lane >= BK / a.box_rows || (TREE ? lane % a.head_blocks : lane & (a.head_blocks - 1)) != hb)   // (1 or 2 CTAs without a tree)
+          if (!box || a.fetch_bytes == 0 || lane >= BK / a.box_rows || (lane & (a.head_blocks - 1)) != hb)   // (1 or 2 CTAs)
             fetch_next = -1;
         }
         const bool first = enter;
