@@ -13,7 +13,7 @@ import pytest
 
 import oracle.dsa_oracle as O
 from gpu_util import bf, f32, i32, need_gpu, torch
-from test_gpu_draft_step import BF, U, Norm, Tree, bad_count, f64, signed
+from test_gpu_draft_step import BF, F32, U, Norm, Tree, ancestors, bad_count, f64, signed
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +195,68 @@ def test_first_calls_of_a_process_from_several_threads():
         r = subprocess.run([sys.executable, "-c", FIRST_USE.format(root=os.path.dirname(here), tests=here)], capture_output=True,
                            text=True, timeout=300)
         assert r.returncode == 0 and r.stdout.strip().endswith("all right"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,d_norm", [(100003, 1, 0, 128, None), (20001, 5, 3, 64, None), (25001, 4, 1, 256, None),
+                                              (100001, 1, 0, 576, 512), (20001, 5, 2, 70, None)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_gradient_counts_every_row_once(T, Hq, Hk, d, d_norm, dtype):
+    """Inputs and gradients of 1 and -1, weights of 1: a row's r is 1 within 4 u and its terms are 1 or -1, so a row
+    left out or added twice changes every column's sum by one.  The sums are integers; a lane adds the rows of its
+    share of at least 152 x 8 workers one after another, its warp's lanes, its CTA's warps and the CTAs' partial sums
+    (38 and 8 in a column) are less than 60 additions more: (rows / 1216 + 64) u of the number of rows, which is below
+    one."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    rng = np.random.default_rng(d)
+
+    def signs(H):
+        t = torch.from_numpy(rng.integers(0, 2, (T, H, d), dtype=np.int8)).cuda()
+        return (t * 2 - 1).to(dtype)
+    n = d_norm or d
+    one = torch.ones(n, dtype=dtype, device="cuda")
+    x = [signs(H) if H else None for H in (Hq, Hk)]
+    g = [signs(H) if H else None for H in (Hq, Hk)]
+    got = dsa.dsa_qk_norm_rope_gradient(*g, *x, one, one if Hk else None, None, None, eps=0.0, d_norm=d_norm)
+    for a, b, w in zip(x, g, got[2:]):
+        if a is None:
+            assert w is None
+            continue
+        want = (a[..., :n] * b[..., :n]).double().sum((0, 1))
+        rows = a.shape[0] * a.shape[1]
+        tol = (rows / 1216 + 64) * U * rows
+        assert tol < 1
+        assert (w.double() - want).abs().max().item() <= tol
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,H", [(2, 16), (5, 16), (4, 64)])
+def test_tree_chain_is_the_decode_steps(fmt, n, H):
+    """A chain of drafted tokens attended at once is what attending them one after another gives: both within the
+    decode step's bound (test_gpu_decode_step.py) of the same exact result, element by element, so within two of it of
+    each other."""
+    import dsa_sparse_mla_prefill_gb300 as dsa
+    t = Tree(n, [300, 1029, 64, 4000], n, H, fmt=fmt, bs=64, mask=[ancestors(range(-1, n - 1))] * 4)
+    got = t.run()
+    t.check(got)
+    q, cache, bt, lens, _, bs, scale = t.args()
+    tiles = -(-int(t.lens.max()) // 128)
+    for i in range(n):
+        out, lse = dsa.dsa_paged_decode(q[:, i].contiguous(), cache, bt, lens - (n - 1 - i), bs, scale)
+        ref = O.paged_decode(t.q[:, i], t.values, t.bt, t.lens - (n - 1 - i), bs, scale)
+        score = 1155 * U * ref["mass"]
+        tol = (2 * (2.0 ** -8 + score) * (1 + 2.0 ** -7))[..., None] * ref["spread"] + 2.0 ** -8 * np.abs(ref["out"]) + 1e-30
+        ltol = score + 2.0 ** -21 + (tiles + 32) * U + 4 * U * np.abs(ref["lse"])
+        assert (np.abs(f32(out) - ref["out"]) <= tol).all() and (np.abs(f64(lse) - ref["lse"]) <= ltol).all()
+        assert (np.abs(f32(got[0][:, i]) - f32(out)) <= 2 * tol).all() and (np.abs(f64(got[1][:, i]) - f64(lse)) <= 2 * ltol).all()
+    assert bad_count() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,H", [(2, 16), (8, 16), (8, 32)])
+def test_tree_one_long_request_among_short_ones(fmt, n, H):
+    """A request that most of the ranges share while the batch's average is a few: its many parts are joined whatever
+    the join was launched for."""
+    lens = [300] * 31
+    lens.insert(11, 40000)
+    t = Tree(n, lens, n, H, fmt=fmt, bs=64)
+    t.check(t.run())
