@@ -265,11 +265,16 @@ constexpr int kDecodeMaxCtas = 152;   // one per SM; also what the workspace is 
 // How a decode or tree call is cut: query rows of a block (the CTAs that walk the same keys),
 // keys of a tile, CTAs of a block.  Many rows of a tree are blocks of 128 to a CTA pair
 // (tree_pair.cu), fewer as many heads would be.  In us, one CTA against a pair, for 32 requests of
-// 512..16384 keys and for one of 777:
-//   bf16  32 rows  51 : 54   17 : 18      FP8  32 rows  57 : 81   17 : 22
-//         48       69 : 55   22 : 18           64       93 : 82   17 : 23
-//         64       71 : 56   22 : 19           80      128 : 82   19 : 23
-//         80       92 : 57   24 : 19          128      165 : 82   19 : 24
+// 512..16384 keys, one of 777 and one of 131072 (bf16 from 48 rows on: with the CTA of 64 rows
+// that trees had before the pairs):
+//   bf16  32 rows  52 : 55   17 : 17   51 : 50      FP8  32 rows  56 : 82   16 : 22   56 : 71
+//         48       69 : 56   22 : 18                     48       92 : 82   16 : 23   84 : 73
+//         64       71 : 57   22 : 19                     64       92 : 82   16 : 24   85 : 74
+//         80       92 : 57   24 : 19                     80      128 : 83   18 : 24  114 : 74
+//                                                        128     164 : 83   18 : 24  140 : 74
+// FP8 calls of 33 to 64 rows are the ones where neither is ahead everywhere: rows alone decide
+// because lengths are on the device, where the host cannot look, and the short call, whose time
+// is all latency, would lose half of itself where the long ones gain an eighth.
 struct DecodeForm {
   int rows, keys, ctas;
 };

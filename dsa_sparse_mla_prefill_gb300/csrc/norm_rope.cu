@@ -24,9 +24,14 @@
 // last RM pieces; in the half layout a pair's other half is a shuffle away, or where the halves
 // fill pieces of every lane, in the lane.
 //
-// Measured, against the bytes at the copy rate: 16384 tokens of 32 heads of 192 columns 64.4 us (59.3),
-// 32767 latent rows of 576 13.4 (11.1), the gradient of 4095 x 40 x 128 in float32 45.1 (37.1)
-// and of 8192 x 32 x 256 64.6 (59.3), both with the summing kernel; 8 tokens 2.9, the launch.
+// Measured on inputs that change from call to call, against the bytes at the copy rate: 16384 tokens of 32
+// heads of 192 columns 65.3 us (59.4), 8192 of them in float32 65.2 (59.4), 32767 latent rows of 576 14.4
+// (11.1), in float32 27.4 (22.3), the gradient of 4095 x 40 x 128 in float32 45.1 (37.1) and of 8192 x 32 x
+// 256 65.4 (59.4), both with the summing kernel; 8 tokens 3.2, the launch.  Further off: heads turned whole,
+// whose cos and sin and pieces take more registers than three CTAs leave (8192 x 32 x 256 in bf16, four RoPE pieces
+// a lane, 112 bytes of spills: 74.1 in halves, 70.8 interleaved, 39.6 at the copy rate), the gradient of latent rows, 32
+// lanes a row with a quarter of their pieces off (32767: 35.3 us, 16.7; in float32 49.0, 33.4), and rows that no
+// 16-byte piece fits, element by element (16384 x 32 x 70: 177 us, 21.7; gradient 798, 32.5).
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
 #include "dsa_launch.cuh"

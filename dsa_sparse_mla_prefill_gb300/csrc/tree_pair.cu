@@ -32,10 +32,10 @@
 // Split over the length, join and the rows of absent keys as in paged_decode.cuh; a range of
 // tiles is walked by the pairs of all row blocks at the same time.  A tile takes some 5200 cycles
 // (its MMAs 4352), a range 7000 to its first scores, a request's change some 5000, the join 7 us:
-// 8 x 4096..32768 at 512 rows 94 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
+// 8 x 4096..32768 at 512 rows 97 us of which 67 at the cuBLAS rate, 32 x 512..16384 at 128 rows
 // 58 (27 at the copy rate; 8300 cycles a tile, four slots of K in flight from HBM), 1 x 131072 at
-// 256 rows 62 (38).
-// FP8 rows: 24 x 1024..16384 at 256 rows 117 us (one CTA per 32 rows 283), 12000 cycles a tile
+// 256 rows 63 (38); all on inputs that change from call to call.
+// FP8 rows: 24 x 1024..16384 at 256 rows 121 us (one CTA per 32 rows 283), 12000 cycles a tile
 // for the conversion: see there.
 #include <cfloat>
 
@@ -279,7 +279,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8>::NTHREADS, 1
       //
       // What bounds it: a slot's way from one use to the next, 5000 cycles for 17 uses a tile in
       // seven slots (free 400, asked for 700, landed 1000, converted 2400 beside the other warps,
-      // handed over 800), the load-store pipe at half of its peak.  On 24 x 1024..16384 at 256 rows, 117 us: without the loads it would take 103, without
+      // handed over 800), the load-store pipe at half of its peak.  In that time the warps have
+      // nothing else to do: codes land in the slot itself, so none can be asked for before it is
+      // free.  The 72 registers at launch leave 108 bytes a thread stored to local memory and 404
+      // loaded from it.  On 24 x 1024..16384 at 256 rows, 117 us when these were
+      // measured: without the loads it would take 103, without
       // the arithmetic no less; all by 16-byte copies 122; half or all of the codes through
       // registers, ahead of the free slot, 137 to 160 (a load's data in flight takes room in 28 KB
       // of L1); one warp a slot 170; four warps on every slot in turn 185.
